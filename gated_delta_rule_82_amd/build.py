@@ -87,6 +87,10 @@ def build(verbose: bool = True) -> str:
     # object holding that dk's kernels
     units = [("kda_decode", "kda_decode", [])]
     units += [("kda_prefill", f"kda_prefill_dk{dk}", [f"-DKDA_PREFILL_DK={dk}"]) for dk in (32, 64, 128)]
+    # the decode windows once per form of the gate
+    units += [("kda_window", f"kda_window_{gate}", [f"-DKDA_WINDOW_CHANNEL={i}"])
+              for i, gate in enumerate(("head", "channel"))]
+    units.append(("kda_verify", "kda_verify", []))
     lib_objs = [os.path.join(BUILD, f"{obj}.o") for _, obj, _ in units]
     bench_o = os.path.join(BUILD, "bench_copy.o")
     units.append(("bench_copy", "bench_copy", []))

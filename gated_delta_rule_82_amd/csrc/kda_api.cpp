@@ -73,6 +73,12 @@ int launch_prefill(const DecodeArgs& args, int dk, int dv, bool qkv_bf16, bool s
   }
 }
 
+int launch_window(const WindowArgs& args, int dk, int dv, bool qkv_bf16, bool state_bf16, int state_layout,
+                  bool channel, hipStream_t stream) {
+  return channel ? launch_window_gate<true>(args, dk, dv, qkv_bf16, state_bf16, state_layout, stream)
+                 : launch_window_gate<false>(args, dk, dv, qkv_bf16, state_bf16, state_layout, stream);
+}
+
 }  // namespace kda
 
 extern "C" {
@@ -122,23 +128,31 @@ struct Plan {
   int dk, dv;
   bool qkv_bf16, state_bf16, empty;
   int layout;
+  bool head_gate;   // one decay per (token, value head)
 };
+
+// Which gate tensors a call takes: raw_gate [1, T, HV, dk] with dt_bias
+// [HV, dk] (per channel), or raw_gate [1, T, HV] with dt_bias [HV] (per
+// head); kAny goes by raw_gate's rank.
+enum class Gate { kChannel, kHead, kAny };
 
 int plan_decode(const kda_tensor* out, const kda_tensor* q, const kda_tensor* k,
                 const kda_tensor* v, const kda_tensor* raw_gate,
                 const kda_tensor* beta_logits, const kda_tensor* a_log,
                 const kda_tensor* dt_bias, const kda_tensor* cu_seqlens,
                 const kda_tensor* state_pool, const kda_tensor* state_indices,
-                const kda_mode* mode, Plan* plan, bool qk_f32 = false) {
+                const kda_mode* mode, Plan* plan, bool qk_f32 = false,
+                Gate gate = Gate::kChannel) {
   if (mode == nullptr) return KDA_ERR_NULL;
   KDA_TRY(check_tensor(out, 4));
   KDA_TRY(check_tensor(q, 4));
   KDA_TRY(check_tensor(k, 4));
   KDA_TRY(check_tensor(v, 4));
-  KDA_TRY(check_tensor(raw_gate, 4));
+  const bool head_gate = gate == Gate::kHead || (gate == Gate::kAny && raw_gate != nullptr && raw_gate->ndim == 3);
+  KDA_TRY(check_tensor(raw_gate, head_gate ? 3 : 4));
   KDA_TRY(check_tensor(beta_logits, 3));
   KDA_TRY(check_tensor(a_log, 1));
-  KDA_TRY(check_tensor(dt_bias, 2));
+  KDA_TRY(check_tensor(dt_bias, head_gate ? 1 : 2));
   KDA_TRY(check_tensor(cu_seqlens, 1));
   KDA_TRY(check_tensor(state_pool, 4));
   KDA_TRY(check_tensor(state_indices, 1));
@@ -167,9 +181,10 @@ int plan_decode(const kda_tensor* out, const kda_tensor* q, const kda_tensor* k,
     if (k->shape[i] != q->shape[i] || out->shape[i] != v->shape[i]) return KDA_ERR_SHAPE;
   if (v->shape[1] != T || raw_gate->shape[1] != T || beta_logits->shape[1] != T)
     return KDA_ERR_SHAPE;
-  if (raw_gate->shape[2] != HV || raw_gate->shape[3] != DK) return KDA_ERR_SHAPE;
+  if (raw_gate->shape[2] != HV || (!head_gate && raw_gate->shape[3] != DK)) return KDA_ERR_SHAPE;
   if (beta_logits->shape[2] != HV) return KDA_ERR_SHAPE;
-  if (a_log->shape[0] != HV || dt_bias->shape[0] != HV || dt_bias->shape[1] != DK)
+  if (a_log->shape[0] != HV || dt_bias->shape[0] != HV ||
+      (!head_gate && dt_bias->shape[1] != DK))
     return KDA_ERR_SHAPE;
   if (cu_seqlens->shape[0] - 1 != B) return KDA_ERR_SHAPE;
   if (mode->state_layout != KDA_STATE_K_FIRST && mode->state_layout != KDA_STATE_V_FIRST)
@@ -235,6 +250,7 @@ int plan_decode(const kda_tensor* out, const kda_tensor* q, const kda_tensor* k,
   plan->qkv_bf16 = qkv == KDA_BF16;
   plan->state_bf16 = state_pool->dtype == KDA_BF16;
   plan->layout = mode->state_layout;
+  plan->head_gate = head_gate;
   return KDA_OK;
 }
 
@@ -349,6 +365,179 @@ int kda_prefill(const kda_tensor* out, const kda_tensor* q, const kda_tensor* k,
   if (plan.empty) return KDA_OK;
   return kda::launch_prefill(plan.args, plan.dk, plan.dv, plan.qkv_bf16, plan.state_bf16,
                              plan.layout, matmul, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// The parts of a window call that a decode plan holds; stream `s` gets the
+// plan's tokens.
+kda::WindowArgs window_args(const Plan& plan, int s) {
+  const kda::DecodeArgs& d = plan.args;
+  kda::WindowArgs w{};
+  w.out = d.out;
+  w.src[s].q = d.q;
+  w.src[s].k = d.k;
+  w.src[s].v = d.v;
+  w.src[s].raw_gate = d.raw_gate;
+  w.src[s].beta_logits = d.beta_logits;
+  w.src[s].T = d.T;
+  w.a_log = d.a_log;
+  w.dt_bias = d.dt_bias;
+  w.cu_seqlens = d.cu_seqlens;
+  w.state_pool = d.state_pool;
+  w.state_indices = d.state_indices;
+  w.B = d.B;
+  w.H = d.H;
+  w.HV = d.HV;
+  w.G = d.G;
+  w.N = d.N;
+  w.gate_mode = d.gate_mode;
+  w.lower_bound = d.lower_bound;
+  w.l2_eps = d.l2_eps;
+  w.scale = d.scale;
+  w.window = s;
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+int kda_gdr_decode(const kda_tensor* out, const kda_tensor* q, const kda_tensor* k,
+                   const kda_tensor* v, const kda_tensor* raw_gate,
+                   const kda_tensor* beta_logits, const kda_tensor* a_log,
+                   const kda_tensor* dt_bias, const kda_tensor* cu_seqlens,
+                   const kda_tensor* state_pool, const kda_tensor* state_indices,
+                   const kda_mode* mode, hipStream_t stream) {
+  Plan plan;
+  KDA_TRY(plan_decode(out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens,
+                      state_pool, state_indices, mode, &plan, false, Gate::kHead));
+  if (plan.empty) return KDA_OK;
+  return kda::launch_window(window_args(plan, 0), plan.dk, plan.dv, plan.qkv_bf16, plan.state_bf16,
+                            plan.layout, false, stream);
+}
+
+int kda_gdr_prefill(const kda_tensor* out, const kda_tensor* q, const kda_tensor* k,
+                    const kda_tensor* v, const kda_tensor* raw_gate,
+                    const kda_tensor* beta_logits, const kda_tensor* a_log,
+                    const kda_tensor* dt_bias, const kda_tensor* cu_seqlens,
+                    const kda_tensor* state_pool, const kda_tensor* state_indices,
+                    const kda_mode* mode, hipStream_t stream) {
+  Plan plan;
+  KDA_TRY(plan_decode(out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens,
+                      state_pool, state_indices, mode, &plan, false, Gate::kHead));
+  if (plan.dk < 32 || plan.dv < 32) return KDA_ERR_UNSUPPORTED;
+  if (plan.empty) return KDA_OK;
+  return kda::launch_window(window_args(plan, 0), plan.dk, plan.dv, plan.qkv_bf16, plan.state_bf16,
+                            plan.layout, false, stream);
+}
+
+int kda_decode_window(const kda_tensor* out, const kda_tensor* q, const kda_tensor* k,
+                      const kda_tensor* v, const kda_tensor* raw_gate,
+                      const kda_tensor* beta_logits, const kda_tensor* a_log,
+                      const kda_tensor* dt_bias, const kda_tensor* cu_seqlens,
+                      const kda_tensor* state_pool, const kda_tensor* state_indices,
+                      const kda_replay* replay, const kda_mode* mode, hipStream_t stream) {
+  if (replay == nullptr) return KDA_ERR_NULL;
+  Plan plan;
+  KDA_TRY(plan_decode(out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens,
+                      state_pool, state_indices, mode, &plan, false, Gate::kAny));
+  const kda_tensor* const rk = &replay->k;
+  const kda_tensor* const rv = &replay->v;
+  const kda_tensor* const rg = &replay->raw_gate;
+  const kda_tensor* const rb = &replay->beta_logits;
+  const int gate_rank = plan.head_gate ? 3 : 4;
+  KDA_TRY(check_tensor(rk, 4));
+  KDA_TRY(check_tensor(rv, 4));
+  KDA_TRY(check_tensor(rg, gate_rank));
+  KDA_TRY(check_tensor(rb, 3));
+  KDA_TRY(check_tensor(&replay->begin, 1));
+  KDA_TRY(check_tensor(&replay->count, 1));
+  if (rk->dtype != k->dtype || rv->dtype != v->dtype || rg->dtype != KDA_F32 || rb->dtype != KDA_F32 ||
+      replay->begin.dtype != KDA_I32 || replay->count.dtype != KDA_I32)
+    return KDA_ERR_DTYPE;
+  // the replayed tokens have the window's heads and sizes, and a length of their own
+  const int64_t T = rk->shape[1], B = state_indices->shape[0];
+  if (rv->shape[1] != T || rg->shape[1] != T || rb->shape[1] != T) return KDA_ERR_SHAPE;
+  for (int i = 0; i < 4; ++i) {
+    if (i == 1) continue;
+    if (rk->shape[i] != k->shape[i] || rv->shape[i] != v->shape[i]) return KDA_ERR_SHAPE;
+    if (i < gate_rank && rg->shape[i] != raw_gate->shape[i]) return KDA_ERR_SHAPE;
+    if (i < 3 && rb->shape[i] != beta_logits->shape[i]) return KDA_ERR_SHAPE;
+  }
+  if (replay->begin.shape[0] != B || replay->count.shape[0] != B) return KDA_ERR_SHAPE;
+  if (T > std::numeric_limits<int32_t>::max()) return KDA_ERR_UNSUPPORTED;
+  const kda_tensor* wide[] = {rk, rv, rg, rb};
+  for (const kda_tensor* t : wide)
+    if (!aligned(t, 16)) return KDA_ERR_UNSUPPORTED;
+  if (!aligned(&replay->begin, 4) || !aligned(&replay->count, 4)) return KDA_ERR_UNSUPPORTED;
+  if (B == 0 || (T == 0 && plan.args.T == 0)) return KDA_OK;
+
+  kda::WindowArgs w = window_args(plan, 1);
+  w.src[0].k = rk->data;
+  w.src[0].v = rv->data;
+  w.src[0].raw_gate = static_cast<const float*>(rg->data);
+  w.src[0].beta_logits = static_cast<const float*>(rb->data);
+  w.src[0].T = static_cast<int32_t>(T);
+  w.begin = static_cast<const int32_t*>(replay->begin.data);
+  w.count = static_cast<const int32_t*>(replay->count.data);
+  return kda::launch_window(w, plan.dk, plan.dv, plan.qkv_bf16, plan.state_bf16, plan.layout,
+                            !plan.head_gate, stream);
+}
+
+int kda_verify(const kda_tensor* n_commit, const kda_tensor* next_token, const kda_tensor* target_probs,
+               const kda_tensor* draft_probs, const kda_tensor* tokens, const kda_tensor* u_accept,
+               const kda_tensor* u_sample, const kda_tensor* cu_seqlens, const kda_tensor* workspace,
+               hipStream_t stream) {
+  KDA_TRY(check_tensor(n_commit, 1));
+  KDA_TRY(check_tensor(next_token, 1));
+  KDA_TRY(check_tensor(target_probs, 2));
+  if (draft_probs != nullptr) KDA_TRY(check_tensor(draft_probs, 2));
+  KDA_TRY(check_tensor(tokens, 1));
+  KDA_TRY(check_tensor(u_accept, 1));
+  KDA_TRY(check_tensor(u_sample, 1));
+  KDA_TRY(check_tensor(cu_seqlens, 1));
+  KDA_TRY(check_tensor(workspace, 1));
+  const int32_t dt = target_probs->dtype;
+  if (dt != KDA_F32 && dt != KDA_BF16) return KDA_ERR_DTYPE;
+  if (draft_probs != nullptr && draft_probs->dtype != dt) return KDA_ERR_DTYPE;
+  if (n_commit->dtype != KDA_I32 || next_token->dtype != KDA_I32 || tokens->dtype != KDA_I32 ||
+      cu_seqlens->dtype != KDA_I32 || u_accept->dtype != KDA_F32 || u_sample->dtype != KDA_F32 ||
+      workspace->dtype != KDA_F32)
+    return KDA_ERR_DTYPE;
+  const int64_t B = n_commit->shape[0], T = target_probs->shape[0], V = target_probs->shape[1];
+  if (next_token->shape[0] != B || u_sample->shape[0] != B || cu_seqlens->shape[0] - 1 != B) return KDA_ERR_SHAPE;
+  if (tokens->shape[0] != T || u_accept->shape[0] != T) return KDA_ERR_SHAPE;
+  if (draft_probs != nullptr && (draft_probs->shape[0] != T || draft_probs->shape[1] != V)) return KDA_ERR_SHAPE;
+  if (V < 1) return KDA_ERR_SHAPE;
+  constexpr int64_t kI32 = std::numeric_limits<int32_t>::max();
+  if (T > kI32 || B > kI32 || V > kI32) return KDA_ERR_UNSUPPORTED;
+  // one wave of 64 work-items per segment of 1024 probabilities, at most
+  if (product_exceeds({B, V / KDA_VERIFY_SEGMENT + 5, 64}, kMaxWorkItems)) return KDA_ERR_UNSUPPORTED;
+  if (!aligned(target_probs, 16) || (draft_probs != nullptr && !aligned(draft_probs, 16)) || !aligned(workspace, 16))
+    return KDA_ERR_UNSUPPORTED;
+  const kda_tensor* narrow[] = {n_commit, next_token, tokens, u_accept, u_sample, cu_seqlens};
+  for (const kda_tensor* t : narrow)
+    if (!aligned(t, 4)) return KDA_ERR_UNSUPPORTED;
+  if (workspace->shape[0] < KDA_VERIFY_WORKSPACE(B, V)) return KDA_ERR_SHAPE;
+  if (B == 0) return KDA_OK;
+
+  kda::VerifyArgs a{};
+  a.n_commit = static_cast<int32_t*>(n_commit->data);
+  a.next_token = static_cast<int32_t*>(next_token->data);
+  a.target = target_probs->data;
+  a.draft = draft_probs != nullptr ? draft_probs->data : nullptr;
+  a.tokens = static_cast<const int32_t*>(tokens->data);
+  a.u_accept = static_cast<const float*>(u_accept->data);
+  a.u_sample = static_cast<const float*>(u_sample->data);
+  a.cu_seqlens = static_cast<const int32_t*>(cu_seqlens->data);
+  a.workspace = workspace->data;
+  a.B = static_cast<int32_t>(B);
+  a.T = static_cast<int32_t>(T);
+  a.V = static_cast<int32_t>(V);
+  return kda::launch_verify(a, dt == KDA_BF16, stream);
 }
 
 }  // extern "C"

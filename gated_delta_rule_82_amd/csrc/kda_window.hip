@@ -1,0 +1,550 @@
+// kda_window.hip - decode windows for CDNA4 (gfx950): the gated delta rule
+// with one decay per (token, value head) (kda_gdr_decode), and windows of
+// drafted tokens that leave the state behind (kda_decode_window).
+//
+// Mathematics.  Per token, with alpha = exp(g):
+//   u = v - alpha kh^T S,  o = alpha qh^T S + beta (qh.kh) u,
+//   S' = alpha S + beta kh u^T
+// (the definition with the decay folded into the reads).  The wave keeps its
+// slab as S = D S^ with D the pending decay, so a token's write is one FMA
+// per element, S^ += (beta / D') kh u^T with D' = D alpha; D' is applied to
+// S^ on the last token before the slab is stored and whenever it would drop
+// below 2^-64, which keeps 1 / D' finite.  With one decay per key channel
+// (kda_decode_window on per-channel gates) D is a vector over the keys.
+//
+// Both calls walk the tokens of stream 0, write the state, walk those of
+// stream 1 and drop what they made of it: a plain decode has its tokens in
+// stream 0, a drafted window the previous window's kept tokens (without
+// outputs) there and its own in stream 1.  So a window costs the same one
+// read and one write of the state as a decode step, and a rejected draft
+// never reaches the pool.
+//
+// Work split: one wave owns a 32-value slab of one (request, value head)
+// tile for all dk keys; the value columns never interact, so no wave needs
+// another.  Lanes hold the slab as the state layout streams best: key-first
+// lane (rs, cq) keys rs + RS i and EPL values, value-first lane (rsub, kc)
+// rows rsub + RPI i and EPL keys.
+//
+// Bound: the state's trip from HBM and back.  With one token a wave is almost
+// all state traffic; with windows the two sweeps per token (2 + 1 FMA per
+// element) come into view.
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "kda.h"
+#include "kda_device.h"
+#include "kda_internal.h"
+#include "kda_tile.h"
+
+namespace kda {
+namespace {
+
+constexpr bool kChannel = KDA_WINDOW_CHANNEL;
+constexpr float kDeferFloor = 5.421010862427522e-20f;   // 2^-64
+
+struct Job {
+  int b, hv, h, slab, slot;
+  int t0, t1;          // rows of the stream with outputs
+  int first[2], n[2];  // rows and tokens of each stream
+};
+
+__device__ __forceinline__ int clamp_to(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
+
+template <int SLABS>
+__device__ __forceinline__ Job resolve(const WindowArgs& a) {
+  // XCD-aware id -> (tile, slab): each XCD takes one contiguous range, so
+  // the slabs of a tile meet in one L2
+  const uint32_t wg = blockIdx.x, nwg = gridDim.x;
+  const uint32_t xcd = wg % kXcds, per = nwg / kXcds, extra = nwg % kXcds;
+  const uint32_t logical = xcd * per + (xcd < extra ? xcd : extra) + wg / kXcds;
+  Job j;
+  j.slab = static_cast<int>(logical % SLABS);
+  const int tile = static_cast<int>(logical / SLABS);
+  j.b = tile / a.HV;
+  j.hv = tile - j.b * a.HV;
+  j.h = j.hv / a.G;
+  j.slot = a.state_indices[j.b];
+  const int T = a.src[a.window].T;
+  j.t0 = clamp_to(a.cu_seqlens[j.b], 0, T);
+  j.t1 = clamp_to(a.cu_seqlens[j.b + 1], j.t0, T);
+  j.first[0] = j.first[1] = j.t0;
+  j.n[0] = j.n[1] = j.t1 - j.t0;
+  if (a.window) {
+    j.first[0] = clamp_to(a.begin[j.b], 0, a.src[0].T);
+    j.n[0] = clamp_to(a.count[j.b], 0, a.src[0].T - j.first[0]);
+  } else {
+    j.n[1] = 0;
+  }
+  return j;
+}
+
+// One token's inputs for one lane, in storage form: q, k and (per-channel
+// gates) the gate pre-activation of its CPL setup channels, the NVL v values
+// at v_ch, the beta logit and (per-head gates) the gate pre-activation.
+template <int DK, int DV, bool QBF16, int CPL, int NVL>
+struct TokenIn {
+  RawRun<QBF16, CPL> q, k;
+  RawRun<false, kChannel ? CPL : 1> x;
+  RawRun<QBF16, NVL> v;
+  float bl;
+  // token i of the job's n[0] + n[1] tokens
+  __device__ __forceinline__ void load(const WindowArgs& a, const Job& j, int i, int c0s, int64_t v_ch) {
+    const int s = i >= j.n[0];
+    const TokenStream& src = a.src[s];
+    const int64_t t = j.first[s] + (s ? i - j.n[0] : i);
+    const int64_t qk_off = (t * a.H + j.h) * DK + c0s;
+    k.load(src.k, qk_off);
+    if (src.q != nullptr) q.load(src.q, qk_off);   // uniform; a replay has no q
+    else q.load(src.k, qk_off);
+    const int64_t th = t * a.HV + j.hv;
+    x.load(src.raw_gate, kChannel ? th * DK + c0s : th);
+    v.load(src.v, t * a.HV * DV + v_ch);
+    bl = src.beta_logits[th];
+  }
+};
+
+// What a token's setup leaves for the sweeps (uniform over the wave).
+struct TokenScalars {
+  float beta_qk;   // beta * (qh . kh)
+  float ka, qa;    // factors of the two reductions
+  float w;         // factor of the write
+  float fold;      // decay to apply to the slab first
+  bool folds;
+};
+
+// Norms, gate and beta of one token; fills the tables
+//   per head:    red[c] = {k, q} raw; the norms, decays and beta are scalars
+//   per channel: red[c] = {kh m, qh m}, upd[c] = {D', beta kh w}
+// where (m, w) = (D', 1 / D') while the decay is deferred and (1, 1) when
+// this token folds it into the slab.
+template <int DK, int CPL, typename In>
+__device__ __forceinline__ TokenScalars setup(const WindowArgs& a, const In& in, int c0, bool chan_lane,
+                                              const float (&dtb)[CPL], float amp, float2* red, float2* upd,
+                                              float (&pend)[CPL], bool last) {
+  float qv[CPL], kv[CPL];
+  in.q.unpack(qv);
+  in.k.unpack(kv);
+  float sq = 0.0f, sk = 0.0f, sqk = 0.0f;
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) {
+    qv[c] = chan_lane ? qv[c] : 0.0f;
+    kv[c] = chan_lane ? kv[c] : 0.0f;
+    sq = fmaf(qv[c], qv[c], sq);
+    sk = fmaf(kv[c], kv[c], sk);
+    sqk = fmaf(qv[c], kv[c], sqk);
+  }
+  constexpr int XN = kChannel ? CPL : 1;
+  float x[XN], alpha[XN];
+  in.x.unpack(x);
+  bool small = false;
+#pragma unroll
+  for (int c = 0; c < XN; ++c) {
+    const float z = x[c] + dtb[c];
+    const float g = a.gate_mode == KDA_GATE_SOFTPLUS ? -amp * softplus_f(z) : a.lower_bound * sigmoid_f(amp * z);
+    alpha[c] = exp_f(g) * pend[c];   // D'
+    small |= (!kChannel || chan_lane) && !(alpha[c] >= kDeferFloor);
+  }
+  TokenScalars s;
+  s.folds = last || __any(small);
+  const float beta = sigmoid_f(in.bl);
+  if constexpr (!kChannel) {
+    if (chan_lane) {
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) red[c0 + c] = make_float2(kv[c], qv[c]);
+    }
+  }
+  sq = wave_sum(sq);
+  sk = wave_sum(sk);
+  sqk = wave_sum(sqk);
+  const float rq = a.scale * rsqrt_f(sq + a.l2_eps);
+  const float rk = rsqrt_f(sk + a.l2_eps);
+  s.beta_qk = beta * (sqk * rq * rk);
+  if constexpr (kChannel) {
+    s.ka = s.qa = s.w = s.fold = 1.0f;
+    if (chan_lane) {
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) {
+        const float kh = kv[c] * rk, qh = qv[c] * rq;
+        const float m = s.folds ? 1.0f : alpha[c];
+        const float w = s.folds ? 1.0f : __builtin_amdgcn_rcpf(alpha[c]);
+        red[c0 + c] = make_float2(kh * m, qh * m);
+        upd[c0 + c] = make_float2(alpha[c], beta * kh * w);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) pend[c] = s.folds ? 1.0f : alpha[c];
+  } else {
+    const float m = s.folds ? 1.0f : alpha[0];
+    s.ka = rk * m;
+    s.qa = rq * m;
+    s.w = beta * rk * (s.folds ? 1.0f : __builtin_amdgcn_rcpf(alpha[0]));
+    s.fold = alpha[0];
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) pend[c] = s.folds ? 1.0f : alpha[0];
+  }
+  return s;
+}
+
+// Skipped request: zero its output rows in this slab, leave every slot alone.
+template <int DV, int CW, bool BF16>
+__device__ __forceinline__ void zero_rows(const WindowArgs& a, const Job& j, int lane) {
+  for (int t = j.t0; t < j.t1; ++t)
+    if (lane < CW) store_scalar<BF16>(a.out, (static_cast<int64_t>(t) * a.HV + j.hv) * DV + j.slab * CW + lane, 0.0f);
+}
+
+// The gate's parameters of the lane's setup channels.
+template <int DK, int CPL>
+__device__ __forceinline__ void load_bias(const WindowArgs& a, const Job& j, int c0s, float (&dtb)[CPL]) {
+  if constexpr (kChannel) {
+    load_f32<CPL>(a.dt_bias + static_cast<int64_t>(j.hv) * DK + c0s, dtb);
+  } else {
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) dtb[c] = a.dt_bias[j.hv];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// key-first layout: state [dk][dv]
+// ---------------------------------------------------------------------------
+
+template <int DK, int DV, bool QBF16, bool SBF16>
+__global__ __launch_bounds__(kWave) void window_kfirst(const WindowArgs a) {
+  constexpr int CW = DV < 32 ? DV : 32;   // value columns of the wave's slab
+  constexpr int SLABS = DV / CW;
+  // values per lane and key row: 8 bf16 (16 bytes) where dk has a row for
+  // each of the row groups that leaves, else 4
+  constexpr int EPL = (SBF16 && DK >= kWave * 8 / CW) ? 8 : 4;
+  constexpr int CQ = CW / EPL;            // lanes across the slab's columns
+  constexpr int RS = kWave / CQ;          // row groups across the wave
+  constexpr int R = DK / RS;              // key rows per lane
+  constexpr int NV = 2 * EPL;             // partial sums per lane (k and q)
+  constexpr int LOG_CQ = log2_exact<CQ>();
+  constexpr int LOG_RS = log2_exact<RS>();
+  constexpr int LOG_NV = log2_exact<NV>();
+  constexpr int CPL = DK >= 2 * kWave ? DK / kWave : 1;   // setup channels per lane
+  static_assert(DK % RS == 0 && R >= 1 && LOG_NV <= LOG_RS, "tile shape");
+  static_assert(CPL * kWave >= DK && CPL <= 2, "setup split");
+  // a 32-column bf16 row is half a cache line, which L2 merges with the
+  // neighbouring slab's; whole-line rows stream past the caches
+  using IO = StateIO<SBF16, EPL, (SBF16 && CW * 2 < 128) ? 0 : kCachePolicyNT>;
+
+  __shared__ __attribute__((aligned(16))) float2 red_tab[2][DK];
+  __shared__ __attribute__((aligned(16))) float2 upd_tab[2][kChannel ? DK : 1];
+  __shared__ __attribute__((aligned(16))) float u_tab[CW];
+
+  const int lane = threadIdx.x;
+  const int cq = lane % CQ;
+  const int rs = lane / CQ;
+  const Job j = resolve<SLABS>(a);
+  if (j.slot < 0 || j.slot >= a.N) {
+    zero_rows<DV, CW, QBF16>(a, j, lane);
+    return;
+  }
+  const int total = j.n[0] + j.n[1];
+  if (total == 0) return;
+
+  const int col0 = j.slab * CW + EPL * cq;
+  char* const tile = static_cast<char*>(a.state_pool) +
+                     (static_cast<int64_t>(j.slot) * a.HV + j.hv) * (DK * DV * IO::kElem);
+  const __amdgpu_buffer_rsrc_t res = tile_resource(tile, DK * DV * IO::kElem);
+  const int voff = (rs * DV + col0) * IO::kElem;
+  constexpr int kRowStep = RS * DV * IO::kElem;
+  float S[R][EPL];
+#pragma unroll
+  for (int i = 0; i < R; ++i) IO::load(res, voff, i * kRowStep, S[i]);
+
+  const int c0 = lane * CPL;
+  const bool chan_lane = CPL * kWave == DK || c0 < DK;
+  const int c0s = chan_lane ? c0 : 0;
+  float dtb[CPL];
+  load_bias<DK, CPL>(a, j, c0s, dtb);
+  const float amp = exp_f(a.a_log[j.hv]);
+
+  // After the reduction lane rs holds sum m = rs & (NV - 1): k^T S of column
+  // col0 + m when m < EPL, else q^T S of column col0 + m - EPL.
+  const int m_final = rs & (NV - 1);
+  const bool holds_k = m_final < EPL;
+  const bool owner = rs < NV;
+  const int my_col = col0 + (m_final & (EPL - 1));
+  const int64_t v_ch = static_cast<int64_t>(j.hv) * DV + my_col;
+
+  float pend[CPL];
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) pend[c] = 1.0f;
+  using In = TokenIn<DK, DV, QBF16, CPL, 1>;
+  In nxt;
+  nxt.load(a, j, 0, c0s, v_ch);
+  for (int i = 0; i < total; ++i) {
+    const In cur = nxt;
+    if (i + 1 < total) nxt.load(a, j, i + 1, c0s, v_ch);   // uniform
+    const int buf = i & 1;
+    float v_mine[1];
+    cur.v.unpack(v_mine);
+    const TokenScalars ts = setup<DK, CPL>(a, cur, c0, chan_lane, dtb, amp, red_tab[buf], upd_tab[buf], pend,
+                                           i + 1 == j.n[0]);
+    __syncthreads();
+    if (ts.folds) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float f = kChannel ? upd_tab[buf][rs + RS * r].x : ts.fold;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) S[r][e] *= f;
+      }
+    }
+    float acc[NV];
+#pragma unroll
+    for (int m = 0; m < NV; ++m) acc[m] = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float2 p = red_tab[buf][rs + RS * r];
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) {
+        acc[e] = fmaf(p.x, S[r][e], acc[e]);
+        acc[EPL + e] = fmaf(p.y, S[r][e], acc[EPL + e]);
+      }
+    }
+    transpose_levels<NV / 2, LOG_CQ + LOG_NV - 1>(acc, lane);
+    const float red = sum_levels<LOG_CQ + LOG_RS - 1, LOG_CQ + LOG_NV>(acc[0]) * (holds_k ? ts.ka : ts.qa);
+    if (holds_k && owner) u_tab[EPL * cq + m_final] = v_mine[0] - red;
+    __syncthreads();
+    float u[EPL];
+#pragma unroll
+    for (int e = 0; e < EPL; e += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(&u_tab[EPL * cq + e]);
+      u[e] = x.x;
+      u[e + 1] = x.y;
+      u[e + 2] = x.z;
+      u[e + 3] = x.w;
+    }
+    if (!holds_k && owner && (i >= j.n[0] || !a.window)) {
+      const int64_t t = j.t0 + (a.window ? i - j.n[0] : i);
+      store_scalar<QBF16>(a.out, t * a.HV * DV + v_ch, fmaf(ts.beta_qk, u[m_final & (EPL - 1)], red));
+    }
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) u[e] *= ts.w;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float p = kChannel ? upd_tab[buf][rs + RS * r].y : red_tab[buf][rs + RS * r].x;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) S[r][e] = fmaf(p, u[e], S[r][e]);
+    }
+    if (i + 1 == j.n[0]) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) IO::store(res, voff, r * kRowStep, S[r]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// value-first layout: state [dv][dk]
+// ---------------------------------------------------------------------------
+
+template <int DK, int DV, bool QBF16, bool SBF16>
+__global__ __launch_bounds__(kWave) void window_vfirst(const WindowArgs a) {
+  constexpr int CW = DV < 32 ? DV : 32;   // value rows of the wave's slab
+  constexpr int SLABS = DV / CW;
+  // keys per lane and value row, as in the decode kernel: 8 where the slab
+  // has a row for each of the 512 / dk rows one load instruction covers
+  constexpr int EPL = (kWave * 8 / DK <= CW && (SBF16 || DK >= 64)) ? 8 : 4;
+  constexpr int Q = EPL / 4;
+  constexpr bool ONE_ACCESS = SBF16 && EPL == 8;
+  constexpr int KSTEP = ONE_ACCESS ? 8 : 4;          // keys between neighbouring lanes
+  constexpr int QSTRIDE = ONE_ACCESS ? 4 : DK / 2;   // keys between a lane's groups
+  constexpr int KC = DK / EPL;            // lanes across one row
+  constexpr int RPI = kWave / KC;         // rows per load instruction
+  constexpr int L = CW / RPI;             // rows per lane
+  constexpr int NV = 2 * L;               // partial sums per lane (k and q)
+  constexpr int LOG_KC = log2_exact<KC>();
+  constexpr int LOG_NV = log2_exact<NV>();
+  constexpr int CPL = DK >= 2 * kWave ? DK / kWave : 1;
+  static_assert(L >= 1 && LOG_NV <= LOG_KC, "tile shape");
+  static_assert(CPL * kWave >= DK && CPL <= 2, "setup split");
+  using IO = StateIO<SBF16, ONE_ACCESS ? 8 : 4>;
+
+  __shared__ __attribute__((aligned(16))) float2 red_tab[2][DK];
+  __shared__ __attribute__((aligned(16))) float2 upd_tab[2][kChannel ? DK : 1];
+  __shared__ __attribute__((aligned(16))) float u_tab[CW];   // [RPI][L]
+
+  const int lane = threadIdx.x;
+  const int kc = lane % KC;
+  const int rsub = lane / KC;
+  const Job j = resolve<SLABS>(a);
+  if (j.slot < 0 || j.slot >= a.N) {
+    zero_rows<DV, CW, QBF16>(a, j, lane);
+    return;
+  }
+  const int total = j.n[0] + j.n[1];
+  if (total == 0) return;
+
+  const int row0 = j.slab * CW + rsub;
+  const int key0 = KSTEP * kc;
+  char* const tile = static_cast<char*>(a.state_pool) +
+                     (static_cast<int64_t>(j.slot) * a.HV + j.hv) * (DK * DV * IO::kElem);
+  const __amdgpu_buffer_rsrc_t res = tile_resource(tile, DK * DV * IO::kElem);
+  const int voff = (row0 * DK + key0) * IO::kElem;
+  constexpr int kRowStep = RPI * DK * IO::kElem;
+  constexpr int kGroupStep = QSTRIDE * IO::kElem;
+  float S[L][EPL];
+#pragma unroll
+  for (int l = 0; l < L; ++l) {
+    if constexpr (ONE_ACCESS) {
+      IO::load(res, voff, l * kRowStep, S[l]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) IO::load(res, voff + q * kGroupStep, l * kRowStep, &S[l][4 * q]);
+    }
+  }
+
+  const int c0 = lane * CPL;
+  const bool chan_lane = CPL * kWave == DK || c0 < DK;
+  const int c0s = chan_lane ? c0 : 0;
+  float dtb[CPL];
+  load_bias<DK, CPL>(a, j, c0s, dtb);
+  const float amp = exp_f(a.a_log[j.hv]);
+
+  // After the reduction lane kc holds sum m of its row group: k^T S of row
+  // i = m when m < L, else q^T S of row i = m - L.
+  const int m_final = (kc >> (LOG_KC - LOG_NV)) & (NV - 1);
+  const bool holds_k = m_final < L;
+  const int i_final = m_final & (L - 1);
+  const bool owner = (kc & ((1 << (LOG_KC - LOG_NV)) - 1)) == 0;
+  const int my_row = row0 + RPI * i_final;
+  const int64_t v_ch = static_cast<int64_t>(j.hv) * DV + my_row;
+
+  float pend[CPL];
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) pend[c] = 1.0f;
+  using In = TokenIn<DK, DV, QBF16, CPL, 1>;
+  In nxt;
+  nxt.load(a, j, 0, c0s, v_ch);
+  for (int i = 0; i < total; ++i) {
+    const In cur = nxt;
+    if (i + 1 < total) nxt.load(a, j, i + 1, c0s, v_ch);   // uniform
+    const int buf = i & 1;
+    float v_mine[1];
+    cur.v.unpack(v_mine);
+    const TokenScalars ts = setup<DK, CPL>(a, cur, c0, chan_lane, dtb, amp, red_tab[buf], upd_tab[buf], pend,
+                                           i + 1 == j.n[0]);
+    __syncthreads();
+    if (ts.folds) {
+      float f[EPL];
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) f[e] = kChannel ? upd_tab[buf][key0 + QSTRIDE * (e / 4) + e % 4].x : ts.fold;
+#pragma unroll
+      for (int l = 0; l < L; ++l)
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) S[l][e] *= f[e];
+    }
+    float kq[EPL], qq[EPL];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const float4 r01 = *reinterpret_cast<const float4*>(&red_tab[buf][key0 + QSTRIDE * q]);
+      const float4 r23 = *reinterpret_cast<const float4*>(&red_tab[buf][key0 + QSTRIDE * q + 2]);
+      kq[4 * q] = r01.x;  qq[4 * q] = r01.y;
+      kq[4 * q + 1] = r01.z;  qq[4 * q + 1] = r01.w;
+      kq[4 * q + 2] = r23.x;  qq[4 * q + 2] = r23.y;
+      kq[4 * q + 3] = r23.z;  qq[4 * q + 3] = r23.w;
+    }
+    float vals[NV];
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+      float sa = kq[0] * S[l][0], sb = qq[0] * S[l][0];
+#pragma unroll
+      for (int e = 1; e < EPL; ++e) {
+        sa = fmaf(kq[e], S[l][e], sa);
+        sb = fmaf(qq[e], S[l][e], sb);
+      }
+      vals[l] = sa;
+      vals[L + l] = sb;
+    }
+    transpose_levels<NV / 2, LOG_KC - 1>(vals, lane);
+    const float red = sum_levels<LOG_KC - LOG_NV - 1, 0>(vals[0]) * (holds_k ? ts.ka : ts.qa);
+    if (holds_k && owner) u_tab[rsub * L + i_final] = v_mine[0] - red;
+    __syncthreads();
+    if (!holds_k && owner && (i >= j.n[0] || !a.window)) {
+      const int64_t t = j.t0 + (a.window ? i - j.n[0] : i);
+      store_scalar<QBF16>(a.out, t * a.HV * DV + v_ch, fmaf(ts.beta_qk, u_tab[rsub * L + i_final], red));
+    }
+    float wk[EPL];
+#pragma unroll
+    for (int e = 0; e < EPL; ++e)
+      wk[e] = kChannel ? upd_tab[buf][key0 + QSTRIDE * (e / 4) + e % 4].y : kq[e] * ts.w;
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+      const float u = u_tab[rsub * L + l];
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) S[l][e] = fmaf(wk[e], u, S[l][e]);
+    }
+    if (i + 1 == j.n[0]) {
+#pragma unroll
+      for (int l = 0; l < L; ++l) {
+        if constexpr (ONE_ACCESS) {
+          IO::store(res, voff, l * kRowStep, S[l]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < Q; ++q) IO::store(res, voff + q * kGroupStep, l * kRowStep, &S[l][4 * q]);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dispatch
+// ---------------------------------------------------------------------------
+
+template <int DK, int DV, bool QBF16, bool SBF16, int LAYOUT>
+hipError_t launch_one(const WindowArgs& args, hipStream_t stream) {
+  constexpr int CW = DV < 32 ? DV : 32;
+  const int64_t nwg = static_cast<int64_t>(args.B) * args.HV * (DV / CW);
+  void* kargs[] = {const_cast<WindowArgs*>(&args)};
+  const void* fn = LAYOUT == KDA_STATE_K_FIRST ? reinterpret_cast<const void*>(&window_kfirst<DK, DV, QBF16, SBF16>)
+                                               : reinterpret_cast<const void*>(&window_vfirst<DK, DV, QBF16, SBF16>);
+  return hipLaunchKernel(fn, dim3(static_cast<uint32_t>(nwg)), dim3(kWave), kargs, 0, stream);
+}
+
+using LaunchFn = hipError_t (*)(const WindowArgs&, hipStream_t);
+
+template <int DK, int DV, bool QBF16, bool SBF16>
+LaunchFn pick_layout(int layout) {
+  return layout == KDA_STATE_V_FIRST ? &launch_one<DK, DV, QBF16, SBF16, KDA_STATE_V_FIRST>
+                                     : &launch_one<DK, DV, QBF16, SBF16, KDA_STATE_K_FIRST>;
+}
+
+template <int DK, int DV>
+LaunchFn pick(bool qbf16, bool sbf16, int layout) {
+  if (qbf16) return sbf16 ? pick_layout<DK, DV, true, true>(layout) : pick_layout<DK, DV, true, false>(layout);
+  return sbf16 ? pick_layout<DK, DV, false, true>(layout) : pick_layout<DK, DV, false, false>(layout);
+}
+
+template <int DK>
+LaunchFn pick_dv(int dv, bool qbf16, bool sbf16, int layout) {
+  switch (dv) {
+    case 16: return pick<DK, 16>(qbf16, sbf16, layout);
+    case 32: return pick<DK, 32>(qbf16, sbf16, layout);
+    case 64: return pick<DK, 64>(qbf16, sbf16, layout);
+    case 128: return pick<DK, 128>(qbf16, sbf16, layout);
+    default: return nullptr;
+  }
+}
+
+}  // namespace
+
+template <>
+int launch_window_gate<kChannel>(const WindowArgs& args, int dk, int dv, bool qkv_bf16, bool state_bf16,
+                                 int state_layout, hipStream_t stream) {
+  LaunchFn fn = nullptr;
+  switch (dk) {
+    case 16: fn = pick_dv<16>(dv, qkv_bf16, state_bf16, state_layout); break;
+    case 32: fn = pick_dv<32>(dv, qkv_bf16, state_bf16, state_layout); break;
+    case 64: fn = pick_dv<64>(dv, qkv_bf16, state_bf16, state_layout); break;
+    case 128: fn = pick_dv<128>(dv, qkv_bf16, state_bf16, state_layout); break;
+    default: break;
+  }
+  if (fn == nullptr) return KDA_ERR_UNSUPPORTED;
+  return fn(args, stream) == hipSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+}
+
+}  // namespace kda

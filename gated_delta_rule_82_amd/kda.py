@@ -40,10 +40,14 @@ KDA_MATMUL_SPLIT_BF16 = 0
 KDA_MATMUL_F32 = 1
 MATMULS = {"split_bf16": KDA_MATMUL_SPLIT_BF16, "f32": KDA_MATMUL_F32}
 
-EXPORTED_SYMBOLS = ("kda_decode", "kda_decode_conv", "kda_prefill", "kda_check_host",
+KDA_VERIFY_SEGMENT = 1024
+
+EXPORTED_SYMBOLS = ("kda_decode", "kda_decode_conv", "kda_prefill", "kda_gdr_decode",
+                    "kda_gdr_prefill", "kda_decode_window", "kda_verify", "kda_check_host",
                     "kda_status_string", "kda_abi_version")
 CONV_FIELDS = ("x_q", "x_k", "x_v", "w_q", "w_k", "w_v", "win_q", "win_k", "win_v", "q_conv",
                "k_conv")
+REPLAY_FIELDS = ("k", "v", "raw_gate", "beta_logits", "begin", "count")
 
 
 class KdaTensor(ctypes.Structure):
@@ -53,6 +57,10 @@ class KdaTensor(ctypes.Structure):
 
 class KdaConv(ctypes.Structure):
     _fields_ = [(n, KdaTensor) for n in CONV_FIELDS]
+
+
+class KdaReplay(ctypes.Structure):
+    _fields_ = [(n, KdaTensor) for n in REPLAY_FIELDS]
 
 
 class KdaMode(ctypes.Structure):
@@ -97,6 +105,14 @@ def library() -> ctypes.CDLL:
     lib.kda_prefill.argtypes = [P] * 11 + [ctypes.POINTER(KdaMode), ctypes.c_int32,
                                             ctypes.c_void_p]
     lib.kda_prefill.restype = ctypes.c_int
+    for fn in (lib.kda_gdr_decode, lib.kda_gdr_prefill):
+        fn.argtypes = [P] * 11 + [ctypes.POINTER(KdaMode), ctypes.c_void_p]
+        fn.restype = ctypes.c_int
+    lib.kda_decode_window.argtypes = [P] * 11 + [ctypes.POINTER(KdaReplay),
+                                                 ctypes.POINTER(KdaMode), ctypes.c_void_p]
+    lib.kda_decode_window.restype = ctypes.c_int
+    lib.kda_verify.argtypes = [P] * 9 + [ctypes.c_void_p]
+    lib.kda_verify.restype = ctypes.c_int
     lib.kda_check_host.argtypes = [ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32),
                                    ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]
     lib.kda_check_host.restype = ctypes.c_int
@@ -158,6 +174,30 @@ def call_raw_conv(out, conv, rest, mode: KdaMode, stream: int = 0) -> int:
     ref = lambda t: ctypes.byref(t) if t is not None else None  # noqa: E731
     return lib.kda_decode_conv(ref(out), ref(conv), *[ref(t) for t in rest], ref(mode),
                                ctypes.c_void_p(stream))
+
+
+def call_raw_gdr(tensors, mode: KdaMode, prefill: bool = False, stream: int = 0) -> int:
+    """Call kda_gdr_decode (or kda_gdr_prefill) on 11 prepared descriptors
+    (None passes NULL); returns the status code without raising."""
+    lib = library()
+    ref = lambda t: ctypes.byref(t) if t is not None else None  # noqa: E731
+    fn = lib.kda_gdr_prefill if prefill else lib.kda_gdr_decode
+    return fn(*[ref(t) for t in tensors], ref(mode), ctypes.c_void_p(stream))
+
+
+def call_raw_window(tensors, replay, mode: KdaMode, stream: int = 0) -> int:
+    """Call kda_decode_window on 11 prepared descriptors and a KdaReplay (None
+    passes NULL); returns the status code without raising."""
+    ref = lambda t: ctypes.byref(t) if t is not None else None  # noqa: E731
+    return library().kda_decode_window(*[ref(t) for t in tensors], ref(replay), ref(mode),
+                                       ctypes.c_void_p(stream))
+
+
+def call_raw_verify(tensors, stream: int = 0) -> int:
+    """Call kda_verify on 9 prepared descriptors (None passes NULL); returns
+    the status code without raising."""
+    ref = lambda t: ctypes.byref(t) if t is not None else None  # noqa: E731
+    return library().kda_verify(*[ref(t) for t in tensors], ctypes.c_void_p(stream))
 
 
 def _descriptor(t, name):
@@ -275,3 +315,114 @@ def decode_conv(out, x_q, x_k, x_v, w_q, w_k, w_v, win_q, win_k, win_v, q_conv, 
         rc = call_raw_conv(out_d, conv, rest, mode, stream)
     if rc != KDA_OK:
         raise KdaError(rc, "kda_decode_conv")
+
+
+def _check_device(named, dev):
+    for n, t in named:
+        if t.device != dev:
+            raise ValueError(f"{n}: on {t.device}, expected {dev}")
+
+
+def _gdr(prefill, tensors, mode, stream, where):
+    import torch
+    descs = [_descriptor(t, n) for t, n in zip(tensors, ARG_NAMES)]
+    dev = tensors[1].device
+    _check_device(zip(ARG_NAMES, tensors), dev)
+    with torch.cuda.device(dev):
+        if stream is None:
+            stream = torch.cuda.current_stream(dev).cuda_stream
+        rc = call_raw_gdr(descs, mode, prefill, stream)
+    if rc != KDA_OK:
+        raise KdaError(rc, where)
+
+
+def gdr_decode(out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool,
+               state_indices, *, gate_mode="softplus", lower_bound=0.0, l2_eps=0.0, scale=0.0,
+               state_layout="k_first", stream: Optional[int] = None) -> None:
+    """The gated delta rule with one decay per (token, value head)
+    (kda_gdr_decode in include/kda.h): as :func:`decode`, with raw_gate
+    [1, T, HV] and dt_bias [HV]."""
+    _gdr(False, (out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool,
+                 state_indices),
+         make_mode(gate_mode, lower_bound, l2_eps, scale, state_layout), stream, "kda_gdr_decode")
+
+
+def gdr_prefill(out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool,
+                state_indices, *, gate_mode="softplus", lower_bound=0.0, l2_eps=0.0, scale=0.0,
+                state_layout="k_first", stream: Optional[int] = None) -> None:
+    """:func:`gdr_decode` for whole prompts (kda_gdr_prefill in
+    include/kda.h): same tensors and result."""
+    _gdr(True, (out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool,
+                state_indices),
+         make_mode(gate_mode, lower_bound, l2_eps, scale, state_layout), stream, "kda_gdr_prefill")
+
+
+def decode_window(out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool,
+                  state_indices, replay_k, replay_v, replay_gate, replay_beta, replay_begin,
+                  replay_count, *, gate_mode="softplus", lower_bound=0.0, l2_eps=0.0, scale=0.0,
+                  state_layout="k_first", stream: Optional[int] = None) -> None:
+    """A window of drafted tokens (kda_decode_window in include/kda.h): the
+    state of request b first advances by rows replay_begin[b] ..
+    + replay_count[b] of the replay tensors and is written; then the window
+    runs from there, with outputs, and leaves the pool alone.  raw_gate is
+    [1, T, HV, dk] with dt_bias [HV, dk], or [1, T, HV] with dt_bias [HV].
+
+    A serving loop passes the previous call's k, v, raw_gate and beta_logits
+    with its ``cu_seqlens[:-1]`` and the ``n_commit`` of :func:`verify`."""
+    import torch
+    tensors = (out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool,
+               state_indices)
+    replay_t = (replay_k, replay_v, replay_gate, replay_beta, replay_begin, replay_count)
+    names = [f"replay {n}" for n in REPLAY_FIELDS]
+    descs = [_descriptor(t, n) for t, n in zip(tensors, ARG_NAMES)]
+    replay = KdaReplay(*[_descriptor(t, n) for t, n in zip(replay_t, names)])
+    dev = q.device
+    _check_device(zip(ARG_NAMES, tensors), dev)
+    _check_device(zip(names, replay_t), dev)
+    mode = make_mode(gate_mode, lower_bound, l2_eps, scale, state_layout)
+    with torch.cuda.device(dev):
+        if stream is None:
+            stream = torch.cuda.current_stream(dev).cuda_stream
+        rc = call_raw_window(descs, replay, mode, stream)
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_decode_window")
+
+
+VERIFY_NAMES = ("n_commit", "next_token", "target_probs", "draft_probs", "tokens", "u_accept",
+                "u_sample", "cu_seqlens", "workspace")
+
+
+def verify_workspace(B: int, V: int) -> int:
+    """Floats of :func:`verify`'s workspace for B requests over V tokens."""
+    return 2 * B * (V // KDA_VERIFY_SEGMENT + 2)
+
+
+def verify(n_commit, next_token, target_probs, draft_probs, tokens, u_accept, u_sample, cu_seqlens,
+           *, workspace=None, stream: Optional[int] = None) -> None:
+    """Which drafted tokens of each request's window stand, and the token that
+    follows them (kda_verify in include/kda.h): n_commit [B] and next_token
+    [B] (int32) are written.  target_probs and draft_probs are [T, V]; None
+    for draft_probs: the drafts were certain.  ``workspace`` (float32, at
+    least ``verify_workspace(B, V)`` values) is taken from torch's allocator
+    if not given; with ``stream`` given it has to be too, since that memory
+    belongs to torch's current stream."""
+    import torch
+    if workspace is None:
+        if stream is not None:
+            raise ValueError("workspace: required with an explicit stream")
+        if not isinstance(target_probs, torch.Tensor) or target_probs.dim() != 2:
+            raise ValueError("target_probs: expected a [T, V] tensor")
+        workspace = torch.empty(max(1, verify_workspace(n_commit.numel(), target_probs.shape[1])),
+                                dtype=torch.float32, device=target_probs.device)
+    tensors = (n_commit, next_token, target_probs, draft_probs, tokens, u_accept, u_sample,
+               cu_seqlens, workspace)
+    descs = [None if n == "draft_probs" and t is None else _descriptor(t, n)
+             for t, n in zip(tensors, VERIFY_NAMES)]
+    dev = target_probs.device
+    _check_device([(n, t) for n, t in zip(VERIFY_NAMES, tensors) if t is not None], dev)
+    with torch.cuda.device(dev):
+        if stream is None:
+            stream = torch.cuda.current_stream(dev).cuda_stream
+        rc = call_raw_verify(descs, stream)
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_verify")

@@ -240,6 +240,129 @@ int kda_prefill(const kda_tensor* out, const kda_tensor* q, const kda_tensor* k,
                 const kda_mode* mode, int32_t matmul, hipStream_t stream);
 
 /*
+ * kda_gdr_decode - the gated delta rule with one decay per (token, value
+ * head): kda_decode's operation with
+ *     x = raw_gate[t,hv] + dt_bias[hv]        (one value, not one per channel)
+ *     S *= exp(g);  u = v[t,hv] - kh^T S;  S += beta * kh u^T
+ *     out[t,hv] = qh^T S
+ * Arguments, preconditions, conventions and errors are those of kda_decode,
+ * but for
+ *   raw_gate      [1, T, HV]      f32, gate pre-activation before dt_bias.
+ *   dt_bias       [HV]            f32.
+ */
+int kda_gdr_decode(const kda_tensor* out, const kda_tensor* q, const kda_tensor* k,
+                   const kda_tensor* v, const kda_tensor* raw_gate,
+                   const kda_tensor* beta_logits, const kda_tensor* a_log,
+                   const kda_tensor* dt_bias, const kda_tensor* cu_seqlens,
+                   const kda_tensor* state_pool, const kda_tensor* state_indices,
+                   const kda_mode* mode, hipStream_t stream);
+
+/*
+ * kda_gdr_prefill - kda_gdr_decode's operation and arguments for whole
+ * prompts.  dk and dv must each be 32, 64 or 128 (else
+ * KDA_ERR_UNSUPPORTED).
+ */
+int kda_gdr_prefill(const kda_tensor* out, const kda_tensor* q, const kda_tensor* k,
+                    const kda_tensor* v, const kda_tensor* raw_gate,
+                    const kda_tensor* beta_logits, const kda_tensor* a_log,
+                    const kda_tensor* dt_bias, const kda_tensor* cu_seqlens,
+                    const kda_tensor* state_pool, const kda_tensor* state_indices,
+                    const kda_mode* mode, hipStream_t stream);
+
+/*
+ * The tokens of an earlier window that stand, for kda_decode_window: rows
+ * begin[b] .. begin[b] + count[b] - 1 of k, v, raw_gate and beta_logits are
+ * request b's.  These are the tensors of the call that ran the earlier
+ * window, with begin its cu_seqlens (without the last entry; in the new
+ * batch's order) and count the n_commit of kda_verify.  Tr is the tensors'
+ * own token count.  A request that joins has count 0.
+ */
+typedef struct kda_replay {
+  kda_tensor k;           /* [1, Tr, H, dk]   dtype of k                     */
+  kda_tensor v;           /* [1, Tr, HV, dv]  dtype of v                     */
+  kda_tensor raw_gate;    /* [1, Tr, HV, dk] or [1, Tr, HV] f32, as raw_gate */
+  kda_tensor beta_logits; /* [1, Tr, HV]      f32                            */
+  kda_tensor begin;       /* [B]  i32, device resident                       */
+  kda_tensor count;       /* [B]  i32, device resident                       */
+} kda_replay;
+
+/*
+ * kda_decode_window - a window of drafted tokens.  kda_decode and
+ * kda_gdr_decode leave the state as it is after ALL tokens of a request,
+ * so a draft that is rejected later would stay in it.  This call first
+ * advances the state of request b by its replayed tokens (no output) and
+ * writes it to its slot; then it runs the request's window from there, with
+ * outputs, and leaves the slot as the replay left it.  After verification
+ * the next call replays what stands.  The state makes one trip from HBM and
+ * one back, as in a decode step.
+ *
+ * Arguments are those of kda_decode (one decay per channel: raw_gate
+ * [1, T, HV, dk], dt_bias [HV, dk]) or of kda_gdr_decode (one per head:
+ * raw_gate [1, T, HV], dt_bias [HV]); raw_gate's rank says which.
+ * Between replay and window the state stays in fp32 also where the pool is
+ * bf16; only what is written is rounded.
+ * Conventions: a request with a negative index is skipped, replay and all;
+ * one without replayed tokens leaves its slot untouched; one without a
+ * window is only replayed.  The kernel clamps begin to [0, Tr] and count to
+ * the rows that follow, so bad values never make it access memory outside
+ * the tensors.  `replay` is required (KDA_ERR_NULL); begin and count need
+ * 4-byte alignment.  Preconditions and errors are otherwise kda_decode's.
+ */
+int kda_decode_window(const kda_tensor* out, const kda_tensor* q, const kda_tensor* k,
+                      const kda_tensor* v, const kda_tensor* raw_gate,
+                      const kda_tensor* beta_logits, const kda_tensor* a_log,
+                      const kda_tensor* dt_bias, const kda_tensor* cu_seqlens,
+                      const kda_tensor* state_pool, const kda_tensor* state_indices,
+                      const kda_replay* replay, const kda_mode* mode, hipStream_t stream);
+
+/* Floats of kda_verify's workspace for B requests over V tokens. */
+#define KDA_VERIFY_SEGMENT 1024
+#define KDA_VERIFY_WORKSPACE(B, V) (2 * (int64_t)(B) * ((int64_t)(V) / KDA_VERIFY_SEGMENT + 2))
+
+/*
+ * kda_verify - which drafted tokens of a window stand, and what follows them
+ * (speculative sampling: the tokens that come out are distributed as the
+ * target's).  Row t of target_probs is the target's distribution of the
+ * token after window token t, row t of draft_probs the one that token was
+ * drafted from.  Request b's window is rows r = cu_seqlens[b] ..
+ * cu_seqlens[b+1] - 1; its first token is known, the others are drafts.
+ * The draft tokens[t+1] stands while all before it do and
+ *     u_accept[t] * draft_probs[t][x] < target_probs[t][x],  x = tokens[t+1]
+ * (compared exactly).  With a drafts standing, n_commit[b] = a + 1 tokens of
+ * the window are final, and with s = cu_seqlens[b] + a
+ *     next_token[b] = min{ v : sum_{w<=v} r[w] > u_sample[b] * sum_w r[w] },
+ *     r = max(target_probs[s] - draft_probs[s], 0)   where a draft fell,
+ *     r = target_probs[s]                            where none did,
+ * the sums in fp64.  A request without tokens gets n_commit 0 and next_token
+ * -1; so does next_token where r has no mass.
+ *
+ * Arguments (B requests, T packed window tokens, V vocabulary):
+ *   n_commit, next_token [B]   i32, written.
+ *   target_probs  [T, V]       f32 or bf16.  Need not sum to one.
+ *   draft_probs   [T, V]       dtype of target_probs; rows of last window
+ *                              tokens are not read.  NULL: the drafts were
+ *                              certain (probability one each), as a lookup
+ *                              makes them.
+ *   tokens        [T]          i32; a draft outside [0, V) falls.
+ *   u_accept      [T]          f32 in [0, 1); those of last window tokens
+ *                              are not read.  A NaN rejects.
+ *   u_sample      [B]          f32 in [0, 1).  Below 0 or NaN counts as 0;
+ *                              1 or more gives the last token with mass.
+ *   cu_seqlens    [B + 1]      i32, device resident, as for kda_decode.
+ *   workspace     [>= KDA_VERIFY_WORKSPACE(B, V)]  f32; its contents before
+ *                              and after mean nothing.  Calls that may run
+ *                              at the same time need one each.
+ * Probabilities that are NaN, negative or infinite count as zero.  Two
+ * kernels are enqueued on `stream`.  target_probs, draft_probs and workspace
+ * need 16-byte alignment, the others 4 (KDA_ERR_UNSUPPORTED), as T, B and V
+ * must stay below 2^31 and B * (V / 1024 + 5) below 2^26.
+ */
+int kda_verify(const kda_tensor* n_commit, const kda_tensor* next_token, const kda_tensor* target_probs,
+               const kda_tensor* draft_probs, const kda_tensor* tokens, const kda_tensor* u_accept,
+               const kda_tensor* u_sample, const kda_tensor* cu_seqlens, const kda_tensor* workspace,
+               hipStream_t stream);
+
+/*
  * kda_check_host - validate host copies of the decode metadata.  This is a
  * convention of this library, not an operation of the pages: it checks the
  * preconditions of the "KdaDecode" tensor contract (cu_seqlens varlen
