@@ -33,11 +33,12 @@ HIP_FLAGS = [
 ]
 
 
-# Per-file additions.  The prefill kernel keeps its MFMA accumulators (the
-# state slab and the chunk products) in the architectural VGPRs: its
+# Per-file additions.  The prefill kernels keep their MFMA accumulators (the
+# state slab and the chunk products) in the architectural VGPRs: their
 # elementwise work reads and scales them every chunk, and with accumulators
 # in AGPRs every such access costs a copy (measured 5-8% faster this way).
-EXTRA_FLAGS = {"kda_prefill": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+EXTRA_FLAGS = {"kda_prefill": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               "kda_gdr_prefill": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _hipcc() -> str:
@@ -91,6 +92,7 @@ def build(verbose: bool = True) -> str:
     units += [("kda_window", f"kda_window_{gate}", [f"-DKDA_WINDOW_CHANNEL={i}"])
               for i, gate in enumerate(("head", "channel"))]
     units.append(("kda_verify", "kda_verify", []))
+    units.append(("kda_gdr_prefill", "kda_gdr_prefill", []))
     lib_objs = [os.path.join(BUILD, f"{obj}.o") for _, obj, _ in units]
     bench_o = os.path.join(BUILD, "bench_copy.o")
     units.append(("bench_copy", "bench_copy", []))

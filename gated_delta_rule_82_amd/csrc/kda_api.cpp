@@ -429,9 +429,14 @@ int kda_gdr_prefill(const kda_tensor* out, const kda_tensor* q, const kda_tensor
   KDA_TRY(plan_decode(out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens,
                       state_pool, state_indices, mode, &plan, false, Gate::kHead));
   if (plan.dk < 32 || plan.dv < 32) return KDA_ERR_UNSUPPORTED;
+  // 512 work-items per (request, value head) where there are many
+  if (product_exceeds({plan.args.B, plan.args.HV, 512}, kMaxWorkItems)) return KDA_ERR_UNSUPPORTED;
   if (plan.empty) return KDA_OK;
-  return kda::launch_window(window_args(plan, 0), plan.dk, plan.dv, plan.qkv_bf16, plan.state_bf16,
-                            plan.layout, false, stream);
+  if (plan.dk == 128 && !plan.qkv_bf16)
+    return kda::launch_window(window_args(plan, 0), plan.dk, plan.dv, plan.qkv_bf16, plan.state_bf16,
+                              plan.layout, false, stream);
+  return kda::launch_gdr_prefill(plan.args, plan.dk, plan.dv, plan.qkv_bf16, plan.state_bf16, plan.layout,
+                                 stream);
 }
 
 int kda_decode_window(const kda_tensor* out, const kda_tensor* q, const kda_tensor* k,
