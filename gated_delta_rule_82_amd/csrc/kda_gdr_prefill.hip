@@ -34,12 +34,12 @@
 // with 16 * NCS columns, all keys in registers, and no exchange with other
 // waves.  What does not depend on the state is made ahead by four helper
 // waves, each a chunk further on:
-//   wave 0  K: fp16 rows in operand order (K for K S0 and the Gram
-//           products, K^T for the state update), norms      chunk c + 3
-//   wave 1  Q: the same, and the gates (g, G, beta)           chunk c + 3
-//   wave 2  the Gram products: A, P, the factor tables        chunk c + 2
-//   wave 3  T: two 16 x 16 triangular inverses and their join chunk c + 1
-//   others  the state chain                                   chunk c
+//   0  K: fp16 rows in operand order (K for K S0 and the Gram
+//      products, K^T for the state update), norms      chunk c + 3
+//   1  Q: the same without K^T                         chunk c + 3
+//   2  the Gram products: A, P, the factor tables      chunk c + 2
+//   3  the gates (g, G, beta)                          chunk c + 3
+//      T: two 16 x 16 triangular inverses, joined      chunk c + 1
 // with one barrier per chunk.  The accumulator layout of one product (four
 // consecutive rows per lane) is the operand layout of the next once the
 // operands' order of k is permuted to match, so the chain never leaves its
@@ -141,54 +141,70 @@ struct Shared {
   float last[kRing];                               // e^(G_last)
 };
 
+// The same for K^T, whose writers hold 8 neighbouring channels.
+__device__ __forceinline__ int kt_slot(int g, int channel) { return g * 16 + (channel ^ ((channel >> 3) & 1)); }
+
 // ---------------------------------------------------------------------------
-// helper waves 0 and 1: rows of k or q
+// the rows of k or q
 // ---------------------------------------------------------------------------
 
-// A lane holds a pair of channels of TL = 8 NG tokens: dk / 2 lanes cover a
-// token, 128 / dk lane groups share the chunk's tokens, each with NG of the
-// four operand groups g.  Token i of group gi is 4 g + i % 4 + 16 (i / 4).
+// A window of rows of a packed tensor: rows of `row` bytes every `stride`
+// bytes, `n` of them (n >= 1).  Loads past the last row give zero and stores
+// are dropped by the hardware's range check, so a chunk's tail needs no masks;
+// all offsets are in the vector offset, which the check covers.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_resource(const void* base, int64_t offset, int n, int stride,
+                                                                int row) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(base)) + offset,
+                                           static_cast<short>(0), ((n < kC ? n : kC) - 1) * stride + row,
+                                           kRawBufferWord3);
+}
+
+// A lane holds 8 channels of TL tokens: dk / 8 lanes cover a token, and lane
+// group q of them has operand positions P = q TL .. q TL + TL - 1, where
+// position P = 8 g + p is token 4 g + p % 4 + 16 (p / 4).
 template <int DK, bool F32>
 struct RowLoader {
-  static constexpr int LANES = DK / 2;
-  static constexpr int SPLIT = kWave / LANES;
-  static constexpr int NG = 4 / SPLIT;
-  static constexpr int TL = 8 * NG;
-  uint32_t w[TL * (F32 ? 2 : 1)];
+  static constexpr int LANES = DK / 8;
+  static constexpr int TL = DK / 16;
+  static constexpr int WORDS = F32 ? 2 : 1;
+  u32x4 w[TL][WORDS];
 
-  static __device__ __forceinline__ int token(int lane, int i) {
-    const int g = (lane / LANES) * NG + i / 8;
-    return 4 * g + i % 4 + 16 * ((i / 4) % 2);
+  static __device__ __forceinline__ int position(int lane) { return (lane / LANES) * TL; }
+  static __device__ __forceinline__ int token(int lane) {   // of the lane's first position
+    const int P = position(lane);
+    return 4 * (P / 8) + P % 4 + 16 * ((P / 4) % 2);
   }
+  static constexpr __device__ int step(int i) { return i % 4 + 16 * (i / 4); }   // token i's distance from it
 
-  // rows t0 .. t0 + n - 1 of head h (n >= 1); rows past them are zero
-  __device__ __forceinline__ void load(const void* base, int64_t t0, int n, int H, int h, int lane) {
-    const int c = 2 * (lane % LANES);
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int voff, int stride) {
 #pragma unroll
-    for (int i = 0; i < TL; ++i) {
-      const int t = token(lane, i);
-      const int64_t off = ((t0 + (t < n ? t : 0)) * H + h) * DK + c;
-      if constexpr (F32) {
-        const u32x2 x = *reinterpret_cast<const u32x2*>(static_cast<const float*>(base) + off);
-        w[2 * i] = t < n ? x.x : 0u;
-        w[2 * i + 1] = t < n ? x.y : 0u;
-      } else {
-        const uint32_t x = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(base) + off);
-        w[i] = t < n ? x : 0u;
-      }
-    }
+    for (int i = 0; i < TL; ++i)
+#pragma unroll
+      for (int x = 0; x < WORDS; ++x)
+        w[i][x] = __builtin_amdgcn_raw_buffer_load_b128(r, voff + step(i) * stride + 16 * x, 0, 0);
   }
 
-  __device__ __forceinline__ void unpack(int i, float& x, float& y) const {
-    if constexpr (F32) {
-      x = __uint_as_float(w[2 * i]);
-      y = __uint_as_float(w[2 * i + 1]);
-    } else {
-      x = bf16_to_f32(w[i] & 0xffffu);
-      y = __uint_as_float(w[i] & 0xffff0000u);
+  __device__ __forceinline__ void unpack(int i, float (&x)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (F32) x[e] = __uint_as_float(w[i][e / 4][e % 4]);
+      else x[e] = e % 2 ? __uint_as_float(w[i][0][e / 2] & 0xffff0000u) : __uint_as_float(w[i][0][e / 2] << 16);
     }
   }
 };
+
+// Sum over the LANES lanes of a group, to all of them.
+template <int LANES>
+__device__ __forceinline__ float group_sum(float x) {
+  x += dpp<kDppXor1>(x);
+  x += dpp<kDppXor2>(x);
+  if constexpr (LANES == 8) x += dpp<kDppHalfMirror>(x);   // quads are uniform by now
+  if constexpr (LANES == 16) {
+    x += dpp<kDppRowRor4>(x);
+    x += dpp<kDppRowRor8>(x);
+  }
+  return x;
+}
 
 // Converts a chunk's rows: fp16 rows in operand order, their factors
 // (norm[token] * stored row = unit row), and for k the transposed operand.
@@ -198,64 +214,60 @@ __device__ __forceinline__ void convert_rows(const RowLoader<DK, F32>& in, float
                                              float* norm) {
   using L = RowLoader<DK, F32>;
   constexpr int TL = L::TL;
-  constexpr int LOG_LANES = log2_exact<L::LANES>();
-  constexpr int LOG_TL = log2_exact<TL>();
-  static_assert(LOG_LANES == LOG_TL + 1, "one level of plain sums");
-  float sq[TL];
+  const int c = 8 * (lane % L::LANES);
+  const int s = c / 32, half = (c % 32) / 16, g = (c % 16) / 4;   // the lane's channels: operand groups g, g + 1
+  const int first = L::token(lane);
+  h2 hi[TL][4], lo[TL][4];
 #pragma unroll
   for (int i = 0; i < TL; ++i) {
-    float x, y;
-    in.unpack(i, x, y);
-    sq[i] = fmaf(x, x, y * y);
-  }
-  // lane bits LOG_LANES - 1 .. 1 pick the token, bit 0 is summed
-  transpose_levels<TL / 2, LOG_LANES - 1>(sq, lane);
-  const float sum = xchg_level<0>(false, sq[0], sq[0]);
-  const int mine = (lane % L::LANES) >> 1;   // index of this lane's token
-  // 2^-e with 2^e <= norm < 2^(e + 1), from the exponent of the square.  A row
-  // whose square is not finite is multiplied by 0, as by 1 / sqrt(inf): finite
-  // values give kh = 0, infinities and NaN give NaN.
-  const uint32_t ex = __float_as_uint(sum) >> 23;
-  const int e = (static_cast<int>(ex) - 127) >> 1;
-  const bool usable = ex < 255u;
-  const float down = usable ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 0.0f;
-  const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-  if ((lane & 1) == 0) norm[L::token(lane, mine)] = usable ? up * rsqrt_f(sum + l2_eps) : 0.0f;
-
-  const int c = 2 * (lane % L::LANES);
-  const int s = c / 32, half = (c % 32) / 16, g = (c % 16) / 4, r = c % 4;
-  constexpr int NG = L::NG;
-  h2 hi[TL], lo[TL];
+    float x[8];
+    in.unpack(i, x);
+    float sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < TL; ++i) {
-    // this lane group's token i is held by its lanes 2 i, 2 i + 1
-    const float f = __shfl(down, (lane & ~(L::LANES - 1)) + 2 * i);
-    float x, y;
-    in.unpack(i, x, y);
-    if constexpr (F32) split2(x, y, f, hi[i], lo[i]);
-    else hi[i] = h2{static_cast<_Float16>(x * f), static_cast<_Float16>(y * f)};
-    const int t = L::token(lane, i);
-    const int at = row_slot(s, g, t % 16);
-    *reinterpret_cast<h2*>(&rows[0][t / 16][s][at][half * 4 + r]) = hi[i];
-    if constexpr (F32) *reinterpret_cast<h2*>(&rows[1][t / 16][s][at][half * 4 + r]) = lo[i];
+    for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
+    sum = group_sum<L::LANES>(sum);
+    // 2^-e with 2^e <= norm < 2^(e + 1), from the exponent of the square.  A row
+    // whose square is not finite is multiplied by 0, as by 1 / sqrt(inf): finite
+    // values give kh = 0, infinities and NaN give NaN.
+    const uint32_t ex = __float_as_uint(sum) >> 23;
+    const uint32_t e = (ex + 1u) >> 1;             // 64 + the exponent: ex = 127 gives 64
+    const bool usable = ex < 255u;
+    const float down = usable ? __uint_as_float((191u - e) << 23) : 0.0f;
+    const float up = usable ? __uint_as_float((63u + e) << 23) * rsqrt_f(sum + l2_eps) : 0.0f;
+    const int t = first + L::step(i);
+    if (lane % L::LANES == 0) norm[t] = up;
+#pragma unroll
+    for (int e2 = 0; e2 < 4; ++e2) {
+      if constexpr (F32) {
+        split2(x[2 * e2], x[2 * e2 + 1], down, hi[i][e2], lo[i][e2]);
+      } else {
+        hi[i][e2] = h2{static_cast<_Float16>(x[2 * e2] * down), static_cast<_Float16>(x[2 * e2 + 1] * down)};
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int at = row_slot(s, g + q, t % 16);
+      *reinterpret_cast<h4*>(&rows[0][t / 16][s][at][half * 4]) =
+          h4{hi[i][2 * q].x, hi[i][2 * q].y, hi[i][2 * q + 1].x, hi[i][2 * q + 1].y};
+      if constexpr (F32)
+        *reinterpret_cast<h4*>(&rows[1][t / 16][s][at][half * 4]) =
+            h4{lo[i][2 * q].x, lo[i][2 * q].y, lo[i][2 * q + 1].x, lo[i][2 * q + 1].y};
+    }
   }
   if constexpr (KT) {
+    typedef _Float16 run __attribute__((ext_vector_type(TL)));
+    const int P = L::position(lane);
 #pragma unroll
-    for (int gi = 0; gi < NG; ++gi) {
-      const int tg = (lane / L::LANES) * NG + gi;   // operand group: these 8 tokens
+    for (int ch = 0; ch < 8; ++ch) {
+      const int cc = c + ch;
+      run v;
 #pragma unroll
-      for (int ch = 0; ch < 2; ++ch) {
-        const int cc = c + ch;
-        const int at = tg * 16 + (cc % 16);
-        h8 v;
+      for (int i = 0; i < TL; ++i) v[i] = hi[i][ch / 2][ch % 2];
+      *reinterpret_cast<run*>(&kt[0][cc / 16][kt_slot(P / 8, cc % 16)][P % 8]) = v;
+      if constexpr (F32) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = ch ? hi[8 * gi + i].y : hi[8 * gi + i].x;
-        *reinterpret_cast<h8*>(&kt[0][cc / 16][at][0]) = v;
-        if constexpr (F32) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = ch ? lo[8 * gi + i].y : lo[8 * gi + i].x;
-          *reinterpret_cast<h8*>(&kt[1][cc / 16][at][0]) = v;
-        }
+        for (int i = 0; i < TL; ++i) v[i] = lo[i][ch / 2][ch % 2];
+        *reinterpret_cast<run*>(&kt[1][cc / 16][kt_slot(P / 8, cc % 16)][P % 8]) = v;
       }
     }
   }
@@ -270,6 +282,98 @@ __device__ __forceinline__ void convert_rows(const RowLoader<DK, F32>& in, float
 template <int NCS>
 __device__ __forceinline__ int column(int lane, int cs) {
   return NCS == 2 ? 2 * (lane % 16) + cs : lane % 16;
+}
+
+// NCS neighbouring values of a row of v or out.
+template <bool F32, int NCS>
+struct Columns {
+  static constexpr int W = F32 ? NCS : 1;
+  uint32_t w[W];
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int voff) {
+    if constexpr (F32 && NCS == 2) {
+      const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(r, voff, 0, 0);
+      w[0] = x.x;
+      w[1] = x.y;
+    } else if constexpr (F32 || NCS == 2) {
+      w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, voff, 0, 0);
+    } else {
+      w[0] = __builtin_amdgcn_raw_buffer_load_b16(r, voff, 0, 0);
+    }
+  }
+  __device__ __forceinline__ void unpack(float (&x)[NCS]) const {
+    if constexpr (F32) {
+#pragma unroll
+      for (int c = 0; c < NCS; ++c) x[c] = __uint_as_float(w[c]);
+    } else {
+      x[0] = bf16_to_f32(w[0]);
+      if constexpr (NCS == 2) x[1] = __uint_as_float(w[0] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, int voff, const float (&x)[NCS]) {
+    if constexpr (F32 && NCS == 2) {
+      __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(x[0]), __float_as_uint(x[1])}, r, voff, 0, 0);
+    } else if constexpr (F32) {
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[0]), r, voff, 0, 0);
+    } else if constexpr (NCS == 2) {
+      __builtin_amdgcn_raw_buffer_store_b32(f32x2_to_bf16x2_rne(x[0], x[1]), r, voff, 0, 0);
+    } else {
+      __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(f32_to_bf16_rne(x[0])), r, voff, 0, 0);
+    }
+  }
+};
+
+// The wave's columns of the state tile, from or to memory: a lane's keys
+// 16 j + 4 g + 0..3 are one access of a value-first tile, its NCS columns one
+// of a key-first tile.
+template <bool STORE, int KB, int NCS, bool V_FIRST, bool BF16>
+__device__ __forceinline__ void slab_form(__amdgpu_buffer_rsrc_t res, int dv, int col, int lane, f32x4 (&S)[KB][NCS]) {
+  constexpr int E = BF16 ? 2 : 4;
+  const int key0 = 4 * (lane / 16);
+#pragma unroll
+  for (int j = 0; j < KB; ++j) {
+    if constexpr (V_FIRST) {
+      using IO = StateIO<BF16, 4, 0>;
+#pragma unroll
+      for (int cs = 0; cs < NCS; ++cs) {
+        const int voff = ((col + column<NCS>(lane, cs)) * (KB * 16) + key0) * E;
+        float x[4] = {S[j][cs][0], S[j][cs][1], S[j][cs][2], S[j][cs][3]};
+        if constexpr (STORE) IO::store(res, voff, 16 * j * E, x);
+        else IO::load(res, voff, 16 * j * E, x);
+        S[j][cs] = f32x4{x[0], x[1], x[2], x[3]};
+      }
+    } else {
+      const int voff = (key0 * dv + col + column<NCS>(lane, 0)) * E;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int at = voff + (16 * j + r) * dv * E;
+        float x[NCS];
+        if constexpr (STORE) {
+#pragma unroll
+          for (int cs = 0; cs < NCS; ++cs) x[cs] = S[j][cs][r];
+          Columns<!BF16, NCS>::store(res, at, x);
+        } else {
+          Columns<!BF16, NCS> c;
+          c.load(res, at);
+          c.unpack(x);
+#pragma unroll
+          for (int cs = 0; cs < NCS; ++cs) S[j][cs][r] = x[cs];
+        }
+      }
+    }
+  }
+}
+
+template <bool STORE, int KB, int NCS>
+__device__ __forceinline__ void slab_io(__amdgpu_buffer_rsrc_t res, int layout, int bf16, int dv, int col, int lane,
+                                        f32x4 (&S)[KB][NCS]) {
+  asm("" : "+v"(lane));   // addresses are made here, not kept through the chunks
+  if (layout == KDA_STATE_V_FIRST) {
+    if (bf16) slab_form<STORE, KB, NCS, true, true>(res, dv, col, lane, S);
+    else slab_form<STORE, KB, NCS, true, false>(res, dv, col, lane, S);
+  } else {
+    if (bf16) slab_form<STORE, KB, NCS, false, true>(res, dv, col, lane, S);
+    else slab_form<STORE, KB, NCS, false, false>(res, dv, col, lane, S);
+  }
 }
 
 struct Tile {
@@ -319,6 +423,8 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
   }
   if (w.n == 0) return;
   const int chunks = (w.n + kC - 1) / kC;
+  constexpr int E = F32 ? 4 : 2;
+  const int role = wave - NCW;   // >= 0: helper
 
   // the upper blocks of P and T stay zero
   for (int i = threadIdx.x; i < kRing * 2 * 64; i += blockDim.x)
@@ -326,57 +432,31 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
   for (int i = threadIdx.x; i < 2 * 2 * 64; i += blockDim.x)
     *reinterpret_cast<h4*>(&sh.t[i / 128][(i / 64) % 2][0][i % 64][4]) = h4{0, 0, 0, 0};
 
-  if (wave < 2) {
+  if (role == 0 || role == 1) {
     // ---- helpers 0 and 1: k / q rows of chunk it + 3 ----
-    RowLoader<DK, F32> raw;
-    const void* const src = wave == 0 ? a.k : a.q;
-    raw.load(src, t0, w.n, a.H, w.h, lane);
-    const float amp = exp_f(a.a_log[w.hv]);
-    const float bias = a.dt_bias[w.hv];
-    const int tl = lane % kC;
-    auto gate_at = [&](int c) {   // raw gate and beta logit of the lane's token
-      const int t = c * kC + tl;
-      const int64_t off = (static_cast<int64_t>(t0) + (t < w.n ? t : 0)) * a.HV + w.hv;
-      return make_float2(a.raw_gate[off], a.beta_logits[off]);
+    using L = RowLoader<DK, F32>;
+    const void* const src = role == 0 ? a.k : a.q;
+    const int stride = a.H * DK * E;
+    const int voff = L::token(lane) * stride + 8 * (lane % L::LANES) * E;
+    auto chunk_rows = [&](int c) {
+      return rows_resource(src, ((static_cast<int64_t>(t0) + c * kC) * a.H + w.h) * (DK * E), w.n - c * kC, stride,
+                           DK * E);
     };
-    float2 gate = make_float2(0.0f, 0.0f);
-    if (wave == 1) gate = gate_at(0);
+    L raw;
+    raw.load(chunk_rows(0), voff, stride);
     lds_barrier();
     for (int it = -3; it < chunks; ++it) {
       const int c = it + 3;
       if (c < chunks) {
-        const RowLoader<DK, F32> cur = raw;
-        const float2 gb = gate;
-        if (c + 1 < chunks) {
-          raw.load(src, static_cast<int64_t>(t0) + (c + 1) * kC, w.n - (c + 1) * kC, a.H, w.h, lane);
-          if (wave == 1) gate = gate_at(c + 1);
-        }
+        const L cur = raw;
+        if (c + 1 < chunks) raw.load(chunk_rows(c + 1), voff, stride);
         const int ring = c % kRing, two = c % 2;
-        if (wave == 0) {
-          convert_rows<DK, F32, true>(cur, a.l2_eps, lane, sh.k[ring], sh.kt[ring], sh.norm_k[two]);
-        } else {
-          convert_rows<DK, F32, false>(cur, a.l2_eps, lane, sh.q[ring], nullptr, sh.norm_q[two]);
-          const bool live = c * kC + tl < w.n;
-          const float x = gb.x + bias;
-          float gv = a.gate_mode == KDA_GATE_SOFTPLUS ? -amp * softplus_f(x) : a.lower_bound * sigmoid_f(amp * x);
-          gv = gv < -200.0f ? -200.0f : gv;   // exp(-200) is 0 in fp32, and sums stay finite
-          double sum = live ? static_cast<double>(gv) : 0.0;
-#pragma unroll
-          for (int m = 1; m < kC; m *= 2) {
-            const double y = __shfl_up(sum, m, kC);
-            if (tl >= m) sum += y;
-          }
-          if (lane < kC) {
-            const float hi = static_cast<float>(sum);
-            sh.g_hi[two][tl] = hi;
-            sh.g_lo[two][tl] = static_cast<float>(sum - static_cast<double>(hi));
-            sh.beta[two][tl] = live ? sigmoid_f(gb.y) : 0.0f;
-          }
-        }
+        if (role == 0) convert_rows<DK, F32, true>(cur, a.l2_eps, lane, sh.k[ring], sh.kt[ring], sh.norm_k[two]);
+        else convert_rows<DK, F32, false>(cur, a.l2_eps, lane, sh.q[ring], nullptr, sh.norm_q[two]);
       }
       lds_barrier();
     }
-  } else if (wave == 2) {
+  } else if (role == 2) {
     // ---- helper 2: Gram products of chunk it + 2 ----
     lds_barrier();
     for (int it = -3; it < chunks; ++it) {
@@ -463,10 +543,40 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
       }
       lds_barrier();
     }
-  } else if (wave == 3) {
-    // ---- helper 3: T of chunk it + 1 ----
+  } else if (role == 3) {
+    // ---- helper 3: gates of chunk it + 3, T of chunk it + 1 ----
+    const float amp = exp_f(a.a_log[w.hv]);
+    const float bias = a.dt_bias[w.hv];
+    const int tl = lane % kC;
+    auto gate_at = [&](int c) {   // raw gate and beta logit of the lane's token
+      const int t = c * kC + tl;
+      const int64_t off = (static_cast<int64_t>(t0) + (t < w.n ? t : 0)) * a.HV + w.hv;
+      return make_float2(a.raw_gate[off], a.beta_logits[off]);
+    };
+    float2 gate = gate_at(0);
     lds_barrier();
     for (int it = -3; it < chunks; ++it) {
+      if (it + 3 < chunks) {
+        const int c = it + 3, two = c % 2;
+        const float2 gb = gate;
+        if (c + 1 < chunks) gate = gate_at(c + 1);
+        const bool live = c * kC + tl < w.n;
+        const float x = gb.x + bias;
+        float gv = a.gate_mode == KDA_GATE_SOFTPLUS ? -amp * softplus_f(x) : a.lower_bound * sigmoid_f(amp * x);
+        gv = gv < -200.0f ? -200.0f : gv;   // exp(-200) is 0 in fp32, and sums stay finite
+        double sum = live ? static_cast<double>(gv) : 0.0;
+#pragma unroll
+        for (int m = 1; m < kC; m *= 2) {
+          const double y = __shfl_up(sum, m, kC);
+          if (tl >= m) sum += y;
+        }
+        if (lane < kC) {
+          const float hi = static_cast<float>(sum);
+          sh.g_hi[two][tl] = hi;
+          sh.g_lo[two][tl] = static_cast<float>(sum - static_cast<double>(hi));
+          sh.beta[two][tl] = live ? sigmoid_f(gb.y) : 0.0f;
+        }
+      }
       const int c = it + 1;
       if (c >= 0 && c < chunks) {
         const int two = c % 2;
@@ -512,34 +622,34 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
     }
   } else {
     // ---- state waves ----
-    const int cw = wave - kHelpers;
+    const int cw = wave;
     const int colw = w.col0 + cw * 16 * NCS;
-    const int64_t tile_off = (static_cast<int64_t>(w.slot) * a.HV + w.hv) * (static_cast<int64_t>(DK) * dv);
-    auto state_at = [&](int j, int r, int cs) {   // element of key 16 j + 4 g + r
-      const int key = 16 * j + 4 * g + r, col = colw + column<NCS>(lane, cs);
-      return tile_off + (layout == KDA_STATE_V_FIRST ? static_cast<int64_t>(col) * DK + key
-                                                     : static_cast<int64_t>(key) * dv + col);
-    };
+    const int elem = state_bf16 ? 2 : 4;
+    char* const tile_base = static_cast<char*>(a.state_pool) +
+                            (static_cast<int64_t>(w.slot) * a.HV + w.hv) * (static_cast<int64_t>(DK) * dv * elem);
+    const __amdgpu_buffer_rsrc_t res = tile_resource(tile_base, DK * dv * elem);
     f32x4 S[KB][NCS];
-#pragma unroll
-    for (int j = 0; j < KB; ++j)
-#pragma unroll
-      for (int cs = 0; cs < NCS; ++cs)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          S[j][cs][r] = state_bf16 ? load_scalar<true>(a.state_pool, state_at(j, r, cs))
-                                   : load_scalar<false>(a.state_pool, state_at(j, r, cs));
+    slab_io<false, KB, NCS>(res, layout, state_bf16, dv, colw, lane, S);
 
-    const int64_t vcol = static_cast<int64_t>(w.hv) * dv + colw + column<NCS>(lane, 0);
-    RawRun<!F32, NCS> v[2][4];
+    // v and out of a chunk: the lane's rows 16 rb + 4 g + r, NCS columns
+    const int stride = a.HV * dv * E;
+    int voff[2][4];
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        voff[rb][r] = (16 * rb + 4 * g + r) * stride + (colw + column<NCS>(lane, 0)) * E;
+    auto chunk_rows = [&](const void* base, int c) {
+      return rows_resource(base, ((static_cast<int64_t>(t0) + c * kC) * a.HV + w.hv) * (dv * E), w.n - c * kC, stride,
+                           dv * E);
+    };
+    Columns<F32, NCS> v[2][4];
     auto load_v = [&](int c) {
+      const __amdgpu_buffer_rsrc_t r0 = chunk_rows(a.v, c);
 #pragma unroll
       for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int t = c * kC + 16 * rb + 4 * g + r;
-          v[rb][r].load(a.v, (static_cast<int64_t>(t0) + (t < w.n ? t : 0)) * a.HV * dv + vcol);
-        }
+        for (int r = 0; r < 4; ++r) v[rb][r].load(r0, voff[rb][r]);
     };
     load_v(0);
     lds_barrier();
@@ -598,10 +708,9 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
           for (int r = 0; r < 4; ++r) {
             float x[NCS];
             v[rb][r].unpack(x);
-            const bool live = it * kC + 16 * rb + 4 * g + r < w.n;
 #pragma unroll
-            for (int cs = 0; cs < NCS; ++cs)
-              R[rb][cs][r] = live ? fmaf(-ck[r] * up_s[cs], ks[rb][cs][r], be[r] * x[cs]) : 0.0f;
+            for (int cs = 0; cs < NCS; ++cs)   // past the end: beta = 0
+              R[rb][cs][r] = fmaf(-ck[r] * up_s[cs], ks[rb][cs][r], be[r] * x[cs]);
           }
         }
         if (it + 1 < chunks) load_v(it + 1);
@@ -630,6 +739,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
         }
         // S = e^(G_last) S + (diag(e^(G_last - G)) Kh)^T U
         const float last = sh.last[ring];
+        const int kat = kt_slot(g, lane % 16);
         const f32x4 w0 = *reinterpret_cast<const f32x4*>(&sh.tab[ring][3][4 * g]);
         const f32x4 w1 = *reinterpret_cast<const f32x4*>(&sh.tab[ring][3][16 + 4 * g]);
 #pragma unroll
@@ -638,9 +748,9 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
           split8(U[0][cs] * w0, U[1][cs] * w1, 1.0f, hi, lo);
 #pragma unroll
           for (int j = 0; j < KB; ++j) {
-            const h8 k0 = *reinterpret_cast<const h8*>(&sh.kt[ring][0][j][lane][0]);
+            const h8 k0 = *reinterpret_cast<const h8*>(&sh.kt[ring][0][j][kat][0]);
             f32x4 acc = {0, 0, 0, 0};
-            if constexpr (F32) acc = mfma(*reinterpret_cast<const h8*>(&sh.kt[ring][1][j][lane][0]), hi, acc);
+            if constexpr (F32) acc = mfma(*reinterpret_cast<const h8*>(&sh.kt[ring][1][j][kat][0]), hi, acc);
             acc = mfma(k0, lo, acc);
             acc = mfma(k0, hi, acc);
 #pragma unroll
@@ -666,29 +776,20 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
               qs[rb][cs][r] = fmaf(cq[r] * up_s[cs], qs[rb][cs][r], a.scale * up_u[cs] * acc[r]);
           }
         }
+        const __amdgpu_buffer_rsrc_t ro = chunk_rows(a.out, it);
 #pragma unroll
         for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int t = it * kC + 16 * rb + 4 * g + r;
-            if (t < w.n) {
-              const int64_t off = (static_cast<int64_t>(t0) + t) * a.HV * dv + vcol;
-              if constexpr (NCS == 2) store_pair<!F32>(a.out, off, qs[rb][0][r], qs[rb][1][r]);
-              else store_scalar<!F32>(a.out, off, qs[rb][0][r]);
-            }
+            float x[NCS];
+#pragma unroll
+            for (int cs = 0; cs < NCS; ++cs) x[cs] = qs[rb][cs][r];
+            Columns<F32, NCS>::store(ro, voff[rb][r], x);
           }
       }
       lds_barrier();
     }
-#pragma unroll
-    for (int j = 0; j < KB; ++j)
-#pragma unroll
-      for (int cs = 0; cs < NCS; ++cs)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if (state_bf16) store_scalar<true>(a.state_pool, state_at(j, r, cs), S[j][cs][r]);
-          else store_scalar<false>(a.state_pool, state_at(j, r, cs), S[j][cs][r]);
-        }
+    slab_io<true, KB, NCS>(res, layout, state_bf16, dv, colw, lane, S);
   }
 }
 
