@@ -4,8 +4,8 @@
 // Mathematics.  One decay per token and head, G_i its log summed from the
 // chunk's start, S0 the state before the chunk:
 //   A_ij = beta_i e^(G_i - G_j) kh_i.kh_j          (i > j)
-//   T    = (I + A)^-1                              (unit lower triangular)
-//   U    = T diag(beta) (V - diag(e^G) Kh S0)
+//   T    = (I + A)^-1 diag(beta)                   (lower triangular)
+//   U    = T (V - diag(e^G) Kh S0)
 //   P_ij = e^(G_i - G_j) qh_i.kh_j / scale         (i >= j)
 //   O    = diag(e^G) Qh S0 + scale P U
 //   S    = e^(G_last) S0 + (diag(e^(G_last - G)) Kh)^T U
@@ -19,9 +19,11 @@
 //   - a row of q or k is divided by a power of two near its norm; a bf16 row
 //     then is exact in fp16 (but for values below 2^-17 of the norm, off by
 //     at most 2^-25 of it), an fp32 row is taken as hi + lo, 22 bits;
-//   - the state, R = diag(beta)(V - ...) and U are scaled by a power of two
-//     per value column and taken as hi + lo; T and P, whose entries are at
-//     most 1 in size, as hi + lo.
+//   - the state, R = V - diag(e^G) Kh S0 and U are held in a unit 2^sig per
+//     value column and taken as hi + lo; T and P, whose entries are at most 1
+//     in size, as hi + lo.  The unit follows a bound on the state's size
+//     (below); fp16's smallest step, 2^-24, then is at most 2^-25 of the
+//     largest value also where the bound is 2^13 too wide.
 // |T_ij| <= 1: T_ij = -beta_i kh_i^T [product of contractions] kh_j.  The
 // lo.lo terms (2^-22) are dropped.  So an operand carries about 22 bits and
 // the result is close to fp32's; two bf16 terms would leave 16 bits.  G is
@@ -60,6 +62,7 @@ namespace {
 constexpr int kC = 32;            // tokens per chunk
 constexpr int kHelpers = 4;
 constexpr int kRing = 4;          // chunks of q and k held in LDS
+constexpr int kRefresh = 8;       // chunks between looks at the state's true size
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
@@ -76,32 +79,46 @@ __device__ __forceinline__ f32x4 mfma(h8 a, h8 b, f32x4 c) {
 }
 
 // x * s as hi + lo in fp16 (s a power of two).  The packed hi is made opaque
-// so that lo is taken from it and not from conversions of its own.
-__device__ __forceinline__ void split2(float x0, float x1, float s, h2& hi, h2& lo) {
-  hi = h2{static_cast<_Float16>(x0 * s), static_cast<_Float16>(x1 * s)};
+// so that lo is taken from it and not from conversions of its own, in one
+// mixed-precision FMA each.
+__device__ __forceinline__ h2 low_part(float x0, float x1, float s, h2& hi) {
   asm("" : "+v"(hi));
-  lo = h2{static_cast<_Float16>(__builtin_fmaf(x0, s, -static_cast<float>(hi.x))),
-          static_cast<_Float16>(__builtin_fmaf(x1, s, -static_cast<float>(hi.y)))};
+  return h2{static_cast<_Float16>(__builtin_fmaf(x0, s, -static_cast<float>(hi.x))),
+            static_cast<_Float16>(__builtin_fmaf(x1, s, -static_cast<float>(hi.y)))};
 }
 
-__device__ __forceinline__ void split8(const f32x4& x, const f32x4& y, float s, h8& hi, h8& lo) {
+__device__ __forceinline__ void split2(float x0, float x1, float s, h2& hi, h2& lo) {
+  hi = h2{static_cast<_Float16>(x0 * s), static_cast<_Float16>(x1 * s)};
+  lo = low_part(x0, x1, s, hi);
+}
+
+// The same with s = 1 for two accumulators' rows, as an operand.  `one` is a
+// 1.0f that the compiler does not see as such: it would take the FMA apart.
+__device__ __forceinline__ void split8(const f32x4& x, const f32x4& y, float one, h8& hi, h8& lo) {
   h2 h[4], l[4];
-  split2(x[0], x[1], s, h[0], l[0]);
-  split2(x[2], x[3], s, h[1], l[1]);
-  split2(y[0], y[1], s, h[2], l[2]);
-  split2(y[2], y[3], s, h[3], l[3]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x0 = i < 2 ? x[2 * i] : y[2 * i - 4], x1 = i < 2 ? x[2 * i + 1] : y[2 * i - 3];
+    h[i] = h2{static_cast<_Float16>(x0), static_cast<_Float16>(x1)};
+    l[i] = low_part(x0, x1, one, h[i]);
+  }
   hi = h8{h[0].x, h[0].y, h[1].x, h[1].y, h[2].x, h[2].y, h[3].x, h[3].y};
   lo = h8{l[0].x, l[0].y, l[1].x, l[1].y, l[2].x, l[2].y, l[3].x, l[3].y};
 }
 
-// The power of two that brings m (>= 0) into [2^P, 2^(P + 1)), and its
-// inverse; below 2^-100 the factor stays where it is there (zero included).
-template <int P>
-__device__ __forceinline__ float scale_for(float m, float& inverse) {
-  uint32_t e = __float_as_uint(m) >> 23;
-  e = e < 27u ? 27u : e;
-  inverse = __uint_as_float((e - P) << 23);
-  return __uint_as_float((254u + P - e) << 23);
+// The unit of a state column is 2^sig.  Moves it so that `bound`, a bound on
+// the column in it, comes into [2^13, 2^14), but not below 2^min; returns by
+// how many powers it moved.
+constexpr int kSigMin = -100;
+__device__ __forceinline__ int rescale(float& bound, int& sig, int min) {
+  const int e = static_cast<int>(__float_as_uint(bound) >> 23) - 127;
+  int to = sig + e - 13;
+  min = min < kSigMin ? kSigMin : min;
+  to = to < min ? min : to;
+  const int d = to - sig;
+  sig = to;
+  bound = __builtin_ldexpf(bound, -d);
+  return d;
 }
 
 __device__ __forceinline__ float max16_32(float x) {   // over lanes that share lane % 16
@@ -109,6 +126,23 @@ __device__ __forceinline__ float max16_32(float x) {   // over lanes that share 
   x = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
   const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+
+// A double moved within its row of 16 lanes (0 where none comes in), and
+// lane 15's.
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, 0xf, 0xf, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, 0xf, 0xf, true);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+__device__ __forceinline__ double lane15_f64(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(u), 15);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), 15);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 
 // ---------------------------------------------------------------------------
@@ -121,8 +155,12 @@ __device__ __forceinline__ float max16_32(float x) {   // over lanes that share 
 // holds of two stacked accumulators).  Slots are permuted within their row
 // of 16 so that the writes of one token spread over the banks.
 __device__ __forceinline__ int row_slot(int s, int g, int row) {
-  return g * 16 + (row ^ ((g + 4 * s) & 7));
+  return g * 16 + (row ^ (((g >> 1) + 2 * s) & 7));
 }
+
+// The same for key block j of K^T, whose writers hold one channel of every
+// other block at a time.
+__device__ __forceinline__ int kt_slot(int j, int g, int channel) { return g * 16 + (channel ^ (j & 7)); }
 
 template <int DK, bool F32>
 struct Shared {
@@ -132,17 +170,14 @@ struct Shared {
   _Float16 q[kRing][TERMS][2][KS][64][8];
   _Float16 kt[kRing][TERMS][DK / 16][64][8];       // K^T: [key block], k = token
   _Float16 p[kRing][2][2][64][8];                  // P hi, lo: [token block]
-  _Float16 t[2][2][2][64][8];                      // T hi, lo
-  float a[2][3][16][16];                           // A: blocks 00, 11, 10; [column][row]
-  float join[2][16][16];                           // T's diagonal blocks, row-major
+  _Float16 t[2][2][2][64][8];                      // T hi, lo, beta included
+  float a[2][3][16][16];                           // A: blocks 00, 11, 10; row-major
+  float join[2][16][16];                           // diagonal blocks of (I + A)^-1, row-major
   float norm_k[2][kC], norm_q[2][kC];              // kh = norm_k * stored row
   float g_hi[2][kC], g_lo[2][kC], beta[2][kC];
-  float tab[kRing][4][kC];                         // beta; beta e^G norm_k; scale e^G norm_q; norm_k e^(last - G)
+  float tab[kRing][4][kC];                         // beta; e^G norm_k; scale e^G norm_q; norm_k e^(last - G)
   float last[kRing];                               // e^(G_last)
 };
-
-// The same for K^T, whose writers hold 8 neighbouring channels.
-__device__ __forceinline__ int kt_slot(int g, int channel) { return g * 16 + (channel ^ ((channel >> 3) & 1)); }
 
 // ---------------------------------------------------------------------------
 // the rows of k or q
@@ -193,17 +228,24 @@ struct RowLoader {
   }
 };
 
-// Sum over the LANES lanes of a group, to all of them.
-template <int LANES>
-__device__ __forceinline__ float group_sum(float x) {
-  x += dpp<kDppXor1>(x);
-  x += dpp<kDppXor2>(x);
-  if constexpr (LANES == 8) x += dpp<kDppHalfMirror>(x);   // quads are uniform by now
-  if constexpr (LANES == 16) {
-    x += dpp<kDppRowRor4>(x);
-    x += dpp<kDppRowRor8>(x);
+// Sums over the LANES lanes of a group, to all of them; level by level, so
+// that the moves of one sum hide the latency of another's.
+template <int LANES, int N>
+__device__ __forceinline__ void group_sums(float (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] += dpp<kDppXor1>(x[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] += dpp<kDppXor2>(x[i]);
+  if constexpr (LANES == 8) {   // quads are uniform by now
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] += dpp<kDppHalfMirror>(x[i]);
   }
-  return x;
+  if constexpr (LANES == 16) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] += dpp<kDppRowRor4>(x[i]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] += dpp<kDppRowRor8>(x[i]);
+  }
 }
 
 // Converts a chunk's rows: fp16 rows in operand order, their factors
@@ -217,15 +259,22 @@ __device__ __forceinline__ void convert_rows(const RowLoader<DK, F32>& in, float
   const int c = 8 * (lane % L::LANES);
   const int s = c / 32, half = (c % 32) / 16, g = (c % 16) / 4;   // the lane's channels: operand groups g, g + 1
   const int first = L::token(lane);
+  float sums[TL];
+#pragma unroll
+  for (int i = 0; i < TL; ++i) {
+    float x[8];
+    in.unpack(i, x);
+    sums[i] = x[0] * x[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) sums[i] = fmaf(x[e], x[e], sums[i]);
+  }
+  group_sums<L::LANES>(sums);
   h2 hi[TL][4], lo[TL][4];
 #pragma unroll
   for (int i = 0; i < TL; ++i) {
     float x[8];
     in.unpack(i, x);
-    float sum = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
-    sum = group_sum<L::LANES>(sum);
+    const float sum = sums[i];
     // 2^-e with 2^e <= norm < 2^(e + 1), from the exponent of the square.  A row
     // whose square is not finite is multiplied by 0, as by 1 / sqrt(inf): finite
     // values give kh = 0, infinities and NaN give NaN.
@@ -263,11 +312,11 @@ __device__ __forceinline__ void convert_rows(const RowLoader<DK, F32>& in, float
       run v;
 #pragma unroll
       for (int i = 0; i < TL; ++i) v[i] = hi[i][ch / 2][ch % 2];
-      *reinterpret_cast<run*>(&kt[0][cc / 16][kt_slot(P / 8, cc % 16)][P % 8]) = v;
+      *reinterpret_cast<run*>(&kt[0][cc / 16][kt_slot(cc / 16, P / 8, cc % 16)][P % 8]) = v;
       if constexpr (F32) {
 #pragma unroll
         for (int i = 0; i < TL; ++i) v[i] = lo[i][ch / 2][ch % 2];
-        *reinterpret_cast<run*>(&kt[1][cc / 16][kt_slot(P / 8, cc % 16)][P % 8]) = v;
+        *reinterpret_cast<run*>(&kt[1][cc / 16][kt_slot(cc / 16, P / 8, cc % 16)][P % 8]) = v;
       }
     }
   }
@@ -376,6 +425,17 @@ __device__ __forceinline__ void slab_io(__amdgpu_buffer_rsrc_t res, int layout, 
   }
 }
 
+// max |S| of a column, to the four lanes that hold it.
+template <int KB, int NCS>
+__device__ __forceinline__ float largest(const f32x4 (&S)[KB][NCS], int cs) {
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < KB; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(S[j][cs][r]));
+  return max16_32(m);
+}
+
 struct Tile {
   int b, hv, h, slot, col0;   // col0: first column of the workgroup
   int t0, n;                  // first row and tokens
@@ -480,11 +540,12 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
 #pragma unroll
           for (int m = 0; m < 3; ++m) {
             const int i = m > 0, j = m == 1;   // row block i, column block j
-            ka[m] = mfma(kk[0][i], kk[0][j], ka[m]);   // rows i, columns j
-            pa[m] = mfma(kk[0][j], qq[0][i], pa[m]);   // rows j, columns i
+            // transposed: a lane holds row lane % 16 of block i, columns 4 g + 0..3 of block j
+            ka[m] = mfma(kk[0][j], kk[0][i], ka[m]);
+            pa[m] = mfma(kk[0][j], qq[0][i], pa[m]);
             if constexpr (F32) {
-              ka[m] = mfma(kk[0][i], kk[1][j], ka[m]);
-              ka[m] = mfma(kk[1][i], kk[0][j], ka[m]);
+              ka[m] = mfma(kk[0][j], kk[1][i], ka[m]);
+              ka[m] = mfma(kk[1][j], kk[0][i], ka[m]);
               pa[m] = mfma(kk[0][j], qq[1][i], pa[m]);
               pa[m] = mfma(kk[1][j], qq[0][i], pa[m]);
             }
@@ -494,35 +555,24 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
 #pragma unroll
         for (int m = 0; m < 3; ++m) {
           const int i = m > 0, j = m == 1;
-          // A: column 16 j + lane % 16, rows 16 i + 4 g + 0..3
-          {
-            const int col = 16 * j + lane % 16, row = 16 * i + 4 * g;
-            const float gh = sh.g_hi[two][col], gl = sh.g_lo[two][col], nk = sh.norm_k[two][col];
-            const f32x4 rh = *reinterpret_cast<const f32x4*>(&sh.g_hi[two][row]);
-            const f32x4 rl = *reinterpret_cast<const f32x4*>(&sh.g_lo[two][row]);
-            const f32x4 rk = *reinterpret_cast<const f32x4*>(&sh.norm_k[two][row]);
-            const f32x4 rb = *reinterpret_cast<const f32x4*>(&sh.beta[two][row]);
-            f32x4 x;
+          const int row = 16 * i + lane % 16, col = 16 * j + 4 * g;
+          const float gh = sh.g_hi[two][row], gl = sh.g_lo[two][row];
+          const float nq = sh.norm_q[two][row], nk = sh.norm_k[two][row] * sh.beta[two][row];
+          const f32x4 ch = *reinterpret_cast<const f32x4*>(&sh.g_hi[two][col]);
+          const f32x4 cl = *reinterpret_cast<const f32x4*>(&sh.g_lo[two][col]);
+          const f32x4 ck = *reinterpret_cast<const f32x4*>(&sh.norm_k[two][col]);
+          f32x4 y;
+          float x[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float d = exp_f((rh[r] - gh) + (rl[r] - gl));
-              x[r] = row + r > col ? ka[m][r] * nk * (rk[r] * rb[r]) * d : 0.0f;
-            }
-            *reinterpret_cast<f32x4*>(&sh.a[two][m][lane % 16][4 * g]) = x;
+          for (int r = 0; r < 4; ++r) {
+            // e^(G_row - G_col) norm_col; above the diagonal the exponent may
+            // be positive, and is not used
+            const float d = exp_f((gh - ch[r]) + (gl - cl[r])) * ck[r];
+            y[r] = col + r < row ? ka[m][r] * nk * d : 0.0f;
+            x[r] = col + r <= row ? pa[m][r] * nq * d : 0.0f;
           }
-          // P: row 16 i + lane % 16, columns 16 j + 4 g + 0..3
+          *reinterpret_cast<f32x4*>(&sh.a[two][m][lane % 16][4 * g]) = y;
           {
-            const int row = 16 * i + lane % 16, col = 16 * j + 4 * g;
-            const float gh = sh.g_hi[two][row], gl = sh.g_lo[two][row], nq = sh.norm_q[two][row];
-            const f32x4 ch = *reinterpret_cast<const f32x4*>(&sh.g_hi[two][col]);
-            const f32x4 cl = *reinterpret_cast<const f32x4*>(&sh.g_lo[two][col]);
-            const f32x4 ck = *reinterpret_cast<const f32x4*>(&sh.norm_k[two][col]);
-            float x[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float d = exp_f((gh - ch[r]) + (gl - cl[r]));
-              x[r] = col + r <= row ? pa[m][r] * nq * ck[r] * d : 0.0f;
-            }
             h2 hi0, lo0, hi1, lo1;
             split2(x[0], x[1], 1.0f, hi0, lo0);
             split2(x[2], x[3], 1.0f, hi1, lo1);
@@ -535,7 +585,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
           const float nk = sh.norm_k[two][lane], be = sh.beta[two][lane];
           const float eg = exp_f(gh + gl);
           sh.tab[ring][0][lane] = be;
-          sh.tab[ring][1][lane] = be * eg * nk;
+          sh.tab[ring][1][lane] = eg * nk;
           sh.tab[ring][2][lane] = a.scale * eg * sh.norm_q[two][lane];
           sh.tab[ring][3][lane] = nk * exp_f((g_last - gh) + (g_last_lo - gl));
           if (lane == kC - 1) sh.last[ring] = eg;
@@ -565,11 +615,12 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
         float gv = a.gate_mode == KDA_GATE_SOFTPLUS ? -amp * softplus_f(x) : a.lower_bound * sigmoid_f(amp * x);
         gv = gv < -200.0f ? -200.0f : gv;   // exp(-200) is 0 in fp32, and sums stay finite
         double sum = live ? static_cast<double>(gv) : 0.0;
-#pragma unroll
-        for (int m = 1; m < kC; m *= 2) {
-          const double y = __shfl_up(sum, m, kC);
-          if (tl >= m) sum += y;
-        }
+        sum += dpp_f64<0x111>(sum);   // row_shr 1, 2, 4, 8: zero comes in
+        sum += dpp_f64<0x112>(sum);
+        sum += dpp_f64<0x114>(sum);
+        sum += dpp_f64<0x118>(sum);
+        const double row0 = lane15_f64(sum);
+        if (tl >= 16) sum += row0;
         if (lane < kC) {
           const float hi = static_cast<float>(sum);
           sh.g_hi[two][tl] = hi;
@@ -580,24 +631,32 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
       const int c = it + 1;
       if (c >= 0 && c < chunks) {
         const int two = c % 2;
-        // lane: row `row` of diagonal block `blk` (lanes 32.. repeat); x (I + A)
-        // = e_row solved from the last column back
+        // lane: row `row` of diagonal block `blk` (lanes 32.. repeat), x (I + A)
+        // = e_row, from the last column back: with x_k known, row k of A is
+        // taken off all columns before it
         const int blk = (lane / 16) % 2, row = lane % 16;
         float x[16];
 #pragma unroll
-        for (int j = 15; j >= 0; --j) {
-          float acc = row == j ? 1.0f : 0.0f;
+        for (int j = 0; j < 16; ++j) x[j] = row == j ? 1.0f : 0.0f;
 #pragma unroll
-          for (int k = 15; k > j; --k) acc = fmaf(-x[k], sh.a[two][blk][j][k], acc);
-          x[j] = acc;
+        for (int k = 15; k > 0; --k) {
+#pragma unroll
+          for (int j4 = 0; j4 < (k + 3) / 4; ++j4) {
+            const f32x4 ar = *reinterpret_cast<const f32x4*>(&sh.a[two][blk][k][4 * j4]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (4 * j4 + j < k) x[4 * j4 + j] = fmaf(-x[k], ar[j], x[4 * j4 + j]);
+          }
         }
         if (lane < 32) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            *reinterpret_cast<f32x4*>(&sh.join[blk][row][4 * j]) = f32x4{x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]};
+            const f32x4 xj = {x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]};
+            *reinterpret_cast<f32x4*>(&sh.join[blk][row][4 * j]) = xj;
+            const f32x4 xb = xj * *reinterpret_cast<const f32x4*>(&sh.tab[c % kRing][0][16 * blk + 4 * j]);
             h2 hi0, lo0, hi1, lo1;
-            split2(x[4 * j], x[4 * j + 1], 1.0f, hi0, lo0);
-            split2(x[4 * j + 2], x[4 * j + 3], 1.0f, hi1, lo1);
+            split2(xb[0], xb[1], 1.0f, hi0, lo0);
+            split2(xb[2], xb[3], 1.0f, hi1, lo1);
             *reinterpret_cast<h4*>(&sh.t[two][0][blk][16 * j + row][4 * blk]) = h4{hi0.x, hi0.y, hi1.x, hi1.y};
             *reinterpret_cast<h4*>(&sh.t[two][1][blk][16 * j + row][4 * blk]) = h4{lo0.x, lo0.y, lo1.x, lo1.y};
           }
@@ -605,16 +664,16 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront", "local");
         // T10^T = -T00^T (A10^T T11^T) on the fp32 matrix instruction
         f32x4 z = {0, 0, 0, 0}, y = {0, 0, 0, 0};
-        const f32x4 at = *reinterpret_cast<const f32x4*>(&sh.a[two][2][lane % 16][4 * g]);    // A10[4g + r][lane % 16]
         const f32x4 bt = *reinterpret_cast<const f32x4*>(&sh.join[1][lane % 16][4 * g]);      // T11[lane % 16][4g + r]
 #pragma unroll
-        for (int r = 0; r < 4; ++r) z = __builtin_amdgcn_mfma_f32_16x16x4f32(at[r], bt[r], z, 0, 0, 0);
+        for (int r = 0; r < 4; ++r) z = __builtin_amdgcn_mfma_f32_16x16x4f32(sh.a[two][2][4 * g + r][lane % 16], bt[r], z, 0, 0, 0);
 #pragma unroll
         for (int r = 0; r < 4; ++r) y = __builtin_amdgcn_mfma_f32_16x16x4f32(sh.join[0][4 * g + r][lane % 16], z[r], y, 0, 0, 0);
         // y: column (row of T10) lane % 16, rows (columns of T10) 4 g + 0..3
+        y *= -*reinterpret_cast<const f32x4*>(&sh.tab[c % kRing][0][4 * g]);
         h2 hi0, lo0, hi1, lo1;
-        split2(-y[0], -y[1], 1.0f, hi0, lo0);
-        split2(-y[2], -y[3], 1.0f, hi1, lo1);
+        split2(y[0], y[1], 1.0f, hi0, lo0);
+        split2(y[2], y[3], 1.0f, hi1, lo1);
         *reinterpret_cast<h4*>(&sh.t[two][0][1][lane][0]) = h4{hi0.x, hi0.y, hi1.x, hi1.y};
         *reinterpret_cast<h4*>(&sh.t[two][1][1][lane][0]) = h4{lo0.x, lo0.y, lo1.x, lo1.y};
       }
@@ -652,29 +711,39 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
         for (int r = 0; r < 4; ++r) v[rb][r].load(r0, voff[rb][r]);
     };
     load_v(0);
+    // S of column cs is held divided by 2^sig[cs]; |S| <= bound[cs] < 2^14 so held
+    int sig[NCS];
+    float bound[NCS];
+    float one = 1.0f;
+    asm("" : "+s"(one));
+#pragma unroll
+    for (int cs = 0; cs < NCS; ++cs) {
+      sig[cs] = 0;
+      bound[cs] = largest(S, cs);
+      const int d = rescale(bound[cs], sig[cs], kSigMin);
+      const float f = __builtin_ldexpf(1.0f, -d);
+#pragma unroll
+      for (int j = 0; j < KB; ++j) S[j][cs] *= f;
+    }
     lds_barrier();
     for (int it = -3; it < chunks; ++it) {
       if (it >= 0) {
         const int ring = it % kRing;
+        if (it % kRefresh == kRefresh - 1) {
+#pragma unroll
+          for (int cs = 0; cs < NCS; ++cs) bound[cs] = largest(S, cs);
+        }
         // K S and Q S, the state as hi + lo
         f32x4 ks[2][NCS], qs[2][NCS];
-        float down_s[NCS], up_s[NCS];
 #pragma unroll
-        for (int cs = 0; cs < NCS; ++cs) {
-          float m = 0.0f;
+        for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
-          for (int j = 0; j < KB; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(S[j][cs][r]));
-          down_s[cs] = scale_for<13>(max16_32(m), up_s[cs]);
-#pragma unroll
-          for (int rb = 0; rb < 2; ++rb) ks[rb][cs] = qs[rb][cs] = f32x4{0, 0, 0, 0};
-        }
+          for (int cs = 0; cs < NCS; ++cs) ks[rb][cs] = qs[rb][cs] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
           h8 hi[NCS], lo[NCS];
 #pragma unroll
-          for (int cs = 0; cs < NCS; ++cs) split8(S[2 * s][cs], S[2 * s + 1][cs], down_s[cs], hi[cs], lo[cs]);
+          for (int cs = 0; cs < NCS; ++cs) split8(S[2 * s][cs], S[2 * s + 1][cs], one, hi[cs], lo[cs]);
           const int at = row_slot(s, g, lane % 16);
 #pragma unroll
           for (int rb = 0; rb < 2; ++rb) {
@@ -698,25 +767,32 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
             }
           }
         }
-        // R = beta v - beta e^G kh^T S
+        // R = v - e^G kh^T S, in units of 2^sig (zero past the end)
         f32x4 R[2][NCS];
+        float down[NCS], up_old[NCS];
+#pragma unroll
+        for (int cs = 0; cs < NCS; ++cs) {
+          down[cs] = __builtin_ldexpf(1.0f, -sig[cs]);
+          up_old[cs] = __builtin_ldexpf(1.0f, sig[cs]);
+        }
 #pragma unroll
         for (int rb = 0; rb < 2; ++rb) {
-          const f32x4 be = *reinterpret_cast<const f32x4*>(&sh.tab[ring][0][16 * rb + 4 * g]);
           const f32x4 ck = *reinterpret_cast<const f32x4*>(&sh.tab[ring][1][16 * rb + 4 * g]);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             float x[NCS];
             v[rb][r].unpack(x);
 #pragma unroll
-            for (int cs = 0; cs < NCS; ++cs)   // past the end: beta = 0
-              R[rb][cs][r] = fmaf(-ck[r] * up_s[cs], ks[rb][cs][r], be[r] * x[cs]);
+            for (int cs = 0; cs < NCS; ++cs)
+              R[rb][cs][r] = fmaf(-ck[r], ks[rb][cs][r], down[cs] * x[cs]);
           }
         }
         if (it + 1 < chunks) load_v(it + 1);
-        // U = T R
+        // The new state is at most last |S| + sum_j |kh_j| |U_j| in size, and
+        // |U_j| <= 32 max|R|: move the unit so that this bound is in [2^13, 2^14)
+        const float last = sh.last[ring];
         f32x4 U[2][NCS];
-        float up_u[NCS];
+        float keep[NCS], up_new[NCS];
 #pragma unroll
         for (int cs = 0; cs < NCS; ++cs) {
           float m = 0.0f;
@@ -724,9 +800,19 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
           for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
             for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(R[rb][cs][r]));
-          const float down = scale_for<9>(max16_32(m), up_u[cs]);   // |U| <= 32 max|R|
+          bound[cs] = fmaf(last, bound[cs], 1024.0f * max16_32(m));
+          const int d = rescale(bound[cs], sig[cs], sig[cs] - 100);
+          keep[cs] = __builtin_ldexpf(last, -d);
+          up_new[cs] = __builtin_ldexpf(1.0f, sig[cs]);
+          // U = T R
           h8 hi, lo;
-          split8(R[0][cs], R[1][cs], down, hi, lo);
+          f32x4 r0, r1;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            r0[r] = __builtin_ldexpf(R[0][cs][r], -d);
+            r1[r] = __builtin_ldexpf(R[1][cs][r], -d);
+          }
+          split8(r0, r1, one, hi, lo);
 #pragma unroll
           for (int rb = 0; rb < 2; ++rb) {
             const h8 t0h = *reinterpret_cast<const h8*>(&sh.t[it % 2][0][rb][lane][0]);
@@ -738,30 +824,27 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
           }
         }
         // S = e^(G_last) S + (diag(e^(G_last - G)) Kh)^T U
-        const float last = sh.last[ring];
-        const int kat = kt_slot(g, lane % 16);
         const f32x4 w0 = *reinterpret_cast<const f32x4*>(&sh.tab[ring][3][4 * g]);
         const f32x4 w1 = *reinterpret_cast<const f32x4*>(&sh.tab[ring][3][16 + 4 * g]);
 #pragma unroll
         for (int cs = 0; cs < NCS; ++cs) {
           h8 hi, lo;
-          split8(U[0][cs] * w0, U[1][cs] * w1, 1.0f, hi, lo);
+          split8(U[0][cs] * w0, U[1][cs] * w1, one, hi, lo);
 #pragma unroll
           for (int j = 0; j < KB; ++j) {
-            const h8 k0 = *reinterpret_cast<const h8*>(&sh.kt[ring][0][j][kat][0]);
-            f32x4 acc = {0, 0, 0, 0};
-            if constexpr (F32) acc = mfma(*reinterpret_cast<const h8*>(&sh.kt[ring][1][j][kat][0]), hi, acc);
+            const int at = kt_slot(j, g, lane % 16);
+            f32x4 acc = S[j][cs] * keep[cs];
+            if constexpr (F32) acc = mfma(*reinterpret_cast<const h8*>(&sh.kt[ring][1][j][at][0]), hi, acc);
+            const h8 k0 = *reinterpret_cast<const h8*>(&sh.kt[ring][0][j][at][0]);
             acc = mfma(k0, lo, acc);
-            acc = mfma(k0, hi, acc);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) S[j][cs][r] = fmaf(acc[r], up_u[cs], last * S[j][cs][r]);
+            S[j][cs] = mfma(k0, hi, acc);
           }
         }
         // O = e^G Qh S0 + P U
 #pragma unroll
         for (int cs = 0; cs < NCS; ++cs) {
           h8 hi, lo;
-          split8(U[0][cs], U[1][cs], 1.0f, hi, lo);
+          split8(U[0][cs], U[1][cs], one, hi, lo);
 #pragma unroll
           for (int rb = 0; rb < 2; ++rb) {
             const h8 p0 = *reinterpret_cast<const h8*>(&sh.p[ring][0][rb][lane][0]);
@@ -773,7 +856,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
             const f32x4 cq = *reinterpret_cast<const f32x4*>(&sh.tab[ring][2][16 * rb + 4 * g]);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              qs[rb][cs][r] = fmaf(cq[r] * up_s[cs], qs[rb][cs][r], a.scale * up_u[cs] * acc[r]);
+              qs[rb][cs][r] = fmaf(cq[r] * up_old[cs], qs[rb][cs][r], a.scale * up_new[cs] * acc[r]);
           }
         }
         const __amdgpu_buffer_rsrc_t ro = chunk_rows(a.out, it);
@@ -788,6 +871,12 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
           }
       }
       lds_barrier();
+    }
+#pragma unroll
+    for (int cs = 0; cs < NCS; ++cs) {
+      const float f = __builtin_ldexpf(1.0f, sig[cs]);
+#pragma unroll
+      for (int j = 0; j < KB; ++j) S[j][cs] *= f;
     }
     slab_io<true, KB, NCS>(res, layout, state_bf16, dv, colw, lane, S);
   }
