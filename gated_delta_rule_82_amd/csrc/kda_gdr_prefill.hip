@@ -38,10 +38,9 @@
 // waves, each a chunk further on:
 //   0  K: fp16 rows in operand order (K for K S0 and the Gram
 //      products, K^T for the state update), norms      chunk c + 3
-//   1  Q: the same without K^T                         chunk c + 3
+//   1  Q: the same without K^T; the gates: G and beta  chunk c + 3
 //   2  the Gram products: A, P, the factor tables      chunk c + 2
-//   3  the gates (g, G, beta)                          chunk c + 3
-//      T: two 16 x 16 triangular inverses, joined      chunk c + 1
+//   3  T: two 16 x 16 triangular inverses, joined      chunk c + 1
 // with one barrier per chunk.  The accumulator layout of one product (four
 // consecutive rows per lane) is the operand layout of the next once the
 // operands' order of k is permuted to match, so the chain never leaves its
@@ -83,8 +82,9 @@ __device__ __forceinline__ f32x4 mfma(h8 a, h8 b, f32x4 c) {
 // mixed-precision FMA each.
 __device__ __forceinline__ h2 low_part(float x0, float x1, float s, h2& hi) {
   asm("" : "+v"(hi));
-  return h2{static_cast<_Float16>(__builtin_fmaf(x0, s, -static_cast<float>(hi.x))),
-            static_cast<_Float16>(__builtin_fmaf(x1, s, -static_cast<float>(hi.y)))};
+  _Float16 lo = static_cast<_Float16>(__builtin_fmaf(x0, s, -static_cast<float>(hi.x)));
+  asm("" : "+v"(lo));   // not a packed conversion of two separate FMAs
+  return h2{lo, static_cast<_Float16>(__builtin_fmaf(x1, s, -static_cast<float>(hi.y)))};
 }
 
 __device__ __forceinline__ void split2(float x0, float x1, float s, h2& hi, h2& lo) {
@@ -248,6 +248,20 @@ __device__ __forceinline__ void group_sums(float (&x)[N]) {
   }
 }
 
+// A row's power of two 2^-e, with 2^e <= norm < 2^(e + 1), from the exponent of
+// its square; and the factor that makes the row times 2^-e a unit row.  A row
+// whose square is not finite is multiplied by 0, as by 1 / sqrt(inf): finite
+// values give kh = 0, infinities and NaN give NaN.
+__device__ __forceinline__ float row_down(float square) {
+  const uint32_t ex = __float_as_uint(square) >> 23;
+  return ex < 255u ? __uint_as_float((191u - ((ex + 1u) >> 1)) << 23) : 0.0f;   // e = (ex + 1) / 2 - 64
+}
+
+__device__ __forceinline__ float row_factor(float square, float l2_eps) {
+  const uint32_t ex = __float_as_uint(square) >> 23;
+  return ex < 255u ? __uint_as_float((63u + ((ex + 1u) >> 1)) << 23) * rsqrt_f(square + l2_eps) : 0.0f;
+}
+
 // Converts a chunk's rows: fp16 rows in operand order, their factors
 // (norm[token] * stored row = unit row), and for k the transposed operand.
 template <int DK, bool F32, bool KT>
@@ -269,22 +283,19 @@ __device__ __forceinline__ void convert_rows(const RowLoader<DK, F32>& in, float
     for (int e = 1; e < 8; ++e) sums[i] = fmaf(x[e], x[e], sums[i]);
   }
   group_sums<L::LANES>(sums);
+  // lane i of a group writes the factor of the group's token i
+  const int mine = lane % L::LANES;
+  float own = sums[0];
+#pragma unroll
+  for (int i = 1; i < TL; ++i) own = mine == i ? sums[i] : own;
+  if (mine < TL) norm[first + L::step(mine)] = row_factor(own, l2_eps);
   h2 hi[TL][4], lo[TL][4];
 #pragma unroll
   for (int i = 0; i < TL; ++i) {
     float x[8];
     in.unpack(i, x);
-    const float sum = sums[i];
-    // 2^-e with 2^e <= norm < 2^(e + 1), from the exponent of the square.  A row
-    // whose square is not finite is multiplied by 0, as by 1 / sqrt(inf): finite
-    // values give kh = 0, infinities and NaN give NaN.
-    const uint32_t ex = __float_as_uint(sum) >> 23;
-    const uint32_t e = (ex + 1u) >> 1;             // 64 + the exponent: ex = 127 gives 64
-    const bool usable = ex < 255u;
-    const float down = usable ? __uint_as_float((191u - e) << 23) : 0.0f;
-    const float up = usable ? __uint_as_float((63u + e) << 23) * rsqrt_f(sum + l2_eps) : 0.0f;
+    const float down = row_down(sums[i]);
     const int t = first + L::step(i);
-    if (lane % L::LANES == 0) norm[t] = up;
 #pragma unroll
     for (int e2 = 0; e2 < 4; ++e2) {
       if constexpr (F32) {
@@ -484,7 +495,11 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
   if (w.n == 0) return;
   const int chunks = (w.n + kC - 1) / kC;
   constexpr int E = F32 ? 4 : 2;
-  const int role = wave - NCW;   // >= 0: helper
+  // Helper's role, or -1.  Waves i and i + 4 share a SIMD: one state wave gets
+  // one to itself and the last helper goes with the lightest (16384 tokens x
+  // 32 heads 965 us with the state wave beside it, 876 us so).
+  int role = wave - NCW;
+  if constexpr (NCW == 1) role = wave == 3 ? -1 : wave == 4 ? 3 : wave == 0 ? 2 : wave - 1;
 
   // the upper blocks of P and T stay zero
   for (int i = threadIdx.x; i < kRing * 2 * 64; i += blockDim.x)
@@ -493,7 +508,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
     *reinterpret_cast<h4*>(&sh.t[i / 128][(i / 64) % 2][0][i % 64][4]) = h4{0, 0, 0, 0};
 
   if (role == 0 || role == 1) {
-    // ---- helpers 0 and 1: k / q rows of chunk it + 3 ----
+    // ---- helpers 0 and 1: k / q rows of chunk it + 3, and with q the gates ----
     using L = RowLoader<DK, F32>;
     const void* const src = role == 0 ? a.k : a.q;
     const int stride = a.H * DK * E;
@@ -504,15 +519,49 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
     };
     L raw;
     raw.load(chunk_rows(0), voff, stride);
+    const float amp = exp_f(a.a_log[w.hv]);
+    const float bias = a.dt_bias[w.hv];
+    const int tl = lane % kC;
+    auto gate_at = [&](int c) {   // raw gate and beta logit of the lane's token
+      const int t = c * kC + tl;
+      const int64_t off = (static_cast<int64_t>(t0) + (t < w.n ? t : 0)) * a.HV + w.hv;
+      return make_float2(a.raw_gate[off], a.beta_logits[off]);
+    };
+    float2 gate = make_float2(0.0f, 0.0f);
+    if (role == 1) gate = gate_at(0);
     lds_barrier();
     for (int it = -3; it < chunks; ++it) {
       const int c = it + 3;
       if (c < chunks) {
         const L cur = raw;
-        if (c + 1 < chunks) raw.load(chunk_rows(c + 1), voff, stride);
+        const float2 gb = gate;
+        if (c + 1 < chunks) {
+          raw.load(chunk_rows(c + 1), voff, stride);
+          if (role == 1) gate = gate_at(c + 1);
+        }
         const int ring = c % kRing, two = c % 2;
-        if (role == 0) convert_rows<DK, F32, true>(cur, a.l2_eps, lane, sh.k[ring], sh.kt[ring], sh.norm_k[two]);
-        else convert_rows<DK, F32, false>(cur, a.l2_eps, lane, sh.q[ring], nullptr, sh.norm_q[two]);
+        if (role == 0) {
+          convert_rows<DK, F32, true>(cur, a.l2_eps, lane, sh.k[ring], sh.kt[ring], sh.norm_k[two]);
+        } else {
+          convert_rows<DK, F32, false>(cur, a.l2_eps, lane, sh.q[ring], nullptr, sh.norm_q[two]);
+          const bool live = c * kC + tl < w.n;
+          const float x = gb.x + bias;
+          float gv = a.gate_mode == KDA_GATE_SOFTPLUS ? -amp * softplus_f(x) : a.lower_bound * sigmoid_f(amp * x);
+          gv = gv < -200.0f ? -200.0f : gv;   // exp(-200) is 0 in fp32, and sums stay finite
+          double sum = live ? static_cast<double>(gv) : 0.0;
+          sum += dpp_f64<0x111>(sum);   // row_shr 1, 2, 4, 8: zero comes in
+          sum += dpp_f64<0x112>(sum);
+          sum += dpp_f64<0x114>(sum);
+          sum += dpp_f64<0x118>(sum);
+          const double row0 = lane15_f64(sum);
+          if (tl >= 16) sum += row0;
+          if (lane < kC) {
+            const float hi = static_cast<float>(sum);
+            sh.g_hi[two][tl] = hi;
+            sh.g_lo[two][tl] = static_cast<float>(sum - static_cast<double>(hi));
+            sh.beta[two][tl] = live ? sigmoid_f(gb.y) : 0.0f;
+          }
+        }
       }
       lds_barrier();
     }
@@ -594,40 +643,9 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
       lds_barrier();
     }
   } else if (role == 3) {
-    // ---- helper 3: gates of chunk it + 3, T of chunk it + 1 ----
-    const float amp = exp_f(a.a_log[w.hv]);
-    const float bias = a.dt_bias[w.hv];
-    const int tl = lane % kC;
-    auto gate_at = [&](int c) {   // raw gate and beta logit of the lane's token
-      const int t = c * kC + tl;
-      const int64_t off = (static_cast<int64_t>(t0) + (t < w.n ? t : 0)) * a.HV + w.hv;
-      return make_float2(a.raw_gate[off], a.beta_logits[off]);
-    };
-    float2 gate = gate_at(0);
+    // ---- helper 3: T of chunk it + 1 ----
     lds_barrier();
     for (int it = -3; it < chunks; ++it) {
-      if (it + 3 < chunks) {
-        const int c = it + 3, two = c % 2;
-        const float2 gb = gate;
-        if (c + 1 < chunks) gate = gate_at(c + 1);
-        const bool live = c * kC + tl < w.n;
-        const float x = gb.x + bias;
-        float gv = a.gate_mode == KDA_GATE_SOFTPLUS ? -amp * softplus_f(x) : a.lower_bound * sigmoid_f(amp * x);
-        gv = gv < -200.0f ? -200.0f : gv;   // exp(-200) is 0 in fp32, and sums stay finite
-        double sum = live ? static_cast<double>(gv) : 0.0;
-        sum += dpp_f64<0x111>(sum);   // row_shr 1, 2, 4, 8: zero comes in
-        sum += dpp_f64<0x112>(sum);
-        sum += dpp_f64<0x114>(sum);
-        sum += dpp_f64<0x118>(sum);
-        const double row0 = lane15_f64(sum);
-        if (tl >= 16) sum += row0;
-        if (lane < kC) {
-          const float hi = static_cast<float>(sum);
-          sh.g_hi[two][tl] = hi;
-          sh.g_lo[two][tl] = static_cast<float>(sum - static_cast<double>(hi));
-          sh.beta[two][tl] = live ? sigmoid_f(gb.y) : 0.0f;
-        }
-      }
       const int c = it + 1;
       if (c >= 0 && c < chunks) {
         const int two = c % 2;
@@ -681,7 +699,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
     }
   } else {
     // ---- state waves ----
-    const int cw = wave;
+    const int cw = NCW == 1 ? 0 : wave;
     const int colw = w.col0 + cw * 16 * NCS;
     const int elem = state_bf16 ? 2 : 4;
     char* const tile_base = static_cast<char*>(a.state_pool) +
