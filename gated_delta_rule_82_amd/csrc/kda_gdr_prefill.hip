@@ -61,6 +61,7 @@ namespace {
 constexpr int kC = 32;            // tokens per chunk
 constexpr int kHelpers = 4;
 constexpr int kRing = 4;          // chunks of q and k held in LDS
+constexpr int kRingP = 3;         // of P, made a chunk later
 constexpr int kRefresh = 8;       // chunks between looks at the state's true size
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
@@ -169,7 +170,7 @@ struct Shared {
   _Float16 k[kRing][TERMS][2][KS][64][8];          // K rows: [token block][key step]
   _Float16 q[kRing][TERMS][2][KS][64][8];
   _Float16 kt[kRing][TERMS][DK / 16][64][8];       // K^T: [key block], k = token
-  _Float16 p[kRing][2][2][64][8];                  // P hi, lo: [token block]
+  _Float16 p[kRingP][2][2][64][8];                 // P hi, lo: [token block]
   _Float16 t[2][2][2][64][8];                      // T hi, lo, beta included
   float a[2][3][16][16];                           // A: blocks 00, 11, 10; row-major
   float join[2][16][16];                           // diagonal blocks of (I + A)^-1, row-major
@@ -495,14 +496,14 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
   if (w.n == 0) return;
   const int chunks = (w.n + kC - 1) / kC;
   constexpr int E = F32 ? 4 : 2;
-  // Helper's role, or -1.  Waves i and i + 4 share a SIMD: one state wave gets
-  // one to itself and the last helper goes with the lightest (16384 tokens x
-  // 32 heads 965 us with the state wave beside it, 876 us so).
-  int role = wave - NCW;
-  if constexpr (NCW == 1) role = wave == 3 ? -1 : wave == 4 ? 3 : wave == 0 ? 2 : wave - 1;
+  // Waves i and i + 4 share a SIMD.  With fewer than four state waves they get
+  // SIMDs of their own and the helpers share the others.
+  constexpr uint32_t kRoles = NCW == 1 ? 0x3f102u : NCW == 2 ? 0x13ff02u : NCW == 4 ? 0x3210ffffu : 0u;
+  const int role = static_cast<int>(kRoles >> (4 * wave) & 15u);   // 15: state wave
+  const int cw = NCW == 1 ? 0 : NCW == 2 ? wave - 2 : wave;
 
   // the upper blocks of P and T stay zero
-  for (int i = threadIdx.x; i < kRing * 2 * 64; i += blockDim.x)
+  for (int i = threadIdx.x; i < kRingP * 2 * 64; i += blockDim.x)
     *reinterpret_cast<h4*>(&sh.p[i / 128][(i / 64) % 2][0][i % 64][4]) = h4{0, 0, 0, 0};
   for (int i = threadIdx.x; i < 2 * 2 * 64; i += blockDim.x)
     *reinterpret_cast<h4*>(&sh.t[i / 128][(i / 64) % 2][0][i % 64][4]) = h4{0, 0, 0, 0};
@@ -568,6 +569,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
   } else if (role == 2) {
     // ---- helper 2: Gram products of chunk it + 2 ----
     lds_barrier();
+    int third = 0;   // c % kRingP
     for (int it = -3; it < chunks; ++it) {
       const int c = it + 2;
       if (c >= 0 && c < chunks) {
@@ -625,8 +627,8 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
             h2 hi0, lo0, hi1, lo1;
             split2(x[0], x[1], 1.0f, hi0, lo0);
             split2(x[2], x[3], 1.0f, hi1, lo1);
-            *reinterpret_cast<h4*>(&sh.p[ring][0][i][lane][4 * j]) = h4{hi0.x, hi0.y, hi1.x, hi1.y};
-            *reinterpret_cast<h4*>(&sh.p[ring][1][i][lane][4 * j]) = h4{lo0.x, lo0.y, lo1.x, lo1.y};
+            *reinterpret_cast<h4*>(&sh.p[third][0][i][lane][4 * j]) = h4{hi0.x, hi0.y, hi1.x, hi1.y};
+            *reinterpret_cast<h4*>(&sh.p[third][1][i][lane][4 * j]) = h4{lo0.x, lo0.y, lo1.x, lo1.y};
           }
         }
         if (lane < kC) {
@@ -639,6 +641,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
           sh.tab[ring][3][lane] = nk * exp_f((g_last - gh) + (g_last_lo - gl));
           if (lane == kC - 1) sh.last[ring] = eg;
         }
+        third = third == kRingP - 1 ? 0 : third + 1;
       }
       lds_barrier();
     }
@@ -699,7 +702,6 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
     }
   } else {
     // ---- state waves ----
-    const int cw = NCW == 1 ? 0 : wave;
     const int colw = w.col0 + cw * 16 * NCS;
     const int elem = state_bf16 ? 2 : 4;
     char* const tile_base = static_cast<char*>(a.state_pool) +
@@ -734,6 +736,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
     float bound[NCS];
     float one = 1.0f;
     asm("" : "+s"(one));
+    int third = 0;   // it % kRingP
 #pragma unroll
     for (int cs = 0; cs < NCS; ++cs) {
       sig[cs] = 0;
@@ -865,8 +868,8 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
           split8(U[0][cs], U[1][cs], one, hi, lo);
 #pragma unroll
           for (int rb = 0; rb < 2; ++rb) {
-            const h8 p0 = *reinterpret_cast<const h8*>(&sh.p[ring][0][rb][lane][0]);
-            const h8 p1 = *reinterpret_cast<const h8*>(&sh.p[ring][1][rb][lane][0]);
+            const h8 p0 = *reinterpret_cast<const h8*>(&sh.p[third][0][rb][lane][0]);
+            const h8 p1 = *reinterpret_cast<const h8*>(&sh.p[third][1][rb][lane][0]);
             f32x4 acc = {0, 0, 0, 0};
             acc = mfma(p1, hi, acc);
             acc = mfma(p0, lo, acc);
@@ -887,6 +890,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
             for (int cs = 0; cs < NCS; ++cs) x[cs] = qs[rb][cs][r];
             Columns<F32, NCS>::store(ro, voff[rb][r], x);
           }
+        third = third == kRingP - 1 ? 0 : third + 1;
       }
       lds_barrier();
     }
@@ -919,13 +923,29 @@ hipError_t launch_form(const DecodeArgs& args, int dv, int layout, int state_bf1
   return hipLaunchKernel(fn, dim3(static_cast<uint32_t>(nwg)), dim3((NCW + kHelpers) * kWave), kargs, lds, stream);
 }
 
+// A workgroup fills a CU (its LDS ring does), so the time is the number of
+// rounds of 256 workgroups times a form's time per chunk.  The fewer columns,
+// the shorter the chain of a chunk, but the more workgroups: the narrowest form
+// that is one round, else the widest.  1024 tokens, dk = dv = 128, us by number
+// of tiles (forms of 16 / 32 / 64 / 128 columns):
+//      8 tiles   52   57   62   86
+//     32         55   60   65   89
+//     64        105   64   67   90
+//    128        202  120   72   93
+//    256        389  230  139  101
+//    768       1169  667  408  306
+// 16 columns per state wave beat 32 (64 columns in two waves 86 us against 65
+// in four) but for the 128-column form, where eight waves of 16 columns and the
+// helpers are short of registers and issue slots (652 us against 624 on 768
+// tiles x 2048 tokens).
 template <int DK, bool F32>
 hipError_t launch_dk(const DecodeArgs& args, int dv, int layout, int state_bf16, hipStream_t stream) {
   const int64_t tiles = static_cast<int64_t>(args.B) * args.HV;
-  if (dv >= 128 && tiles >= kCus) return launch_form<4, 2, DK, F32>(args, dv, layout, state_bf16, stream);
-  if (dv >= 64 && tiles * (dv / 64) >= kCus) return launch_form<2, 2, DK, F32>(args, dv, layout, state_bf16, stream);
-  if (tiles * (dv / 32) >= kCus) return launch_form<1, 2, DK, F32>(args, dv, layout, state_bf16, stream);
-  return launch_form<1, 1, DK, F32>(args, dv, layout, state_bf16, stream);
+  const auto one_round = [&](int columns) { return tiles * (dv / columns) <= kCus; };
+  if (one_round(16)) return launch_form<1, 1, DK, F32>(args, dv, layout, state_bf16, stream);
+  if (dv == 32 || one_round(32)) return launch_form<2, 1, DK, F32>(args, dv, layout, state_bf16, stream);
+  if (dv == 64 || one_round(64)) return launch_form<4, 1, DK, F32>(args, dv, layout, state_bf16, stream);
+  return launch_form<4, 2, DK, F32>(args, dv, layout, state_bf16, stream);
 }
 
 }  // namespace
