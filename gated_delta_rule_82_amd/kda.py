@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -80,6 +81,9 @@ class KdaLibraryMissing(RuntimeError):
 
 
 _lib: Optional[ctypes.CDLL] = None
+_torch = None          # set by library()
+_raw_stream = None
+_DTYPES = {}           # torch dtype -> kda_dtype
 
 
 def library() -> ctypes.CDLL:
@@ -94,24 +98,29 @@ def library() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise KdaLibraryMissing(
             f"{LIB_PATH} is not built; run `python -m gated_delta_rule_82_amd.build`")
-    import torch  # noqa: F401  (binds the process to torch's HIP runtime first)
+    import torch  # (binds the process to torch's HIP runtime first)
+    global _torch, _raw_stream
+    _torch = torch
+    _DTYPES.update({torch.float32: KDA_F32, torch.bfloat16: KDA_BF16, torch.int32: KDA_I32})
+    # the current stream's handle without a Stream object (microseconds of a short call)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
     lib = ctypes.CDLL(LIB_PATH, mode=ctypes.RTLD_LOCAL)
-    P = ctypes.POINTER(KdaTensor)
-    lib.kda_decode.argtypes = [P] * 11 + [ctypes.POINTER(KdaMode), ctypes.c_void_p]
+    # tensors and structs go by address: of a ctypes structure, or of packed
+    # descriptors (see _pack)
+    P = ctypes.c_void_p
+    lib.kda_decode.argtypes = [P] * 13
     lib.kda_decode.restype = ctypes.c_int
-    lib.kda_decode_conv.argtypes = [P, ctypes.POINTER(KdaConv)] + [P] * 7 + [ctypes.POINTER(KdaMode),
-                                                                        ctypes.c_void_p]
+    lib.kda_decode_conv.argtypes = [P] * 11
     lib.kda_decode_conv.restype = ctypes.c_int
-    lib.kda_prefill.argtypes = [P] * 11 + [ctypes.POINTER(KdaMode), ctypes.c_int32,
-                                            ctypes.c_void_p]
+    lib.kda_prefill.argtypes = [P] * 12 + [ctypes.c_int32, P]
     lib.kda_prefill.restype = ctypes.c_int
     for fn in (lib.kda_gdr_decode, lib.kda_gdr_prefill):
-        fn.argtypes = [P] * 11 + [ctypes.POINTER(KdaMode), ctypes.c_void_p]
+        fn.argtypes = [P] * 13
         fn.restype = ctypes.c_int
-    lib.kda_decode_window.argtypes = [P] * 11 + [ctypes.POINTER(KdaReplay),
-                                                 ctypes.POINTER(KdaMode), ctypes.c_void_p]
+    lib.kda_decode_window.argtypes = [P] * 14
     lib.kda_decode_window.restype = ctypes.c_int
-    lib.kda_verify.argtypes = [P] * 9 + [ctypes.c_void_p]
+    lib.kda_verify.argtypes = [P] * 10
     lib.kda_verify.restype = ctypes.c_int
     lib.kda_check_host.argtypes = [ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32),
                                    ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]
@@ -220,6 +229,86 @@ ARG_NAMES = ("out", "q", "k", "v", "raw_gate", "beta_logits", "a_log", "dt_bias"
              "cu_seqlens", "state_pool", "state_indices")
 
 
+# ---------------------------------------------------------------------------
+# the call path: descriptors are packed straight into one buffer per call (a
+# decode step of one user takes a few microseconds on the GPU, and building
+# ctypes structures for 11 tensors took 20)
+# ---------------------------------------------------------------------------
+
+_TENSOR = struct.Struct("=Qii4q")     # kda_tensor
+_MODE = struct.Struct("=ifffi")       # kda_mode
+assert _TENSOR.size == ctypes.sizeof(KdaTensor) and _MODE.size == ctypes.sizeof(KdaMode)
+_BUFFERS = {n: ctypes.c_char * (n * _TENSOR.size + _MODE.size) for n in range(1, 20)}
+
+
+def _refuse(tensors, names, dev):
+    """Say what is wrong with the tensors of a call that _pack stopped at."""
+    for t, n in zip(tensors, names):
+        _descriptor(t, n)
+    for t, n in zip(tensors, names):
+        if t.device.index != dev:
+            raise ValueError(f"{n}: on {t.device}, expected cuda:{dev}")
+    raise ValueError("a tensor cannot be passed to libkda")
+
+
+def _pack(tensors, names, dev):
+    """kda_tensor descriptors of ``tensors``, all on GPU ``dev``, one behind
+    the other, with room for a kda_mode.  Returns the buffer and its address."""
+    buf = _BUFFERS[len(tensors)]()
+    pack, at, size = _TENSOR.pack_into, 0, _TENSOR.size
+    for t in tensors:
+        try:
+            shape = t.shape
+            n = len(shape)
+            dt = _DTYPES.get(t.dtype)
+            if dt is None or n > 4 or t.get_device() != dev or not t.is_contiguous():
+                _refuse(tensors, names, dev)
+            if n < 4:
+                shape = (*shape, 0, 0, 0, 0)[:4]
+            pack(buf, at, t.data_ptr(), dt, n, *shape)
+        except AttributeError:
+            _refuse(tensors, names, dev)
+        at += size
+    return buf, ctypes.addressof(buf)
+
+
+def _device(t, name):
+    """Index of the GPU that ``t`` is on."""
+    if not hasattr(t, "get_device") or t.get_device() < 0:
+        _descriptor(t, name)
+    return t.get_device()
+
+
+def _pack_mode(buf, n, gate_mode, lower_bound, l2_eps, scale, state_layout):
+    """kda_mode behind n descriptors."""
+    at = n * _TENSOR.size
+    gm = GATE_MODES[gate_mode] if isinstance(gate_mode, str) else int(gate_mode)
+    sl = STATE_LAYOUTS[state_layout] if isinstance(state_layout, str) else int(state_layout)
+    try:
+        _MODE.pack_into(buf, at, gm, lower_bound, l2_eps, scale, sl)
+    except OverflowError:   # past fp32: infinite, as ctypes has it
+        mode = make_mode(gm, lower_bound, l2_eps, scale, sl)
+        ctypes.memmove(ctypes.addressof(buf) + at, ctypes.addressof(mode), _MODE.size)
+
+
+def _call(fn, args, dev, stream, where, tail=()):
+    """Call ``fn`` with GPU ``dev`` current, on ``stream`` or torch's current one."""
+    if _torch.cuda.current_device() != dev:
+        with _torch.cuda.device(dev):
+            return _call(fn, args, dev, stream, where, tail)
+    rc = fn(*args, *tail, _raw_stream(dev) if stream is None else stream)
+    if rc != KDA_OK:
+        raise KdaError(rc, where)
+
+
+def _recurrence(fn, where, tensors, gate_mode, lower_bound, l2_eps, scale, state_layout, stream, tail=()):
+    """The calls that take the 11 tensors of kda_decode and a mode."""
+    dev = _device(tensors[1], "q")
+    buf, at = _pack(tensors, ARG_NAMES, dev)
+    _pack_mode(buf, 11, gate_mode, lower_bound, l2_eps, scale, state_layout)
+    _call(fn, range(at, at + 12 * 48, 48), dev, stream, where, tail)
+
+
 def decode(out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool,
            state_indices, *, gate_mode="softplus", lower_bound=0.0, l2_eps=0.0, scale=0.0,
            state_layout="k_first", stream: Optional[int] = None) -> None:
@@ -230,21 +319,9 @@ def decode(out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, stat
     out [N, HV, dk, dv] ("k_first") or [N, HV, dv, dk] ("v_first").  The work
     is enqueued on ``stream`` (a raw hipStream_t handle; default: torch's
     current stream of q's device)."""
-    import torch
-    tensors = (out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool,
-               state_indices)
-    descs = [_descriptor(t, n) for t, n in zip(tensors, ARG_NAMES)]
-    dev = q.device
-    for t, n in zip(tensors, ARG_NAMES):
-        if t.device != dev:
-            raise ValueError(f"{n}: on {t.device}, expected {dev}")
-    mode = make_mode(gate_mode, lower_bound, l2_eps, scale, state_layout)
-    with torch.cuda.device(dev):
-        if stream is None:
-            stream = torch.cuda.current_stream(dev).cuda_stream
-        rc = call_raw(descs, mode, stream)
-    if rc != KDA_OK:
-        raise KdaError(rc)
+    _recurrence(library().kda_decode, "kda_decode",
+                (out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool, state_indices),
+                gate_mode, lower_bound, l2_eps, scale, state_layout, stream)
 
 
 def prefill(out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool,
@@ -253,22 +330,10 @@ def prefill(out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, sta
     """The recurrence over long requests in chunks of 16 tokens on the matrix
     cores (kda_prefill in include/kda.h): same tensors and result as
     :func:`decode`; ``matmul`` is "split_bf16" (default) or "f32"."""
-    import torch
-    tensors = (out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool,
-               state_indices)
-    descs = [_descriptor(t, n) for t, n in zip(tensors, ARG_NAMES)]
-    dev = q.device
-    for t, n in zip(tensors, ARG_NAMES):
-        if t.device != dev:
-            raise ValueError(f"{n}: on {t.device}, expected {dev}")
-    mode = make_mode(gate_mode, lower_bound, l2_eps, scale, state_layout)
     mm = MATMULS[matmul] if isinstance(matmul, str) else int(matmul)
-    with torch.cuda.device(dev):
-        if stream is None:
-            stream = torch.cuda.current_stream(dev).cuda_stream
-        rc = call_raw_prefill(descs, mode, mm, stream)
-    if rc != KDA_OK:
-        raise KdaError(rc, "kda_prefill")
+    _recurrence(library().kda_prefill, "kda_prefill",
+                (out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool, state_indices),
+                gate_mode, lower_bound, l2_eps, scale, state_layout, stream, (mm,))
 
 
 def check_host(cu_seqlens, state_indices, T: int, n_slots: int) -> int:
@@ -298,42 +363,14 @@ def decode_conv(out, x_q, x_k, x_v, w_q, w_k, w_v, win_q, win_k, win_v, q_conv, 
     [1, T, HV, dv] pre-convolution inputs; taps w_* [K, C]; windows win_*
     [N, K-1, C] (updated in place); q_conv, k_conv [1, T, H, dk] receive the
     convolved q and k (they may be x_q and x_k themselves)."""
-    import torch
-    conv_t = (x_q, x_k, x_v, w_q, w_k, w_v, win_q, win_k, win_v, q_conv, k_conv)
-    rest_t = (raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool, state_indices)
-    conv = KdaConv(*[_descriptor(t, n) for t, n in zip(conv_t, CONV_FIELDS)])
-    rest = [_descriptor(t, n) for t, n in zip(rest_t, CONV_REST)]
-    out_d = _descriptor(out, "out")
-    dev = out.device
-    for t, n in zip(conv_t + rest_t, CONV_FIELDS + CONV_REST):
-        if t.device != dev:
-            raise ValueError(f"{n}: on {t.device}, expected {dev}")
-    mode = make_mode(gate_mode, lower_bound, l2_eps, scale, state_layout)
-    with torch.cuda.device(dev):
-        if stream is None:
-            stream = torch.cuda.current_stream(dev).cuda_stream
-        rc = call_raw_conv(out_d, conv, rest, mode, stream)
-    if rc != KDA_OK:
-        raise KdaError(rc, "kda_decode_conv")
-
-
-def _check_device(named, dev):
-    for n, t in named:
-        if t.device != dev:
-            raise ValueError(f"{n}: on {t.device}, expected {dev}")
-
-
-def _gdr(prefill, tensors, mode, stream, where):
-    import torch
-    descs = [_descriptor(t, n) for t, n in zip(tensors, ARG_NAMES)]
-    dev = tensors[1].device
-    _check_device(zip(ARG_NAMES, tensors), dev)
-    with torch.cuda.device(dev):
-        if stream is None:
-            stream = torch.cuda.current_stream(dev).cuda_stream
-        rc = call_raw_gdr(descs, mode, prefill, stream)
-    if rc != KDA_OK:
-        raise KdaError(rc, where)
+    fn = library().kda_decode_conv
+    tensors = (out, x_q, x_k, x_v, w_q, w_k, w_v, win_q, win_k, win_v, q_conv, k_conv, raw_gate,
+               beta_logits, a_log, dt_bias, cu_seqlens, state_pool, state_indices)
+    dev = _device(out, "out")
+    buf, at = _pack(tensors, ("out",) + CONV_FIELDS + CONV_REST, dev)
+    _pack_mode(buf, 19, gate_mode, lower_bound, l2_eps, scale, state_layout)
+    # out, the kda_conv (11 descriptors), the 7 others and the mode
+    _call(fn, (at, at + 48, *range(at + 12 * 48, at + 20 * 48, 48)), dev, stream, "kda_decode_conv")
 
 
 def gdr_decode(out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool,
@@ -342,9 +379,9 @@ def gdr_decode(out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, 
     """The gated delta rule with one decay per (token, value head)
     (kda_gdr_decode in include/kda.h): as :func:`decode`, with raw_gate
     [1, T, HV] and dt_bias [HV]."""
-    _gdr(False, (out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool,
-                 state_indices),
-         make_mode(gate_mode, lower_bound, l2_eps, scale, state_layout), stream, "kda_gdr_decode")
+    _recurrence(library().kda_gdr_decode, "kda_gdr_decode",
+                (out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool, state_indices),
+                gate_mode, lower_bound, l2_eps, scale, state_layout, stream)
 
 
 def gdr_prefill(out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool,
@@ -352,9 +389,12 @@ def gdr_prefill(out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens,
                 state_layout="k_first", stream: Optional[int] = None) -> None:
     """:func:`gdr_decode` for whole prompts (kda_gdr_prefill in
     include/kda.h): same tensors and result."""
-    _gdr(True, (out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool,
-                state_indices),
-         make_mode(gate_mode, lower_bound, l2_eps, scale, state_layout), stream, "kda_gdr_prefill")
+    _recurrence(library().kda_gdr_prefill, "kda_gdr_prefill",
+                (out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool, state_indices),
+                gate_mode, lower_bound, l2_eps, scale, state_layout, stream)
+
+
+_WINDOW_NAMES = ARG_NAMES + tuple(f"replay {n}" for n in REPLAY_FIELDS)
 
 
 def decode_window(out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool,
@@ -369,23 +409,14 @@ def decode_window(out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlen
 
     A serving loop passes the previous call's k, v, raw_gate and beta_logits
     with its ``cu_seqlens[:-1]`` and the ``n_commit`` of :func:`verify`."""
-    import torch
-    tensors = (out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool,
-               state_indices)
-    replay_t = (replay_k, replay_v, replay_gate, replay_beta, replay_begin, replay_count)
-    names = [f"replay {n}" for n in REPLAY_FIELDS]
-    descs = [_descriptor(t, n) for t, n in zip(tensors, ARG_NAMES)]
-    replay = KdaReplay(*[_descriptor(t, n) for t, n in zip(replay_t, names)])
-    dev = q.device
-    _check_device(zip(ARG_NAMES, tensors), dev)
-    _check_device(zip(names, replay_t), dev)
-    mode = make_mode(gate_mode, lower_bound, l2_eps, scale, state_layout)
-    with torch.cuda.device(dev):
-        if stream is None:
-            stream = torch.cuda.current_stream(dev).cuda_stream
-        rc = call_raw_window(descs, replay, mode, stream)
-    if rc != KDA_OK:
-        raise KdaError(rc, "kda_decode_window")
+    fn = library().kda_decode_window
+    tensors = (out, q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool, state_indices,
+               replay_k, replay_v, replay_gate, replay_beta, replay_begin, replay_count)
+    dev = _device(q, "q")
+    buf, at = _pack(tensors, _WINDOW_NAMES, dev)
+    _pack_mode(buf, 17, gate_mode, lower_bound, l2_eps, scale, state_layout)
+    # 11 tensors, the kda_replay (6 descriptors) and the mode
+    _call(fn, (*range(at, at + 12 * 48, 48), at + 17 * 48), dev, stream, "kda_decode_window")
 
 
 VERIFY_NAMES = ("n_commit", "next_token", "target_probs", "draft_probs", "tokens", "u_accept",
@@ -406,23 +437,22 @@ def verify(n_commit, next_token, target_probs, draft_probs, tokens, u_accept, u_
     least ``verify_workspace(B, V)`` values) is taken from torch's allocator
     if not given; with ``stream`` given it has to be too, since that memory
     belongs to torch's current stream."""
-    import torch
+    fn = library().kda_verify
+    if workspace is None and stream is not None:
+        raise ValueError("workspace: required with an explicit stream")
+    if not hasattr(target_probs, "dim") or target_probs.dim() != 2:
+        raise ValueError("target_probs: expected a [T, V] tensor")
+    dev = _device(target_probs, "target_probs")
     if workspace is None:
-        if stream is not None:
-            raise ValueError("workspace: required with an explicit stream")
-        if not isinstance(target_probs, torch.Tensor) or target_probs.dim() != 2:
-            raise ValueError("target_probs: expected a [T, V] tensor")
-        workspace = torch.empty(max(1, verify_workspace(n_commit.numel(), target_probs.shape[1])),
-                                dtype=torch.float32, device=target_probs.device)
-    tensors = (n_commit, next_token, target_probs, draft_probs, tokens, u_accept, u_sample,
-               cu_seqlens, workspace)
-    descs = [None if n == "draft_probs" and t is None else _descriptor(t, n)
-             for t, n in zip(tensors, VERIFY_NAMES)]
-    dev = target_probs.device
-    _check_device([(n, t) for n, t in zip(VERIFY_NAMES, tensors) if t is not None], dev)
-    with torch.cuda.device(dev):
-        if stream is None:
-            stream = torch.cuda.current_stream(dev).cuda_stream
-        rc = call_raw_verify(descs, stream)
-    if rc != KDA_OK:
-        raise KdaError(rc, "kda_verify")
+        if not hasattr(n_commit, "numel"):
+            _descriptor(n_commit, "n_commit")
+        workspace = _torch.empty(max(1, verify_workspace(n_commit.numel(), target_probs.shape[1])),
+                                 dtype=_torch.float32, device=target_probs.device)
+    # no draft probabilities: any tensor holds their place, and NULL is passed
+    tensors = (n_commit, next_token, target_probs, target_probs if draft_probs is None else draft_probs,
+               tokens, u_accept, u_sample, cu_seqlens, workspace)
+    buf, at = _pack(tensors, VERIFY_NAMES, dev)
+    args = list(range(at, at + 9 * 48, 48))
+    if draft_probs is None:
+        args[3] = None
+    _call(fn, args, dev, stream, "kda_verify")
