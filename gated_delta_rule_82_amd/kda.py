@@ -238,6 +238,7 @@ ARG_NAMES = ("out", "q", "k", "v", "raw_gate", "beta_logits", "a_log", "dt_bias"
 _TENSOR = struct.Struct("=Qii4q")     # kda_tensor
 _MODE = struct.Struct("=ifffi")       # kda_mode
 assert _TENSOR.size == ctypes.sizeof(KdaTensor) and _MODE.size == ctypes.sizeof(KdaMode)
+_TENSORS = {n: struct.Struct("=" + "Qii4q" * n) for n in range(1, 20)}
 _BUFFERS = {n: ctypes.c_char * (n * _TENSOR.size + _MODE.size) for n in range(1, 20)}
 
 
@@ -254,21 +255,23 @@ def _refuse(tensors, names, dev):
 def _pack(tensors, names, dev):
     """kda_tensor descriptors of ``tensors``, all on GPU ``dev``, one behind
     the other, with room for a kda_mode.  Returns the buffer and its address."""
-    buf = _BUFFERS[len(tensors)]()
-    pack, at, size = _TENSOR.pack_into, 0, _TENSOR.size
-    for t in tensors:
-        try:
+    values = []
+    add = values.extend
+    try:
+        for t in tensors:
             shape = t.shape
             n = len(shape)
             dt = _DTYPES.get(t.dtype)
             if dt is None or n > 4 or t.get_device() != dev or not t.is_contiguous():
                 _refuse(tensors, names, dev)
-            if n < 4:
-                shape = (*shape, 0, 0, 0, 0)[:4]
-            pack(buf, at, t.data_ptr(), dt, n, *shape)
-        except AttributeError:
-            _refuse(tensors, names, dev)
-        at += size
+            if n == 4:
+                add((t.data_ptr(), dt, 4, *shape))
+            else:
+                add((t.data_ptr(), dt, n, *shape, 0, 0, 0, 0)[:7])
+    except AttributeError:
+        _refuse(tensors, names, dev)
+    buf = _BUFFERS[len(tensors)]()
+    _TENSORS[len(tensors)].pack_into(buf, 0, *values)
     return buf, ctypes.addressof(buf)
 
 
