@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kLoads = 4;      // 16-byte loads per lane and segment
 constexpr int kBlock = 256;
+constexpr int kHeld = 4;       // rounds of 64 partials that verify_pick keeps
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
@@ -41,7 +42,7 @@ constexpr int kSegment = kWave * kLoads * kVec<BF16>;
 static_assert(kSegment<false> == KDA_VERIFY_SEGMENT, "the workspace formula counts fp32 segments");
 
 // NaN, negative and infinite probabilities count as zero.
-__device__ __forceinline__ float mass(float x) { return x > 0.0f && x <= FLT_MAX ? x : 0.0f; }
+__device__ __forceinline__ float mass(float x) { return fmaxf(x <= FLT_MAX ? x : 0.0f, 0.0f); }
 
 template <bool BF16>
 __device__ __forceinline__ float load_prob(const void* base, int64_t off) {
@@ -56,13 +57,18 @@ struct Verdict {
   int64_t row;    // row to sample from
 };
 
-template <bool BF16>
-__device__ __forceinline__ Verdict judge(const VerifyArgs& a, int b, int lane) {
+__device__ __forceinline__ int window(const VerifyArgs& a, int b, int& n) {   // first row and tokens
   int t0 = a.cu_seqlens[b], t1 = a.cu_seqlens[b + 1];
   t0 = t0 < 0 ? 0 : (t0 > a.T ? a.T : t0);
   t1 = t1 < t0 ? t0 : (t1 > a.T ? a.T : t1);
+  n = t1 - t0;
+  return t0;
+}
+
+template <bool BF16>
+__device__ __forceinline__ Verdict judge(const VerifyArgs& a, int b, int lane) {
   Verdict v;
-  v.n = t1 - t0;
+  const int t0 = window(a, b, v.n);
   v.kept = v.n > 0 ? v.n - 1 : 0;
   v.fell = false;
   for (int base = 0; base < v.n - 1; base += kWave) {
@@ -86,7 +92,7 @@ __device__ __forceinline__ Verdict judge(const VerifyArgs& a, int b, int lane) {
       break;
     }
   }
-  v.row = t0 + v.kept;
+  v.row = static_cast<int64_t>(t0) + v.kept;
   return v;
 }
 
@@ -137,23 +143,36 @@ struct Row {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const double d = static_cast<double>(mass(x[e])) - static_cast<double>(mass(y[e]));
-      r[e] = t + e == gone || d < 0.0 ? 0.0 : d;
+      r[e] = fmax(d, 0.0);
+    }
+    if (gone >= t && gone < t + VEC) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (t + e == gone) r[e] = 0.0;
     }
   }
 
-  // r of the groups g, g + 64, ... of a segment (0 outside the row).
-  __device__ __forceinline__ void segment(int64_t g, double (&r)[kLoads][VEC]) const {
-    u32x4 wp[kLoads], wq[kLoads];
+  // The groups g, g + 64, ... of a segment, as loaded (groups that reach past
+  // the row are left out here).
+  struct Raw {
+    u32x4 p[kLoads], q[kLoads];
+  };
+
+  __device__ __forceinline__ void fetch(int64_t g, Raw& w) const {
 #pragma unroll
     for (int l = 0; l < kLoads; ++l) {
       const int64_t at = g + l * kWave;
-      wp[l] = u32x4{0, 0, 0, 0};
-      wq[l] = u32x4{0, 0, 0, 0};
+      w.p[l] = u32x4{0, 0, 0, 0};
+      w.q[l] = u32x4{0, 0, 0, 0};
       if (at < groups && whole(at)) {
-        wp[l] = *reinterpret_cast<const u32x4*>(p + at * 16);
-        if (q != nullptr) wq[l] = *reinterpret_cast<const u32x4*>(q + at * 16);
+        w.p[l] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + at * 16));
+        if (q != nullptr) w.q[l] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(q + at * 16));
       }
     }
+  }
+
+  // Their r (0 outside the row).
+  __device__ __forceinline__ void values(int64_t g, const Raw& w, double (&r)[kLoads][VEC]) const {
 #pragma unroll
     for (int l = 0; l < kLoads; ++l) {
       const int64_t at = g + l * kWave;
@@ -166,29 +185,49 @@ struct Row {
             d = load_prob<BF16>(p, at * VEC + e);
             if (q != nullptr) d -= load_prob<BF16>(q, at * VEC + e);
           }
-          r[l][e] = d < 0.0 ? 0.0 : d;
+          r[l][e] = fmax(d, 0.0);
         }
       } else {
-        residual(at, wp[l], wq[l], r[l]);
+        residual(at, w.p[l], w.q[l], r[l]);
       }
     }
   }
 };
 
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-  for (int m = kWave / 2; m > 0; m /= 2) x += __shfl_xor(x, m);
-  return x;
+// Moves of a double between lanes: DPP within a row of 16, row swaps across.
+template <int CTRL, bool ZERO = false>
+__device__ __forceinline__ double dpp_f64(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, 0xf, 0xf, ZERO);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, 0xf, 0xf, ZERO);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+__device__ __forceinline__ double lane_f64(double x, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(u), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), lane);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 
 // Sum of x over lanes 0 .. lane.
 __device__ __forceinline__ double wave_scan(double x, int lane) {
-#pragma unroll
-  for (int m = 1; m < kWave; m *= 2) {
-    const double y = __shfl_up(x, m);
-    if (lane >= m) x += y;
-  }
-  return x;
+  x += dpp_f64<0x111, true>(x);   // row_shr 1, 2, 4, 8: zero comes in
+  x += dpp_f64<0x112, true>(x);
+  x += dpp_f64<0x114, true>(x);
+  x += dpp_f64<0x118, true>(x);
+  const double r0 = lane_f64(x, 15), r1 = r0 + lane_f64(x, 31), r2 = r1 + lane_f64(x, 47);
+  const int row = lane / 16;
+  return x + (row == 0 ? 0.0 : row == 1 ? r0 : row == 2 ? r1 : r2);
+}
+
+// Sum over the wave; in lane 0 at least.
+__device__ __forceinline__ double wave_total(double x) {
+  x += dpp_f64<kDppXor1>(x);
+  x += dpp_f64<kDppXor2>(x);
+  x += dpp_f64<kDppRowRor4>(x);
+  x += dpp_f64<kDppRowRor8>(x);
+  return (x + lane_f64(x, 16)) + (lane_f64(x, 32) + lane_f64(x, 48));
 }
 
 __device__ __forceinline__ int64_t segments(int V, int segment) { return V / segment + 2; }
@@ -209,15 +248,21 @@ __global__ __launch_bounds__(kBlock) void verify_sum(const VerifyArgs a, int blo
   row.open(a, v);
   const int64_t nseg = segments(a.V, kSegment<BF16>);
   double* const part = static_cast<double*>(a.workspace) + b * nseg;
-  for (int64_t s = first; s < first + run && s < nseg; ++s) {
+  const int64_t end = first + run < nseg ? first + run : nseg;
+  typename Row<BF16>::Raw next;
+  row.fetch(first * (kWave * kLoads) + lane, next);   // past the row: nothing
+  for (int64_t s = first; s < end; ++s) {
+    const int64_t g = s * (kWave * kLoads) + lane;
+    const typename Row<BF16>::Raw cur = next;
+    if (s + 1 < end) row.fetch(g + kWave * kLoads, next);
     double r[kLoads][kVec<BF16>];
-    row.segment(s * (kWave * kLoads) + lane, r);
+    row.values(g, cur, r);
     double sum = 0.0;
 #pragma unroll
     for (int l = 0; l < kLoads; ++l)
 #pragma unroll
       for (int e = 0; e < kVec<BF16>; ++e) sum += r[l][e];
-    sum = wave_sum(sum);
+    sum = wave_total(sum);
     if (lane == 0) part[s] = sum;
   }
 }
@@ -228,21 +273,37 @@ __global__ __launch_bounds__(kWave) void verify_pick(const VerifyArgs a) {
   constexpr int VEC = kVec<BF16>;
   const int lane = threadIdx.x;
   const int b = blockIdx.x;
-  const Verdict v = judge<BF16>(a, b, lane);
+  // the verdict that verify_sum left
+  Verdict v;
+  const int t0 = window(a, b, v.n);
   if (v.n == 0) {
     if (lane == 0) a.next_token[b] = -1;
     return;
   }
+  v.kept = a.n_commit[b] - 1;
+  v.fell = v.kept < v.n - 1;
+  v.row = static_cast<int64_t>(t0) + v.kept;
   const int64_t nseg = segments(a.V, kSegment<BF16>);
   const double* const part = static_cast<const double*>(a.workspace) + b * nseg;
-  // the total, summed in the order in which the search below adds up
+  // the total, summed in the order in which the search below adds up; the
+  // first kHeld rounds of partials and their sums stay in registers
+  double held[kHeld], upto[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) held[i] = i * kWave + lane < nseg ? part[i * kWave + lane] : 0.0;
   double total = 0.0;
   int64_t last = -1;   // last segment with mass
-  for (int64_t s0 = 0; s0 < nseg; s0 += kWave) {
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const uint64_t some = __ballot(held[i] > 0.0);
+    if (some != 0) last = i * kWave + 63 - __clzll(static_cast<long long>(some));
+    upto[i] = wave_scan(held[i], lane);
+    total += lane_f64(upto[i], kWave - 1);
+  }
+  for (int64_t s0 = kHeld * kWave; s0 < nseg; s0 += kWave) {
     const double x = s0 + lane < nseg ? part[s0 + lane] : 0.0;
     const uint64_t some = __ballot(x > 0.0);
     if (some != 0) last = s0 + 63 - __clzll(static_cast<long long>(some));
-    total += __shfl(wave_scan(x, lane), kWave - 1);
+    total += lane_f64(wave_scan(x, lane), kWave - 1);
   }
   if (last < 0) {
     if (lane == 0) a.next_token[b] = -1;
@@ -252,25 +313,30 @@ __global__ __launch_bounds__(kWave) void verify_pick(const VerifyArgs a) {
   const double bar = (u > 0.0f ? static_cast<double>(u) : 0.0) * total;
   double before = 0.0;   // mass of the segments before `seg`
   int64_t seg = -1;
-  for (int64_t s0 = 0; s0 < nseg && seg < 0; s0 += kWave) {
-    const double x = s0 + lane < nseg ? part[s0 + lane] : 0.0;
-    const double upto = wave_scan(x, lane);
-    const uint64_t over = __ballot(before + upto > bar);
+  const auto search = [&](int64_t s0, double sums) {
+    const uint64_t over = __ballot(before + sums > bar);
     if (over != 0) {
       const int at = __ffsll(static_cast<unsigned long long>(over)) - 1;
       seg = s0 + at;
-      if (at > 0) before += __shfl(upto, at - 1);
+      if (at > 0) before += lane_f64(sums, at - 1);
     } else {
-      before += __shfl(upto, kWave - 1);
+      before += lane_f64(sums, kWave - 1);
     }
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (seg < 0) search(i * kWave, upto[i]);
+  for (int64_t s0 = kHeld * kWave; s0 < nseg && seg < 0; s0 += kWave)
+    search(s0, wave_scan(s0 + lane < nseg ? part[s0 + lane] : 0.0, lane));
   const bool passes = seg >= 0;   // else the last token with mass
   if (!passes) seg = last;
   Row<BF16> row;
   row.open(a, v);
   double r[kLoads][VEC];
   const int64_t g0 = seg * (kWave * kLoads);
-  row.segment(g0 + lane, r);
+  typename Row<BF16>::Raw raw;
+  row.fetch(g0 + lane, raw);
+  row.values(g0 + lane, raw, r);
   int64_t found = -1, tail = -1;
 #pragma unroll
   for (int l = 0; l < kLoads; ++l) {
@@ -282,8 +348,7 @@ __global__ __launch_bounds__(kWave) void verify_pick(const VerifyArgs a) {
       if (r[l][e] > 0.0) some = e;
     }
     const double upto = wave_scan(sum, lane);
-    double run = before + __shfl_up(upto, 1);
-    if (lane == 0) run = before;
+    double run = before + (upto - sum);   // may round: a token's own sum decides below
     int at = -1;     // the lane's first element past the bar
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
@@ -298,7 +363,7 @@ __global__ __launch_bounds__(kWave) void verify_pick(const VerifyArgs a) {
     }
     const uint64_t any = __ballot(some >= 0);
     if (any != 0) tail = __shfl(static_cast<int>(t + some), 63 - __clzll(static_cast<long long>(any)));
-    before += __shfl(upto, kWave - 1);
+    before += lane_f64(upto, kWave - 1);
   }
   // a segment whose own running sum rounds to the bar gives its last token
   if (lane == 0) a.next_token[b] = static_cast<int32_t>(found >= 0 ? found : tail);
@@ -307,10 +372,11 @@ __global__ __launch_bounds__(kWave) void verify_pick(const VerifyArgs a) {
 template <bool BF16>
 hipError_t launch(const VerifyArgs& args, hipStream_t stream) {
   const int64_t nseg = args.V / kSegment<BF16> + 2;
-  // segments per wave: enough waves for the chip first, then fewer waves
-  // that share the walk over the drafts
+  // Segments per wave: waves for the chip first, then fewer of them, which
+  // share the walk over the drafts.  256 requests over 131072 fp32 tokens, us
+  // with at least 2048 / 8192 / 16384 / 65536 waves: 54.0 / 49.2 / 51.3 / 59.9.
   int run = 1;
-  while (run < 8 && static_cast<int64_t>(args.B) * nseg / (2 * run) >= 4096) run *= 2;
+  while (run < 8 && static_cast<int64_t>(args.B) * nseg / (2 * run) >= 8192) run *= 2;
   const int64_t per_block = static_cast<int64_t>(kBlock / kWave) * run;
   int blocks = static_cast<int>((nseg + per_block - 1) / per_block);
   void* sum_args[] = {const_cast<VerifyArgs*>(&args), &blocks, &run};
