@@ -38,7 +38,8 @@ HIP_FLAGS = [
 # elementwise work reads and scales them every chunk, and with accumulators
 # in AGPRs every such access costs a copy (measured 5-8% faster this way).
 EXTRA_FLAGS = {"kda_prefill": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-               "kda_gdr_prefill": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+               "kda_gdr_prefill": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               "kda_window": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _hipcc() -> str:

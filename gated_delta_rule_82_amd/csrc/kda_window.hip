@@ -26,12 +26,15 @@
 // rows rsub + RPI i and EPL keys.
 //
 // Bound: the state's trip from HBM and back.  With one token a wave is almost
-// all state traffic; with windows the two sweeps per token (2 + 1 FMA per
-// element) come into view.
+// all state traffic (96 heads x 256 requests, fp32 pool: 535 us, 6.0 TB/s);
+// with windows the two sweeps per token (2 + 1 FMA per element) come into
+// view, and long ones with one decay per head go 8 tokens at a time
+// (window_chunk below).
 
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "kda.h"
 #include "kda_device.h"
@@ -492,8 +495,364 @@ __global__ __launch_bounds__(kWave) void window_vfirst(const WindowArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// windows of several tokens with one decay per head: up to 8 tokens at once
+// ---------------------------------------------------------------------------
+
+// With a scalar decay a window needs the state only through kh_i^T S0 and
+// qh_i^T S0 (G_i: the log decay summed from the window's start):
+//   U_i = beta_i (v_i - e^(G_i) kh_i^T S0 - sum_{j<i} e^(G_i - G_j) kh_i.kh_j U_j)
+//   o_i = e^(G_i) qh_i^T S0 + sum_{j<=i} e^(G_i - G_j) qh_i.kh_j U_j
+//   S'  = e^(G_last) S0 + sum_j e^(G_last - G_j) kh_j U_j^T
+// So the sweeps over S are matrix products of 8 rows of k and 8 of q against
+// the slab, on the fp32 matrix instruction (exact products of the raw values;
+// norms and decays are factors of rows), which run beside the loads and
+// leave the vector units with the small triangular solve: about 500
+// instructions for up to 8 tokens against 330 for each one.
+//
+// A lane holds value columns n = lane % 16 (NCS neighbours) and keys 32 s + 8 g
+// + 4 b + 0..3 (g = lane / 16): the accumulator layout of the update, the second
+// operand of the products, and 16-byte pieces of a value-first row.
+
+constexpr int kW = 8;   // tokens at once
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+template <int DK, int CW>
+struct ChunkTables {
+  float dots[2 * kW][CW];     // k_i^T S0, q_i^T S0 of the raw rows
+  float u[kW][CW];            // e^(G_last - G_j) norm_k U_j
+  float k[kW][DK + 4];        // raw k
+  float coef[2 * kW][kW];     // of U_j in U_i, and in o_i
+  float row[2 * kW];          // norm factors of the rows of k, and of q (times scale)
+  float g_hi[kW], g_lo[kW], beta[kW];
+  float lead[2 * kW];         // factor of dots[i]
+  float tail[kW];             // e^(G_last - G_j) norm_k
+  float last;                 // e^(G_last)
+};
+
+// exp(G_i - G_j) from two-float sums.
+__device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float lo_j) {
+  return exp_f((hi_i - hi_j) + (lo_i - lo_j));
+}
+
+__device__ __forceinline__ double row_shr_f64(double x, int by) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const int lo = static_cast<int>(u), hi = static_cast<int>(u >> 32);
+  uint32_t l, h;
+  if (by == 1) {
+    l = __builtin_amdgcn_update_dpp(0, lo, 0x111, 0xf, 0xf, true);
+    h = __builtin_amdgcn_update_dpp(0, hi, 0x111, 0xf, 0xf, true);
+  } else if (by == 2) {
+    l = __builtin_amdgcn_update_dpp(0, lo, 0x112, 0xf, 0xf, true);
+    h = __builtin_amdgcn_update_dpp(0, hi, 0x112, 0xf, 0xf, true);
+  } else {
+    l = __builtin_amdgcn_update_dpp(0, lo, 0x114, 0xf, 0xf, true);
+    h = __builtin_amdgcn_update_dpp(0, hi, 0x114, 0xf, 0xf, true);
+  }
+  return __builtin_bit_cast(double, static_cast<uint64_t>(h) << 32 | l);
+}
+
+// Orders the wave's LDS accesses (one wave is the whole workgroup).
+__device__ __forceinline__ void lds_sync() { __syncthreads(); }
+
+template <int DK, int DV, bool QBF16, bool SBF16, int LAYOUT>
+__global__ __launch_bounds__(kWave) void window_chunk(const WindowArgs a) {
+  constexpr int CW = DV < 32 ? DV : 32;
+  constexpr int SLABS = DV / CW;
+  constexpr int NCS = CW / 16;
+  constexpr int KS = DK / 32;
+  constexpr int E = SBF16 ? 2 : 4;
+  __shared__ __attribute__((aligned(16))) ChunkTables<DK, CW> sh;
+
+  const int lane = threadIdx.x;
+  const int n16 = lane % 16, g = lane / 16;
+  const Job j = resolve<SLABS>(a);
+  if (j.slot < 0 || j.slot >= a.N) {
+    zero_rows<DV, CW, QBF16>(a, j, lane);
+    return;
+  }
+  const int total = j.n[0] + j.n[1];
+  if (total == 0) return;
+
+  // ---- the slab ----
+  char* const tile = static_cast<char*>(a.state_pool) +
+                     (static_cast<int64_t>(j.slot) * a.HV + j.hv) * (DK * DV * E);
+  const __amdgpu_buffer_rsrc_t res = tile_resource(tile, DK * DV * E);
+  f32x4 S[KS][2][NCS];
+  const int col = j.slab * CW + NCS * n16;
+  const auto slab_io = [&](auto store) {
+    constexpr bool STORE = decltype(store)::value;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      if constexpr (LAYOUT == KDA_STATE_V_FIRST) {
+#pragma unroll
+        for (int cs = 0; cs < NCS; ++cs) {
+          const int voff = ((col + cs) * DK + 8 * g) * E;
+          float x[8] = {S[s][0][cs][0], S[s][0][cs][1], S[s][0][cs][2], S[s][0][cs][3],
+                        S[s][1][cs][0], S[s][1][cs][1], S[s][1][cs][2], S[s][1][cs][3]};
+          if constexpr (SBF16) {
+            if constexpr (STORE) StateIO<true, 8>::store(res, voff, 32 * s * E, x);
+            else StateIO<true, 8>::load(res, voff, 32 * s * E, x);
+          } else {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              if constexpr (STORE) StateIO<false, 4>::store(res, voff, (32 * s + 4 * b) * E, x + 4 * b);
+              else StateIO<false, 4>::load(res, voff, (32 * s + 4 * b) * E, x + 4 * b);
+            }
+          }
+          if constexpr (!STORE) {
+            S[s][0][cs] = f32x4{x[0], x[1], x[2], x[3]};
+            S[s][1][cs] = f32x4{x[4], x[5], x[6], x[7]};
+          }
+        }
+      } else {
+        const int voff = (8 * g * DV + col) * E;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int soff = (32 * s + 4 * b + r) * DV * E;
+            if constexpr (STORE) {
+              if constexpr (SBF16 && NCS == 2)
+                __builtin_amdgcn_raw_buffer_store_b32(f32x2_to_bf16x2_rne(S[s][b][0][r], S[s][b][1][r]), res, voff, soff, 0);
+              else if constexpr (SBF16)
+                __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(f32_to_bf16_rne(S[s][b][0][r])), res, voff, soff, 0);
+              else if constexpr (NCS == 2)
+                __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(S[s][b][0][r]), __float_as_uint(S[s][b][1][r])},
+                                                      res, voff, soff, kCachePolicyNT);
+              else
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[s][b][0][r]), res, voff, soff, 0);
+            } else if constexpr (SBF16 && NCS == 2) {
+              const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(res, voff, soff, 0);
+              S[s][b][0][r] = bf16_to_f32(w & 0xffffu);
+              S[s][b][1][r] = __uint_as_float(w & 0xffff0000u);
+            } else if constexpr (SBF16) {
+              S[s][b][0][r] = bf16_to_f32(__builtin_amdgcn_raw_buffer_load_b16(res, voff, soff, 0));
+            } else if constexpr (NCS == 2) {
+              const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(res, voff, soff, kCachePolicyNT);
+              S[s][b][0][r] = __uint_as_float(w.x);
+              S[s][b][1][r] = __uint_as_float(w.y);
+            } else {
+              S[s][b][0][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(res, voff, soff, 0));
+            }
+          }
+      }
+    }
+  };
+  slab_io(std::false_type{});
+
+  const float amp = exp_f(a.a_log[j.hv]);
+  const float bias = a.dt_bias[j.hv];
+  const int c = lane % CW;                       // the lane's column in the solve
+  constexpr int SHARE = kWave / CW;              // lanes that solve a column; each stores kW / SHARE outputs
+  const int part = lane / CW;
+
+  for (int done = 0; done < total;) {
+    const int st = done >= j.n[0];               // stream
+    const TokenStream& src = a.src[st];
+    const int left = (st ? total : j.n[0]) - done;
+    const int n = left < kW ? left : kW;
+    const int64_t t0 = j.first[st] + (st ? done - j.n[0] : done);
+    const bool outputs = st == a.window;
+    const bool updates = st == 0 || done + n < total;
+
+    // ---- this chunk's rows: lane row n16 (k 0..7, q 8..15), keys 32 s + 8 g + 0..7 ----
+    const int tok = n16 % kW;
+    const bool live_row = tok < n && (n16 < kW || outputs);
+    const void* const base = n16 < kW || !outputs ? src.k : src.q;
+    const int64_t off = ((t0 + (live_row ? tok : 0)) * a.H + j.h) * DK + 8 * g;
+    u32x4 xw[KS][QBF16 ? 1 : 2];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      if constexpr (QBF16) {
+        xw[s][0] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + off + 32 * s);
+      } else {
+        xw[s][0] = *reinterpret_cast<const u32x4*>(static_cast<const float*>(base) + off + 32 * s);
+        xw[s][1] = *reinterpret_cast<const u32x4*>(static_cast<const float*>(base) + off + 32 * s + 4);
+      }
+    }
+    const int gt = lane % kW;
+    const int64_t goff = (t0 + (gt < n ? gt : 0)) * a.HV + j.hv;
+    const float gate = src.raw_gate[goff];
+    const float bl = src.beta_logits[goff];
+    RawRun<QBF16, 1> vw[kW];
+#pragma unroll
+    for (int i = 0; i < kW; ++i)
+      vw[i].load(src.v, ((t0 + (i < n ? i : 0)) * a.HV + j.hv) * DV + j.slab * CW + c);
+
+    // ---- gates: G summed over the 8 lanes of a group of tokens, in fp64 ----
+    {
+      const float x = gate + bias;
+      float gv = a.gate_mode == KDA_GATE_SOFTPLUS ? -amp * softplus_f(x) : a.lower_bound * sigmoid_f(amp * x);
+      gv = gv < -200.0f ? -200.0f : gv;   // exp(-200) is 0 in fp32, and sums stay finite
+      double sum = gt < n ? static_cast<double>(gv) : 0.0;
+      sum += row_shr_f64(sum, 1);
+      sum += row_shr_f64(sum, 2);
+      sum += row_shr_f64(sum, 4);
+      if (lane < kW) {
+        const float hi = static_cast<float>(sum);
+        sh.g_hi[gt] = hi;
+        sh.g_lo[gt] = static_cast<float>(sum - static_cast<double>(hi));
+        sh.beta[gt] = gt < n ? sigmoid_f(bl) : 0.0f;
+      }
+    }
+
+    // ---- rows: norms, k to LDS ----
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int h = 0; h < (QBF16 ? 1 : 2); ++h)
+        if (!live_row) xw[s][h] = u32x4{0, 0, 0, 0};
+    const auto key_value = [&](int s, int e) {   // key 32 s + 8 g + e
+      if constexpr (QBF16) return e % 2 ? __uint_as_float(xw[s][0][e / 2] & 0xffff0000u) : __uint_as_float(xw[s][0][e / 2] << 16);
+      else return __uint_as_float(xw[s][e / 4][e % 4]);
+    };
+    float sq = 0.0f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sq = fmaf(key_value(s, e), key_value(s, e), sq);
+    sq = swap16_add(sq, sq);
+    sq = swap32_add(sq, sq);
+    if (lane < 2 * kW) sh.row[n16] = (n16 < kW ? 1.0f : a.scale) * rsqrt_f(sq + a.l2_eps);
+    if (n16 < kW && updates) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<f32x4*>(&sh.k[n16][32 * s + 8 * g + 4 * h]) =
+              f32x4{key_value(s, 4 * h), key_value(s, 4 * h + 1), key_value(s, 4 * h + 2), key_value(s, 4 * h + 3)};
+    }
+
+    // ---- Gram matrix of the rows: column n16, rows 4 g + 0..3 ----
+    f32x4 gram = {0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      if constexpr (QBF16) {
+        const bf16x8 x = __builtin_bit_cast(bf16x8, xw[s][0]);
+        gram = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, x, gram, 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          gram = __builtin_amdgcn_mfma_f32_16x16x4f32(key_value(s, e), key_value(s, e), gram, 0, 0, 0);
+      }
+    }
+
+    // ---- rows against the slab ----
+    f32x4 dots[NCS];
+#pragma unroll
+    for (int cs = 0; cs < NCS; ++cs) dots[cs] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int cs = 0; cs < NCS; ++cs)
+          dots[cs] = __builtin_amdgcn_mfma_f32_16x16x4f32(key_value(s, e), S[s][e / 4][cs][e % 4], dots[cs], 0, 0, 0);
+
+    lds_sync();
+    // ---- factors ----
+    if (lane < 2 * kW) {
+      const float gh = sh.g_hi[tok], gl = sh.g_lo[tok];
+      const float eg = exp_f(gh + gl);
+      sh.lead[n16] = eg * sh.row[n16] * (n16 < kW ? sh.beta[tok] : 1.0f);
+      if (n16 < kW) sh.tail[tok] = sh.row[n16] * decay(sh.g_hi[kW - 1], sh.g_lo[kW - 1], gh, gl);
+      if (n16 == kW - 1) sh.last = eg;
+    }
+    if (n16 < kW) {
+      const float gh = sh.g_hi[n16], gl = sh.g_lo[n16], nk = sh.row[n16];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 4 * g + r, i = row % kW;
+        const float f = nk * sh.row[row] * decay(sh.g_hi[i], sh.g_lo[i], gh, gl) * gram[r];
+        sh.coef[row][n16] = row < kW ? (n16 < i ? f * sh.beta[i] : 0.0f) : (n16 <= i ? f : 0.0f);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if constexpr (NCS == 2) *reinterpret_cast<float2*>(&sh.dots[4 * g + r][2 * n16]) = make_float2(dots[0][r], dots[1][r]);
+      else sh.dots[4 * g + r][n16] = dots[0][r];
+    }
+    lds_sync();
+
+    // ---- the solve, one column per lane ----
+    float U[kW];
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+      float v[1];
+      vw[i].unpack(v);
+      float acc = i < n ? fmaf(sh.beta[i], v[0], -sh.lead[i] * sh.dots[i][c]) : 0.0f;
+#pragma unroll
+      for (int k = 0; k < i; ++k) acc = fmaf(-sh.coef[i][k], U[k], acc);
+      U[i] = acc;
+    }
+    if (outputs) {
+#pragma unroll
+      for (int i = 0; i < kW; ++i) {
+        float o = sh.lead[kW + i] * sh.dots[kW + i][c];
+#pragma unroll
+        for (int k = 0; k <= i; ++k) o = fmaf(sh.coef[kW + i][k], U[k], o);
+        if (i < n && i / (kW / SHARE) == part)
+          store_scalar<QBF16>(a.out, ((t0 + i) * a.HV + j.hv) * DV + j.slab * CW + c, o);
+      }
+    }
+    // ---- S' ----
+    if (updates) {
+      if (part == 0) {
+#pragma unroll
+        for (int i = 0; i < kW; ++i) sh.u[i][c] = U[i] * sh.tail[i];
+      }
+      lds_sync();
+      const float last = sh.last;
+      float ub[2][NCS];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int cs = 0; cs < NCS; ++cs) ub[h][cs] = sh.u[4 * h + g][NCS * n16 + cs];
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int key = 32 * s + 8 * (n16 / 4) + 4 * b + n16 % 4;
+          const float k0 = sh.k[g][key], k1 = sh.k[4 + g][key];
+#pragma unroll
+          for (int cs = 0; cs < NCS; ++cs) {
+            f32x4 acc = S[s][b][cs] * last;
+            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(k0, ub[0][cs], acc, 0, 0, 0);
+            S[s][b][cs] = __builtin_amdgcn_mfma_f32_16x16x4f32(k1, ub[1][cs], acc, 0, 0, 0);
+          }
+        }
+    }
+    done += n;
+    if (st == 0 && done == j.n[0]) slab_io(std::true_type{});
+    lds_sync();
+  }
+}
+
+// ---------------------------------------------------------------------------
 // dispatch
 // ---------------------------------------------------------------------------
+
+// Tokens per request from which a window goes 8 tokens at a time
+// (window_chunk) rather than token by token.  dk = dv = 128, bf16 q, k, v, us
+// token by token / 8 at a time, for 2, 4 and 8 tokens per request over 96
+// heads x 256 requests:
+//   decode  f32 key-first      544 / 556    550 / 562    612 / 598
+//           f32 value-first    559 / 682    558 / 684    618 / 732
+//           bf16 key-first     337 / 352    361 / 370    533 / 403
+//           bf16 value-first   285 / 411    328 / 399    527 / 427
+//   window  f32 key-first      542 / 580    569 / 602    786 / 643
+//           f32 value-first    559 / 693    579 / 721    848 / 783
+//           bf16 key-first     351 / 471    466 / 482    743 / 513
+//           bf16 value-first   310 / 498    456 / 512    755 / 540
+// A value-first slab is read in 64-byte pieces of 16 rows there (256 or 512
+// bytes of a row here), which costs 20% of an fp32 pool's streaming rate.
+// One request of 32 heads: 10.3 / 6.9 us at 8 tokens, 4.5 / 6.4 at 2.
+template <bool SBF16, int LAYOUT>
+constexpr int64_t chunk_from(int window) {
+  if (!SBF16 && LAYOUT == KDA_STATE_V_FIRST) return window ? 7 : 12;
+  return window ? 5 : 6;
+}
 
 template <int DK, int DV, bool QBF16, bool SBF16, int LAYOUT>
 hipError_t launch_one(const WindowArgs& args, hipStream_t stream) {
@@ -502,6 +861,10 @@ hipError_t launch_one(const WindowArgs& args, hipStream_t stream) {
   void* kargs[] = {const_cast<WindowArgs*>(&args)};
   const void* fn = LAYOUT == KDA_STATE_K_FIRST ? reinterpret_cast<const void*>(&window_kfirst<DK, DV, QBF16, SBF16>)
                                                : reinterpret_cast<const void*>(&window_vfirst<DK, DV, QBF16, SBF16>);
+  if constexpr (!kChannel && DK >= 32) {
+    if (static_cast<int64_t>(args.src[args.window].T) >= chunk_from<SBF16, LAYOUT>(args.window) * args.B)
+      fn = reinterpret_cast<const void*>(&window_chunk<DK, DV, QBF16, SBF16, LAYOUT>);
+  }
   return hipLaunchKernel(fn, dim3(static_cast<uint32_t>(nwg)), dim3(kWave), kargs, 0, stream);
 }
 

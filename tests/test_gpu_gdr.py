@@ -147,6 +147,29 @@ def test_window(torch_cuda, dk, dv, qkv, layout, state, channel):
         state=state, channel=channel)
 
 
+# windows long enough (on average) to go several tokens at a time, with
+# requests of one token, of none and of whole and broken groups of 8
+LONG = [8, 33, 3, 0, 17, 9, 1, 40]
+LONG_REPLAYS = [(0, 9), (3, 1), (0, 0), (2, 8), (5, 17), (1, 3), (0, 16), (4, 2)]
+
+
+@pytest.mark.parametrize("state", ["f32", "bf16"])
+@pytest.mark.parametrize("qkv", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 128), (128, 64), (32, 32), (32, 16), (64, 16), (16, 32)])
+def test_long_decode(torch_cuda, dk, dv, layout, qkv, state):
+    run(torch_cuda, "decode", f"long {dk}x{dv}", LONG, dk=dk, dv=dv, layout=layout, qkv=qkv, state=state)
+
+
+@pytest.mark.parametrize("state", ["f32", "bf16"])
+@pytest.mark.parametrize("qkv", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 16), (32, 64)])
+def test_long_window(torch_cuda, dk, dv, layout, qkv, state):
+    run(torch_cuda, "window", f"long {dk}x{dv}", LONG, replay=LONG_REPLAYS, dk=dk, dv=dv, layout=layout, qkv=qkv,
+        state=state)
+
+
 @pytest.mark.parametrize("entry", ["decode", "window"])
 @pytest.mark.parametrize("H,HV", [(1, 1), (3, 3), (1, 6), (5, 15)])
 @pytest.mark.parametrize("layout", LAYOUTS)
@@ -165,6 +188,9 @@ def test_skipped_empty_and_clamped_requests(torch_cuda, layout, channel):
         replay=[(0, 2), (2, 3), (1, 1), (0, 0), (0, 0), (4, 1)], layout=layout, channel=channel)
     if not channel:
         run(torch_cuda, "decode", "skips", [2, 0, 1, 3, 0, 1], slots=slots, layout=layout)
+        run(torch_cuda, "decode", "long skips", [20, 0, 30, 35, 0, 11], slots=slots, layout=layout)
+        run(torch_cuda, "window", "long skips", [20, 0, 30, 35, 0, 11], slots=slots,
+            replay=[(0, 2), (2, 3), (1, 1), (0, 0), (0, 0), (4, 10)], layout=layout)
 
 
 def test_replay_only_batch(torch_cuda):
@@ -192,8 +218,9 @@ def test_degenerate(torch_cuda, entry, layout, kind):
             b.tok.beta[:] = np.float32(-120)
     else:
         kw = dict(l2_eps=0.5, scale=3.0)
-    run(torch_cuda, entry, kind, [5, 1, 7], layout=layout, edit=edit,
-        replay=[(0, 4), (2, 2), (1, 0)] if entry == "window" else None, **kw)
+    for lens in ([5, 1, 7], [30, 9, 12]):   # token by token, and several at a time
+        run(torch_cuda, entry, kind, lens, layout=layout, edit=edit,
+            replay=[(0, 4), (2, 2), (1, 0)] if entry == "window" else None, **kw)
 
 
 def test_many_tokens_match_single_token_calls(torch_cuda):
