@@ -431,14 +431,13 @@ int kda_gdr_prefill(const kda_tensor* out, const kda_tensor* q, const kda_tensor
   if (plan.dk < 32 || plan.dv < 32) return KDA_ERR_UNSUPPORTED;
   // 512 work-items per (request, value head) where there are many
   if (product_exceeds({plan.args.B, plan.args.HV, 512}, kMaxWorkItems)) return KDA_ERR_UNSUPPORTED;
+  // token numbers of a last chunk stay within 32 bits
+  if (plan.args.T > std::numeric_limits<int32_t>::max() - 64) return KDA_ERR_UNSUPPORTED;
   // a chunk of 32 rows is addressed with 31-bit byte offsets
   if (product_exceeds({32, plan.args.HV, plan.dk > plan.dv ? plan.dk : plan.dv, 4},
                       std::numeric_limits<int32_t>::max()))
     return KDA_ERR_UNSUPPORTED;
   if (plan.empty) return KDA_OK;
-  if (plan.dk == 128 && !plan.qkv_bf16)
-    return kda::launch_window(window_args(plan, 0), plan.dk, plan.dv, plan.qkv_bf16, plan.state_bf16,
-                              plan.layout, false, stream);
   return kda::launch_gdr_prefill(plan.args, plan.dk, plan.dv, plan.qkv_bf16, plan.state_bf16, plan.layout,
                                  stream);
 }

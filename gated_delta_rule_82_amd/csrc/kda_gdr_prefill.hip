@@ -1,5 +1,6 @@
 // kda_gdr_prefill.hip - the gated delta rule over whole prompts, in chunks
-// of 32 tokens on the matrix cores (kda_gdr_prefill).
+// of 32 tokens (16 for fp32 rows of 128 keys) on the matrix cores
+// (kda_gdr_prefill).
 //
 // Mathematics.  One decay per token and head, G_i its log summed from the
 // chunk's start, S0 the state before the chunk:
@@ -49,6 +50,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "kda.h"
 #include "kda_device.h"
@@ -58,7 +60,6 @@
 namespace kda {
 namespace {
 
-constexpr int kC = 32;            // tokens per chunk
 constexpr int kHelpers = 4;
 constexpr int kRing = 4;          // chunks of q and k held in LDS
 constexpr int kRingP = 3;         // of P, made a chunk later
@@ -74,8 +75,17 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// Blocks of 16 tokens in a chunk: 32 tokens, and 16 where fp32 rows of 128 keys
+// (hi and lo) would need twice the LDS.
+template <int DK, bool F32>
+constexpr int kBlocks = F32 && DK == 128 ? 1 : 2;
+
 __device__ __forceinline__ f32x4 mfma(h8 a, h8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x4 mfma(h4 a, h4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x16f16(a, b, c, 0, 0, 0);
 }
 
 // x * s as hi + lo in fp16 (s a power of two).  The packed hi is made opaque
@@ -105,6 +115,22 @@ __device__ __forceinline__ void split8(const f32x4& x, const f32x4& y, float one
   }
   hi = h8{h[0].x, h[0].y, h[1].x, h[1].y, h[2].x, h[2].y, h[3].x, h[3].y};
   lo = h8{l[0].x, l[0].y, l[1].x, l[1].y, l[2].x, l[2].y, l[3].x, l[3].y};
+}
+
+// A chunk's rows (NB accumulators) as an operand over its tokens.
+__device__ __forceinline__ void split_rows(const f32x4 (&x)[2], float one, h8& hi, h8& lo) {
+  split8(x[0], x[1], one, hi, lo);
+}
+
+__device__ __forceinline__ void split_rows(const f32x4 (&x)[1], float one, h4& hi, h4& lo) {
+  h2 h[2], l[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    h[i] = h2{static_cast<_Float16>(x[0][2 * i]), static_cast<_Float16>(x[0][2 * i + 1])};
+    l[i] = low_part(x[0][2 * i], x[0][2 * i + 1], one, h[i]);
+  }
+  hi = h4{h[0].x, h[0].y, h[1].x, h[1].y};
+  lo = h4{l[0].x, l[0].y, l[1].x, l[1].y};
 }
 
 // The unit of a state column is 2^sig.  Moves it so that `bound`, a bound on
@@ -167,16 +193,19 @@ template <int DK, bool F32>
 struct Shared {
   static constexpr int KS = DK / 32;       // 32-key steps
   static constexpr int TERMS = F32 ? 2 : 1;
-  _Float16 k[kRing][TERMS][2][KS][64][8];          // K rows: [token block][key step]
-  _Float16 q[kRing][TERMS][2][KS][64][8];
-  _Float16 kt[kRing][TERMS][DK / 16][64][8];       // K^T: [key block], k = token
-  _Float16 p[kRingP][2][2][64][8];                 // P hi, lo: [token block]
-  _Float16 t[2][2][2][64][8];                      // T hi, lo, beta included
-  float a[2][3][16][16];                           // A: blocks 00, 11, 10; row-major
-  float join[2][16][16];                           // diagonal blocks of (I + A)^-1, row-major
-  float norm_k[2][kC], norm_q[2][kC];              // kh = norm_k * stored row
-  float g_hi[2][kC], g_lo[2][kC], beta[2][kC];
-  float tab[kRing][4][kC];                         // beta; e^G norm_k; scale e^G norm_q; norm_k e^(last - G)
+  static constexpr int NB = kBlocks<DK, F32>;
+  static constexpr int C = 16 * NB;
+  static constexpr int TK = 4 * NB;        // a lane's positions of an operand over tokens
+  _Float16 k[kRing][TERMS][NB][KS][64][8];         // K rows: [token block][key step]
+  _Float16 q[kRing][TERMS][NB][KS][64][8];
+  _Float16 kt[kRing][TERMS][DK / 16][64][TK];      // K^T: [key block], k = token
+  _Float16 p[kRingP][2][NB][64][TK];               // P hi, lo: [token block]
+  _Float16 t[2][2][NB][64][TK];                    // T hi, lo, beta included
+  float a[2][2 * NB - 1][16][16];                  // A: blocks 00, 11, 10; row-major
+  float join[NB][16][16];                          // diagonal blocks of (I + A)^-1, row-major
+  float norm_k[2][C], norm_q[2][C];                // kh = norm_k * stored row
+  float g_hi[2][C], g_lo[2][C], beta[2][C];
+  float tab[kRing][4][C];                          // beta; e^G norm_k; scale e^G norm_q; norm_k e^(last - G)
   float last[kRing];                               // e^(G_last)
 };
 
@@ -188,27 +217,30 @@ struct Shared {
 // bytes, `n` of them (n >= 1).  Loads past the last row give zero and stores
 // are dropped by the hardware's range check, so a chunk's tail needs no masks;
 // all offsets are in the vector offset, which the check covers.
+template <int C>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_resource(const void* base, int64_t offset, int n, int stride,
                                                                 int row) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(base)) + offset,
-                                           static_cast<short>(0), ((n < kC ? n : kC) - 1) * stride + row,
+                                           static_cast<short>(0), ((n < C ? n : C) - 1) * stride + row,
                                            kRawBufferWord3);
 }
 
 // A lane holds 8 channels of TL tokens: dk / 8 lanes cover a token, and lane
 // group q of them has operand positions P = q TL .. q TL + TL - 1, where
-// position P = 8 g + p is token 4 g + p % 4 + 16 (p / 4).
+// position P = TK g + p is token 4 g + p % 4 + 16 (p / 4) (TK = 8, or 4 with
+// one block of tokens).
 template <int DK, bool F32>
 struct RowLoader {
   static constexpr int LANES = DK / 8;
-  static constexpr int TL = DK / 16;
+  static constexpr int TK = 4 * kBlocks<DK, F32>;
+  static constexpr int TL = TK * LANES / 16;
   static constexpr int WORDS = F32 ? 2 : 1;
   u32x4 w[TL][WORDS];
 
   static __device__ __forceinline__ int position(int lane) { return (lane / LANES) * TL; }
   static __device__ __forceinline__ int token(int lane) {   // of the lane's first position
     const int P = position(lane);
-    return 4 * (P / 8) + P % 4 + 16 * ((P / 4) % 2);
+    return 4 * (P / TK) + P % 4 + 16 * (P % TK / 4);
   }
   static constexpr __device__ int step(int i) { return i % 4 + 16 * (i / 4); }   // token i's distance from it
 
@@ -267,7 +299,8 @@ __device__ __forceinline__ float row_factor(float square, float l2_eps) {
 // (norm[token] * stored row = unit row), and for k the transposed operand.
 template <int DK, bool F32, bool KT>
 __device__ __forceinline__ void convert_rows(const RowLoader<DK, F32>& in, float l2_eps, int lane,
-                                             _Float16 (*rows)[2][DK / 32][64][8], _Float16 (*kt)[DK / 16][64][8],
+                                             _Float16 (*rows)[kBlocks<DK, F32>][DK / 32][64][8],
+                                             _Float16 (*kt)[DK / 16][64][4 * kBlocks<DK, F32>],
                                              float* norm) {
   using L = RowLoader<DK, F32>;
   constexpr int TL = L::TL;
@@ -318,17 +351,18 @@ __device__ __forceinline__ void convert_rows(const RowLoader<DK, F32>& in, float
   if constexpr (KT) {
     typedef _Float16 run __attribute__((ext_vector_type(TL)));
     const int P = L::position(lane);
+    constexpr int TK = L::TK;
 #pragma unroll
     for (int ch = 0; ch < 8; ++ch) {
       const int cc = c + ch;
       run v;
 #pragma unroll
       for (int i = 0; i < TL; ++i) v[i] = hi[i][ch / 2][ch % 2];
-      *reinterpret_cast<run*>(&kt[0][cc / 16][kt_slot(cc / 16, P / 8, cc % 16)][P % 8]) = v;
+      *reinterpret_cast<run*>(&kt[0][cc / 16][kt_slot(cc / 16, P / TK, cc % 16)][P % TK]) = v;
       if constexpr (F32) {
 #pragma unroll
         for (int i = 0; i < TL; ++i) v[i] = lo[i][ch / 2][ch % 2];
-        *reinterpret_cast<run*>(&kt[1][cc / 16][kt_slot(cc / 16, P / 8, cc % 16)][P % 8]) = v;
+        *reinterpret_cast<run*>(&kt[1][cc / 16][kt_slot(cc / 16, P / TK, cc % 16)][P % TK]) = v;
       }
     }
   }
@@ -461,6 +495,10 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
   constexpr int NC = NCW * 16 * NCS;   // columns of the workgroup
   constexpr int TERMS = F32 ? 2 : 1;
   using Sh = Shared<DK, F32>;
+  constexpr int NB = Sh::NB;           // blocks of 16 tokens
+  constexpr int C = Sh::C;             // tokens per chunk
+  constexpr int M = 2 * NB - 1;        // blocks of the lower triangle
+  using ht = std::conditional_t<NB == 2, h8, h4>;   // an operand over tokens
   extern __shared__ __attribute__((aligned(16))) char lds[];
   Sh& sh = *reinterpret_cast<Sh*>(lds);
 
@@ -494,7 +532,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
     return;
   }
   if (w.n == 0) return;
-  const int chunks = (w.n + kC - 1) / kC;
+  const int chunks = (w.n + C - 1) / C;
   constexpr int E = F32 ? 4 : 2;
   // Waves i and i + 4 share a SIMD.  With fewer than four state waves they get
   // SIMDs of their own and the helpers share the others.
@@ -503,10 +541,12 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
   const int cw = NCW == 1 ? 0 : NCW == 2 ? wave - 2 : wave;
 
   // the upper blocks of P and T stay zero
-  for (int i = threadIdx.x; i < kRingP * 2 * 64; i += blockDim.x)
-    *reinterpret_cast<h4*>(&sh.p[i / 128][(i / 64) % 2][0][i % 64][4]) = h4{0, 0, 0, 0};
-  for (int i = threadIdx.x; i < 2 * 2 * 64; i += blockDim.x)
-    *reinterpret_cast<h4*>(&sh.t[i / 128][(i / 64) % 2][0][i % 64][4]) = h4{0, 0, 0, 0};
+  if constexpr (NB == 2) {
+    for (int i = threadIdx.x; i < kRingP * 2 * 64; i += blockDim.x)
+      *reinterpret_cast<h4*>(&sh.p[i / 128][(i / 64) % 2][0][i % 64][4]) = h4{0, 0, 0, 0};
+    for (int i = threadIdx.x; i < 2 * 2 * 64; i += blockDim.x)
+      *reinterpret_cast<h4*>(&sh.t[i / 128][(i / 64) % 2][0][i % 64][4]) = h4{0, 0, 0, 0};
+  }
 
   if (role == 0 || role == 1) {
     // ---- helpers 0 and 1: k / q rows of chunk it + 3, and with q the gates ----
@@ -515,16 +555,16 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
     const int stride = a.H * DK * E;
     const int voff = L::token(lane) * stride + 8 * (lane % L::LANES) * E;
     auto chunk_rows = [&](int c) {
-      return rows_resource(src, ((static_cast<int64_t>(t0) + c * kC) * a.H + w.h) * (DK * E), w.n - c * kC, stride,
+      return rows_resource<C>(src, ((static_cast<int64_t>(t0) + c * C) * a.H + w.h) * (DK * E), w.n - c * C, stride,
                            DK * E);
     };
     L raw;
     raw.load(chunk_rows(0), voff, stride);
     const float amp = exp_f(a.a_log[w.hv]);
     const float bias = a.dt_bias[w.hv];
-    const int tl = lane % kC;
+    const int tl = lane % C;
     auto gate_at = [&](int c) {   // raw gate and beta logit of the lane's token
-      const int t = c * kC + tl;
+      const int t = c * C + tl;
       const int64_t off = (static_cast<int64_t>(t0) + (t < w.n ? t : 0)) * a.HV + w.hv;
       return make_float2(a.raw_gate[off], a.beta_logits[off]);
     };
@@ -545,7 +585,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
           convert_rows<DK, F32, true>(cur, a.l2_eps, lane, sh.k[ring], sh.kt[ring], sh.norm_k[two]);
         } else {
           convert_rows<DK, F32, false>(cur, a.l2_eps, lane, sh.q[ring], nullptr, sh.norm_q[two]);
-          const bool live = c * kC + tl < w.n;
+          const bool live = c * C + tl < w.n;
           const float x = gb.x + bias;
           float gv = a.gate_mode == KDA_GATE_SOFTPLUS ? -amp * softplus_f(x) : a.lower_bound * sigmoid_f(amp * x);
           gv = gv < -200.0f ? -200.0f : gv;   // exp(-200) is 0 in fp32, and sums stay finite
@@ -554,9 +594,11 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
           sum += dpp_f64<0x112>(sum);
           sum += dpp_f64<0x114>(sum);
           sum += dpp_f64<0x118>(sum);
-          const double row0 = lane15_f64(sum);
-          if (tl >= 16) sum += row0;
-          if (lane < kC) {
+          if constexpr (NB == 2) {
+            const double row0 = lane15_f64(sum);
+            if (tl >= 16) sum += row0;
+          }
+          if (lane < C) {
             const float hi = static_cast<float>(sum);
             sh.g_hi[two][tl] = hi;
             sh.g_lo[two][tl] = static_cast<float>(sum - static_cast<double>(hi));
@@ -574,22 +616,22 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
       const int c = it + 2;
       if (c >= 0 && c < chunks) {
         const int ring = c % kRing, two = c % 2;
-        f32x4 ka[3], pa[3];   // blocks 00, 11, 10
+        f32x4 ka[M], pa[M];   // blocks 00, 11, 10
 #pragma unroll
-        for (int m = 0; m < 3; ++m) ka[m] = pa[m] = f32x4{0, 0, 0, 0};
+        for (int m = 0; m < M; ++m) ka[m] = pa[m] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
           const int at = row_slot(s, g, lane % 16);
-          h8 kk[TERMS][2], qq[TERMS][2];
+          h8 kk[TERMS][NB], qq[TERMS][NB];
 #pragma unroll
           for (int term = 0; term < TERMS; ++term)
 #pragma unroll
-            for (int rb = 0; rb < 2; ++rb) {
+            for (int rb = 0; rb < NB; ++rb) {
               kk[term][rb] = *reinterpret_cast<const h8*>(&sh.k[ring][term][rb][s][at][0]);
               qq[term][rb] = *reinterpret_cast<const h8*>(&sh.q[ring][term][rb][s][at][0]);
             }
 #pragma unroll
-          for (int m = 0; m < 3; ++m) {
+          for (int m = 0; m < M; ++m) {
             const int i = m > 0, j = m == 1;   // row block i, column block j
             // transposed: a lane holds row lane % 16 of block i, columns 4 g + 0..3 of block j
             ka[m] = mfma(kk[0][j], kk[0][i], ka[m]);
@@ -602,9 +644,9 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
             }
           }
         }
-        const float g_last = sh.g_hi[two][kC - 1], g_last_lo = sh.g_lo[two][kC - 1];
+        const float g_last = sh.g_hi[two][C - 1], g_last_lo = sh.g_lo[two][C - 1];
 #pragma unroll
-        for (int m = 0; m < 3; ++m) {
+        for (int m = 0; m < M; ++m) {
           const int i = m > 0, j = m == 1;
           const int row = 16 * i + lane % 16, col = 16 * j + 4 * g;
           const float gh = sh.g_hi[two][row], gl = sh.g_lo[two][row];
@@ -631,7 +673,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
             *reinterpret_cast<h4*>(&sh.p[third][1][i][lane][4 * j]) = h4{lo0.x, lo0.y, lo1.x, lo1.y};
           }
         }
-        if (lane < kC) {
+        if (lane < C) {
           const float gh = sh.g_hi[two][lane], gl = sh.g_lo[two][lane];
           const float nk = sh.norm_k[two][lane], be = sh.beta[two][lane];
           const float eg = exp_f(gh + gl);
@@ -639,7 +681,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
           sh.tab[ring][1][lane] = eg * nk;
           sh.tab[ring][2][lane] = a.scale * eg * sh.norm_q[two][lane];
           sh.tab[ring][3][lane] = nk * exp_f((g_last - gh) + (g_last_lo - gl));
-          if (lane == kC - 1) sh.last[ring] = eg;
+          if (lane == C - 1) sh.last[ring] = eg;
         }
         third = third == kRingP - 1 ? 0 : third + 1;
       }
@@ -655,7 +697,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
         // lane: row `row` of diagonal block `blk` (lanes 32.. repeat), x (I + A)
         // = e_row, from the last column back: with x_k known, row k of A is
         // taken off all columns before it
-        const int blk = (lane / 16) % 2, row = lane % 16;
+        const int blk = (lane / 16) % NB, row = lane % 16;
         float x[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) x[j] = row == j ? 1.0f : 0.0f;
@@ -669,7 +711,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
               if (4 * j4 + j < k) x[4 * j4 + j] = fmaf(-x[k], ar[j], x[4 * j4 + j]);
           }
         }
-        if (lane < 32) {
+        if (lane < C) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const f32x4 xj = {x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]};
@@ -682,21 +724,23 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
             *reinterpret_cast<h4*>(&sh.t[two][1][blk][16 * j + row][4 * blk]) = h4{lo0.x, lo0.y, lo1.x, lo1.y};
           }
         }
-        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront", "local");
-        // T10^T = -T00^T (A10^T T11^T) on the fp32 matrix instruction
-        f32x4 z = {0, 0, 0, 0}, y = {0, 0, 0, 0};
-        const f32x4 bt = *reinterpret_cast<const f32x4*>(&sh.join[1][lane % 16][4 * g]);      // T11[lane % 16][4g + r]
+        if constexpr (NB == 2) {
+          __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront", "local");
+          // T10^T = -T00^T (A10^T T11^T) on the fp32 matrix instruction
+          f32x4 z = {0, 0, 0, 0}, y = {0, 0, 0, 0};
+          const f32x4 bt = *reinterpret_cast<const f32x4*>(&sh.join[1][lane % 16][4 * g]);      // T11[lane % 16][4g + r]
 #pragma unroll
-        for (int r = 0; r < 4; ++r) z = __builtin_amdgcn_mfma_f32_16x16x4f32(sh.a[two][2][4 * g + r][lane % 16], bt[r], z, 0, 0, 0);
+          for (int r = 0; r < 4; ++r) z = __builtin_amdgcn_mfma_f32_16x16x4f32(sh.a[two][2][4 * g + r][lane % 16], bt[r], z, 0, 0, 0);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) y = __builtin_amdgcn_mfma_f32_16x16x4f32(sh.join[0][4 * g + r][lane % 16], z[r], y, 0, 0, 0);
-        // y: column (row of T10) lane % 16, rows (columns of T10) 4 g + 0..3
-        y *= -*reinterpret_cast<const f32x4*>(&sh.tab[c % kRing][0][4 * g]);
-        h2 hi0, lo0, hi1, lo1;
-        split2(y[0], y[1], 1.0f, hi0, lo0);
-        split2(y[2], y[3], 1.0f, hi1, lo1);
-        *reinterpret_cast<h4*>(&sh.t[two][0][1][lane][0]) = h4{hi0.x, hi0.y, hi1.x, hi1.y};
-        *reinterpret_cast<h4*>(&sh.t[two][1][1][lane][0]) = h4{lo0.x, lo0.y, lo1.x, lo1.y};
+          for (int r = 0; r < 4; ++r) y = __builtin_amdgcn_mfma_f32_16x16x4f32(sh.join[0][4 * g + r][lane % 16], z[r], y, 0, 0, 0);
+          // y: column (row of T10) lane % 16, rows (columns of T10) 4 g + 0..3
+          y *= -*reinterpret_cast<const f32x4*>(&sh.tab[c % kRing][0][4 * g]);
+          h2 hi0, lo0, hi1, lo1;
+          split2(y[0], y[1], 1.0f, hi0, lo0);
+          split2(y[2], y[3], 1.0f, hi1, lo1);
+          *reinterpret_cast<h4*>(&sh.t[two][0][1][lane][0]) = h4{hi0.x, hi0.y, hi1.x, hi1.y};
+          *reinterpret_cast<h4*>(&sh.t[two][1][1][lane][0]) = h4{lo0.x, lo0.y, lo1.x, lo1.y};
+        }
       }
       lds_barrier();
     }
@@ -712,21 +756,21 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
 
     // v and out of a chunk: the lane's rows 16 rb + 4 g + r, NCS columns
     const int stride = a.HV * dv * E;
-    int voff[2][4];
+    int voff[NB][4];
 #pragma unroll
-    for (int rb = 0; rb < 2; ++rb)
+    for (int rb = 0; rb < NB; ++rb)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         voff[rb][r] = (16 * rb + 4 * g + r) * stride + (colw + column<NCS>(lane, 0)) * E;
     auto chunk_rows = [&](const void* base, int c) {
-      return rows_resource(base, ((static_cast<int64_t>(t0) + c * kC) * a.HV + w.hv) * (dv * E), w.n - c * kC, stride,
+      return rows_resource<C>(base, ((static_cast<int64_t>(t0) + c * C) * a.HV + w.hv) * (dv * E), w.n - c * C, stride,
                            dv * E);
     };
-    Columns<F32, NCS> v[2][4];
+    Columns<F32, NCS> v[NB][4];
     auto load_v = [&](int c) {
       const __amdgpu_buffer_rsrc_t r0 = chunk_rows(a.v, c);
 #pragma unroll
-      for (int rb = 0; rb < 2; ++rb)
+      for (int rb = 0; rb < NB; ++rb)
 #pragma unroll
         for (int r = 0; r < 4; ++r) v[rb][r].load(r0, voff[rb][r]);
     };
@@ -755,9 +799,9 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
           for (int cs = 0; cs < NCS; ++cs) bound[cs] = largest(S, cs);
         }
         // K S and Q S, the state as hi + lo
-        f32x4 ks[2][NCS], qs[2][NCS];
+        f32x4 ks[NB][NCS], qs[NB][NCS];
 #pragma unroll
-        for (int rb = 0; rb < 2; ++rb)
+        for (int rb = 0; rb < NB; ++rb)
 #pragma unroll
           for (int cs = 0; cs < NCS; ++cs) ks[rb][cs] = qs[rb][cs] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -767,7 +811,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
           for (int cs = 0; cs < NCS; ++cs) split8(S[2 * s][cs], S[2 * s + 1][cs], one, hi[cs], lo[cs]);
           const int at = row_slot(s, g, lane % 16);
 #pragma unroll
-          for (int rb = 0; rb < 2; ++rb) {
+          for (int rb = 0; rb < NB; ++rb) {
             const h8 k0 = *reinterpret_cast<const h8*>(&sh.k[ring][0][rb][s][at][0]);
             const h8 q0 = *reinterpret_cast<const h8*>(&sh.q[ring][0][rb][s][at][0]);
 #pragma unroll
@@ -789,7 +833,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
           }
         }
         // R = v - e^G kh^T S, in units of 2^sig (zero past the end)
-        f32x4 R[2][NCS];
+        f32x4 R[NCS][NB];
         float down[NCS], up_old[NCS];
 #pragma unroll
         for (int cs = 0; cs < NCS; ++cs) {
@@ -797,7 +841,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
           up_old[cs] = __builtin_ldexpf(1.0f, sig[cs]);
         }
 #pragma unroll
-        for (int rb = 0; rb < 2; ++rb) {
+        for (int rb = 0; rb < NB; ++rb) {
           const f32x4 ck = *reinterpret_cast<const f32x4*>(&sh.tab[ring][1][16 * rb + 4 * g]);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
@@ -805,58 +849,58 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
             v[rb][r].unpack(x);
 #pragma unroll
             for (int cs = 0; cs < NCS; ++cs)
-              R[rb][cs][r] = fmaf(-ck[r], ks[rb][cs][r], down[cs] * x[cs]);
+              R[cs][rb][r] = fmaf(-ck[r], ks[rb][cs][r], down[cs] * x[cs]);
           }
         }
         if (it + 1 < chunks) load_v(it + 1);
         // The new state is at most last |S| + sum_j |kh_j| |U_j| in size, and
         // |U_j| <= 32 max|R|: move the unit so that this bound is in [2^13, 2^14)
         const float last = sh.last[ring];
-        f32x4 U[2][NCS];
+        f32x4 U[NCS][NB];
         float keep[NCS], up_new[NCS];
 #pragma unroll
         for (int cs = 0; cs < NCS; ++cs) {
           float m = 0.0f;
 #pragma unroll
-          for (int rb = 0; rb < 2; ++rb)
+          for (int rb = 0; rb < NB; ++rb)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(R[rb][cs][r]));
+            for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(R[cs][rb][r]));
           bound[cs] = fmaf(last, bound[cs], 1024.0f * max16_32(m));
           const int d = rescale(bound[cs], sig[cs], sig[cs] - 100);
           keep[cs] = __builtin_ldexpf(last, -d);
           up_new[cs] = __builtin_ldexpf(1.0f, sig[cs]);
           // U = T R
-          h8 hi, lo;
-          f32x4 r0, r1;
+          ht hi, lo;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            r0[r] = __builtin_ldexpf(R[0][cs][r], -d);
-            r1[r] = __builtin_ldexpf(R[1][cs][r], -d);
-          }
-          split8(r0, r1, one, hi, lo);
+          for (int rb = 0; rb < NB; ++rb)
 #pragma unroll
-          for (int rb = 0; rb < 2; ++rb) {
-            const h8 t0h = *reinterpret_cast<const h8*>(&sh.t[it % 2][0][rb][lane][0]);
-            const h8 t0l = *reinterpret_cast<const h8*>(&sh.t[it % 2][1][rb][lane][0]);
+            for (int r = 0; r < 4; ++r) R[cs][rb][r] = __builtin_ldexpf(R[cs][rb][r], -d);
+          split_rows(R[cs], one, hi, lo);
+#pragma unroll
+          for (int rb = 0; rb < NB; ++rb) {
+            const ht t0h = *reinterpret_cast<const ht*>(&sh.t[it % 2][0][rb][lane][0]);
+            const ht t0l = *reinterpret_cast<const ht*>(&sh.t[it % 2][1][rb][lane][0]);
             f32x4 acc = {0, 0, 0, 0};
             acc = mfma(t0l, hi, acc);
             acc = mfma(t0h, lo, acc);
-            U[rb][cs] = mfma(t0h, hi, acc);
+            U[cs][rb] = mfma(t0h, hi, acc);
           }
         }
         // S = e^(G_last) S + (diag(e^(G_last - G)) Kh)^T U
-        const f32x4 w0 = *reinterpret_cast<const f32x4*>(&sh.tab[ring][3][4 * g]);
-        const f32x4 w1 = *reinterpret_cast<const f32x4*>(&sh.tab[ring][3][16 + 4 * g]);
 #pragma unroll
         for (int cs = 0; cs < NCS; ++cs) {
-          h8 hi, lo;
-          split8(U[0][cs] * w0, U[1][cs] * w1, one, hi, lo);
+          ht hi, lo;
+          f32x4 wu[NB];
+#pragma unroll
+          for (int rb = 0; rb < NB; ++rb)
+            wu[rb] = U[cs][rb] * *reinterpret_cast<const f32x4*>(&sh.tab[ring][3][16 * rb + 4 * g]);
+          split_rows(wu, one, hi, lo);
 #pragma unroll
           for (int j = 0; j < KB; ++j) {
             const int at = kt_slot(j, g, lane % 16);
             f32x4 acc = S[j][cs] * keep[cs];
-            if constexpr (F32) acc = mfma(*reinterpret_cast<const h8*>(&sh.kt[ring][1][j][at][0]), hi, acc);
-            const h8 k0 = *reinterpret_cast<const h8*>(&sh.kt[ring][0][j][at][0]);
+            if constexpr (F32) acc = mfma(*reinterpret_cast<const ht*>(&sh.kt[ring][1][j][at][0]), hi, acc);
+            const ht k0 = *reinterpret_cast<const ht*>(&sh.kt[ring][0][j][at][0]);
             acc = mfma(k0, lo, acc);
             S[j][cs] = mfma(k0, hi, acc);
           }
@@ -864,12 +908,12 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
         // O = e^G Qh S0 + P U
 #pragma unroll
         for (int cs = 0; cs < NCS; ++cs) {
-          h8 hi, lo;
-          split8(U[0][cs], U[1][cs], one, hi, lo);
+          ht hi, lo;
+          split_rows(U[cs], one, hi, lo);
 #pragma unroll
-          for (int rb = 0; rb < 2; ++rb) {
-            const h8 p0 = *reinterpret_cast<const h8*>(&sh.p[third][0][rb][lane][0]);
-            const h8 p1 = *reinterpret_cast<const h8*>(&sh.p[third][1][rb][lane][0]);
+          for (int rb = 0; rb < NB; ++rb) {
+            const ht p0 = *reinterpret_cast<const ht*>(&sh.p[third][0][rb][lane][0]);
+            const ht p1 = *reinterpret_cast<const ht*>(&sh.p[third][1][rb][lane][0]);
             f32x4 acc = {0, 0, 0, 0};
             acc = mfma(p1, hi, acc);
             acc = mfma(p0, lo, acc);
@@ -882,7 +926,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
         }
         const __amdgpu_buffer_rsrc_t ro = chunk_rows(a.out, it);
 #pragma unroll
-        for (int rb = 0; rb < 2; ++rb)
+        for (int rb = 0; rb < NB; ++rb)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             float x[NCS];
@@ -958,7 +1002,8 @@ int launch_gdr_prefill(const DecodeArgs& args, int dk, int dv, bool qkv_bf16, bo
                            : launch_dk<32, true>(args, dv, state_layout, state_bf16, stream); break;
     case 64: rc = qkv_bf16 ? launch_dk<64, false>(args, dv, state_layout, state_bf16, stream)
                            : launch_dk<64, true>(args, dv, state_layout, state_bf16, stream); break;
-    case 128: rc = launch_dk<128, false>(args, dv, state_layout, state_bf16, stream); break;
+    case 128: rc = qkv_bf16 ? launch_dk<128, false>(args, dv, state_layout, state_bf16, stream)
+                            : launch_dk<128, true>(args, dv, state_layout, state_bf16, stream); break;
     default: return KDA_ERR_UNSUPPORTED;
   }
   return rc == hipSuccess ? KDA_OK : KDA_ERR_LAUNCH;

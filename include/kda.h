@@ -259,8 +259,14 @@ int kda_gdr_decode(const kda_tensor* out, const kda_tensor* q, const kda_tensor*
 
 /*
  * kda_gdr_prefill - kda_gdr_decode's operation and arguments for whole
- * prompts.  dk and dv must each be 32, 64 or 128 (else
- * KDA_ERR_UNSUPPORTED).
+ * prompts, in chunks of 32 tokens on the matrix cores; the result equals the
+ * token-by-token recurrence up to rounding order, with operands of about 22
+ * significant bits and fp32 sums.  No workspace.  dk and dv must each be 32,
+ * 64 or 128, T at most 2^31 - 65, B * HV at most 2^23 - 1 and
+ * HV * max(dk, dv) below 2^24 (else KDA_ERR_UNSUPPORTED).  Where
+ * kda_gdr_decode gives an infinity or NaN from some token on (non-finite
+ * inputs, or an overflow), this call may give it from up to 31 tokens
+ * earlier: the tokens of a chunk meet in its products.
  */
 int kda_gdr_prefill(const kda_tensor* out, const kda_tensor* q, const kda_tensor* k,
                     const kda_tensor* v, const kda_tensor* raw_gate,

@@ -309,9 +309,10 @@ def test_prefill(torch_cuda, dk, dv, layout, qkv, state):
         state=state)
 
 
+@pytest.mark.parametrize("qkv", ["bf16", "f32"])
 @pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 47, 63, 64, 65, 127, 128, 129, 200])
-def test_prefill_lengths(torch_cuda, n):
-    run(torch_cuda, "prefill", "length", [n, 3], H=1, HV=1, layout="v_first" if n % 2 else "k_first")
+def test_prefill_lengths(torch_cuda, n, qkv):
+    run(torch_cuda, "prefill", "length", [n, 3], H=1, HV=1, qkv=qkv, layout="v_first" if n % 2 else "k_first")
 
 
 @pytest.mark.parametrize("B,H,HV", [(1, 1, 1), (1, 3, 3), (3, 2, 8), (2, 16, 32), (9, 16, 16)])
@@ -320,9 +321,11 @@ def test_prefill_heads(torch_cuda, B, H, HV):
         lower_bound=-5.0, layout="v_first")
 
 
-def test_prefill_many_tiles(torch_cuda):
-    """More (request, head) tiles than compute units, each a few chunks."""
-    run(torch_cuda, "prefill", "tiles", [66 + b for b in range(20)], H=16, HV=16, dk=64, dv=128)
+@pytest.mark.parametrize("HV,dk,dv,qkv", [(16, 64, 128, "bf16"), (16, 128, 128, "f32"), (6, 128, 128, "bf16"),
+                                          (3, 128, 128, "f32"), (5, 32, 64, "f32"), (16, 128, 32, "bf16")])
+def test_prefill_many_tiles(torch_cuda, HV, dk, dv, qkv):
+    """From some to more (request, head) tiles than compute units: each form of the workgroups."""
+    run(torch_cuda, "prefill", "tiles", [66 + b for b in range(20)], H=HV, HV=HV, dk=dk, dv=dv, qkv=qkv)
 
 
 def test_prefill_skips(torch_cuda):
