@@ -5,7 +5,8 @@
 The host argument checker is plain C++ (g++); the kernel files (decode and
 chunked prefill) go through hipcc for gfx950 with packed-fp32 instructions
 disabled; hipcc links them into ``gated_delta_rule_82_amd/lib/libkda.so``.
-The benchmark's streaming-copy kernels (its HBM ceiling) build into a
+The call path of the Python binding (a CPython extension on torch's headers)
+builds into ``lib/_kda_binding.so``.  The benchmark's streaming-copy kernels (its HBM ceiling) build into a
 separate ``lib/libkda_bench.so`` that the library itself never loads.
 """
 from __future__ import annotations
@@ -23,6 +24,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libkda.so")
 BENCH_LIB = os.path.join(LIBDIR, "libkda_bench.so")
+BINDING = os.path.join(LIBDIR, "_kda_binding.so")
 ARCH = "gfx950"
 
 HIP_FLAGS = [
@@ -80,6 +82,19 @@ def _run_all(cmds, verbose):
         raise RuntimeError("\n".join(failed))
 
 
+def _binding_command(out):
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    include, lib = os.path.join(home, "include"), os.path.join(home, "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f"-I{INCLUDE}", f"-I{include}", f"-I{os.path.join(include, 'torch', 'csrc', 'api', 'include')}",
+            f"-I{sysconfig.get_paths()['include']}", os.path.join(CSRC, "kda_binding.cpp"), "-o", out,
+            f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10"]
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
@@ -99,11 +114,14 @@ def build(verbose: bool = True) -> str:
     units.append(("bench_copy", "bench_copy", []))
     _run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", f"-I{INCLUDE}", f"-I{CSRC}",
           "-c", os.path.join(CSRC, "kda_api.cpp"), "-o", api_o], verbose)
+    tmp_binding = BINDING + ".tmp"
+    binding = _binding_command(tmp_binding)
     # the kernel objects compile in parallel (each takes tens of seconds)
     cmds = [[hipcc, *HIP_FLAGS, *EXTRA_FLAGS.get(src, []), *defs, f"-I{INCLUDE}", f"-I{CSRC}", "-c",
              os.path.join(CSRC, f"{src}.hip"), "-o", os.path.join(BUILD, f"{obj}.o")]
             for src, obj, defs in units]
-    _run_all(cmds, verbose)
+    _run_all(cmds + [binding], verbose)
+    os.replace(tmp_binding, BINDING)
     tmp = LIB + ".tmp"
     _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", api_o, *lib_objs, "-o", tmp,
           "-Wl,-z,defs", "-Wl,--no-undefined",
