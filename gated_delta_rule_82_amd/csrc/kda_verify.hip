@@ -273,23 +273,25 @@ __global__ __launch_bounds__(kWave) void verify_pick(const VerifyArgs a) {
   constexpr int VEC = kVec<BF16>;
   const int lane = threadIdx.x;
   const int b = blockIdx.x;
-  // the verdict that verify_sum left
+  // All that does not hang on another load is asked for at once; the first
+  // kHeld rounds of partials and their sums stay in registers.
+  const int64_t nseg = segments(a.V, kSegment<BF16>);
+  const double* const part = static_cast<const double*>(a.workspace) + b * nseg;
+  double held[kHeld], upto[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) held[i] = i * kWave + lane < nseg ? part[i * kWave + lane] : 0.0;
+  const float u = a.u_sample[b];
+  const int commit = a.n_commit[b];   // the verdict that verify_sum left
   Verdict v;
   const int t0 = window(a, b, v.n);
   if (v.n == 0) {
     if (lane == 0) a.next_token[b] = -1;
     return;
   }
-  v.kept = a.n_commit[b] - 1;
+  v.kept = commit - 1;
   v.fell = v.kept < v.n - 1;
   v.row = static_cast<int64_t>(t0) + v.kept;
-  const int64_t nseg = segments(a.V, kSegment<BF16>);
-  const double* const part = static_cast<const double*>(a.workspace) + b * nseg;
-  // the total, summed in the order in which the search below adds up; the
-  // first kHeld rounds of partials and their sums stay in registers
-  double held[kHeld], upto[kHeld];
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) held[i] = i * kWave + lane < nseg ? part[i * kWave + lane] : 0.0;
+  // the total, summed in the order in which the search below adds up
   double total = 0.0;
   int64_t last = -1;   // last segment with mass
 #pragma unroll
@@ -309,7 +311,6 @@ __global__ __launch_bounds__(kWave) void verify_pick(const VerifyArgs a) {
     if (lane == 0) a.next_token[b] = -1;
     return;
   }
-  const float u = a.u_sample[b];
   const double bar = (u > 0.0f ? static_cast<double>(u) : 0.0) * total;
   double before = 0.0;   // mass of the segments before `seg`
   int64_t seg = -1;

@@ -531,11 +531,11 @@ struct ChunkTables {
 };
 
 // exp(G_i - G_j) from two-float sums.
-__device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float lo_j) {
+[[maybe_unused]] __device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float lo_j) {
   return exp_f((hi_i - hi_j) + (lo_i - lo_j));
 }
 
-__device__ __forceinline__ double row_shr_f64(double x, int by) {
+[[maybe_unused]] __device__ __forceinline__ double row_shr_f64(double x, int by) {
   const uint64_t u = __builtin_bit_cast(uint64_t, x);
   const int lo = static_cast<int>(u), hi = static_cast<int>(u >> 32);
   uint32_t l, h;
@@ -553,11 +553,46 @@ __device__ __forceinline__ double row_shr_f64(double x, int by) {
 }
 
 // Orders the wave's LDS accesses (one wave is the whole workgroup).
-__device__ __forceinline__ void lds_sync() { __syncthreads(); }
+[[maybe_unused]] __device__ __forceinline__ void lds_sync() { __syncthreads(); }
 
-template <int DK, int DV, bool QBF16, bool SBF16, int LAYOUT>
+// One chunk's inputs in storage form.
+template <int DK, int DV, int CW, bool QBF16>
+struct ChunkIn {
+  static constexpr int KS = DK / 32;
+  u32x4 x[KS][QBF16 ? 1 : 2];   // lane row n16 (k 0..7, q 8..15), keys 32 s + 8 g + 0..7
+  RawRun<QBF16, 1> v[kW];       // the lane's column of the solve
+  float gate, beta;             // of token lane % 8
+
+  // `n` tokens from row t0 of the stream; rows past them repeat row t0 and are
+  // dropped where they are used
+  __device__ __forceinline__ void load(const WindowArgs& a, const Job& j, const TokenStream& src, int64_t t0, int n,
+                                       bool outputs, int lane) {
+    const int n16 = lane % 16, tok = n16 % kW;
+    const bool live = tok < n && (n16 < kW || outputs);
+    const void* const base = n16 < kW || !outputs ? src.k : src.q;
+    const int64_t off = ((t0 + (live ? tok : 0)) * a.H + j.h) * DK + 8 * (lane / 16);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      if constexpr (QBF16) {
+        x[s][0] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + off + 32 * s);
+      } else {
+        x[s][0] = *reinterpret_cast<const u32x4*>(static_cast<const float*>(base) + off + 32 * s);
+        x[s][1] = *reinterpret_cast<const u32x4*>(static_cast<const float*>(base) + off + 32 * s + 4);
+      }
+    }
+    const int gt = lane % kW;
+    const int64_t goff = (t0 + (gt < n ? gt : 0)) * a.HV + j.hv;
+    gate = src.raw_gate[goff];
+    beta = src.beta_logits[goff];
+#pragma unroll
+    for (int i = 0; i < kW; ++i)
+      v[i].load(src.v, ((t0 + (i < n ? i : 0)) * a.HV + j.hv) * DV + j.slab * CW + lane % CW);
+  }
+};
+
+template <int DK, int DV, bool QBF16, bool SBF16, int LAYOUT, int CWT>
 __global__ __launch_bounds__(kWave) void window_chunk(const WindowArgs a) {
-  constexpr int CW = DV < 32 ? DV : 32;
+  constexpr int CW = DV < CWT ? DV : CWT;
   constexpr int SLABS = DV / CW;
   constexpr int NCS = CW / 16;
   constexpr int KS = DK / 32;
@@ -647,42 +682,46 @@ __global__ __launch_bounds__(kWave) void window_chunk(const WindowArgs a) {
   constexpr int SHARE = kWave / CW;              // lanes that solve a column; each stores kW / SHARE outputs
   const int part = lane / CW;
 
+  // With few waves the next chunk's inputs are asked for before this one is
+  // worked on; with many, that costs the third wave of a SIMD (184 registers
+  // for 156: 8-token windows over 96 heads x 256 requests 643 -> 686 us on an
+  // fp32 pool, 513 -> 603 on bf16).
+  constexpr bool AHEAD = CWT < 32;
+  struct Place {
+    int st, n;
+    int64_t t0;
+  };
+  const auto place = [&](int done) {
+    Place p;
+    p.st = done >= j.n[0];               // stream
+    const int left = (p.st ? total : j.n[0]) - done;
+    p.n = left < kW ? left : kW;
+    p.t0 = j.first[p.st] + (p.st ? done - j.n[0] : done);
+    return p;
+  };
+  ChunkIn<DK, DV, CW, QBF16> next;
+  Place coming = place(0);
+  if constexpr (AHEAD) next.load(a, j, a.src[coming.st], coming.t0, coming.n, coming.st == a.window, lane);
   for (int done = 0; done < total;) {
-    const int st = done >= j.n[0];               // stream
-    const TokenStream& src = a.src[st];
-    const int left = (st ? total : j.n[0]) - done;
-    const int n = left < kW ? left : kW;
-    const int64_t t0 = j.first[st] + (st ? done - j.n[0] : done);
+    const int st = coming.st, n = coming.n;
+    const int64_t t0 = coming.t0;
     const bool outputs = st == a.window;
     const bool updates = st == 0 || done + n < total;
-
-    // ---- this chunk's rows: lane row n16 (k 0..7, q 8..15), keys 32 s + 8 g + 0..7 ----
+    if constexpr (!AHEAD) next.load(a, j, a.src[st], t0, n, outputs, lane);
+    ChunkIn<DK, DV, CW, QBF16> cur = next;
+    if (done + n < total) {
+      coming = place(done + n);
+      if constexpr (AHEAD) next.load(a, j, a.src[coming.st], coming.t0, coming.n, coming.st == a.window, lane);
+    }
+    auto& xw = cur.x;
+    auto& vw = cur.v;
     const int tok = n16 % kW;
     const bool live_row = tok < n && (n16 < kW || outputs);
-    const void* const base = n16 < kW || !outputs ? src.k : src.q;
-    const int64_t off = ((t0 + (live_row ? tok : 0)) * a.H + j.h) * DK + 8 * g;
-    u32x4 xw[KS][QBF16 ? 1 : 2];
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      if constexpr (QBF16) {
-        xw[s][0] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + off + 32 * s);
-      } else {
-        xw[s][0] = *reinterpret_cast<const u32x4*>(static_cast<const float*>(base) + off + 32 * s);
-        xw[s][1] = *reinterpret_cast<const u32x4*>(static_cast<const float*>(base) + off + 32 * s + 4);
-      }
-    }
     const int gt = lane % kW;
-    const int64_t goff = (t0 + (gt < n ? gt : 0)) * a.HV + j.hv;
-    const float gate = src.raw_gate[goff];
-    const float bl = src.beta_logits[goff];
-    RawRun<QBF16, 1> vw[kW];
-#pragma unroll
-    for (int i = 0; i < kW; ++i)
-      vw[i].load(src.v, ((t0 + (i < n ? i : 0)) * a.HV + j.hv) * DV + j.slab * CW + c);
 
     // ---- gates: G summed over the 8 lanes of a group of tokens, in fp64 ----
     {
-      const float x = gate + bias;
+      const float x = cur.gate + bias;
       float gv = a.gate_mode == KDA_GATE_SOFTPLUS ? -amp * softplus_f(x) : a.lower_bound * sigmoid_f(amp * x);
       gv = gv < -200.0f ? -200.0f : gv;   // exp(-200) is 0 in fp32, and sums stay finite
       double sum = gt < n ? static_cast<double>(gv) : 0.0;
@@ -693,7 +732,7 @@ __global__ __launch_bounds__(kWave) void window_chunk(const WindowArgs a) {
         const float hi = static_cast<float>(sum);
         sh.g_hi[gt] = hi;
         sh.g_lo[gt] = static_cast<float>(sum - static_cast<double>(hi));
-        sh.beta[gt] = gt < n ? sigmoid_f(bl) : 0.0f;
+        sh.beta[gt] = gt < n ? sigmoid_f(cur.beta) : 0.0f;
       }
     }
 
@@ -847,9 +886,15 @@ __global__ __launch_bounds__(kWave) void window_chunk(const WindowArgs a) {
 //           bf16 value-first   310 / 498    456 / 512    755 / 540
 // A value-first slab is read in 64-byte pieces of 16 rows there (256 or 512
 // bytes of a row here), which costs 20% of an fp32 pool's streaming rate.
-// One request of 32 heads: 10.3 / 6.9 us at 8 tokens, 4.5 / 6.4 at 2.
+// Few waves (up to half a wave per SIMD) take 16 columns each and are bound by
+// the chain of latencies; 32 heads x 4 requests, fp32 pool, value-first:
+//   decode  2: 5.6 / 7.5   4: 7.7 / 7.8   8: 11.5 / 8.1
+//   window  2: 7.4 / 9.9   4: 11.1 / 10.1   8: 18.8 / 10.5
+constexpr int64_t kFewWaves = 512;   // 32-column waves: half a wave per SIMD
+
 template <bool SBF16, int LAYOUT>
-constexpr int64_t chunk_from(int window) {
+constexpr int64_t chunk_from(int window, bool few) {
+  if (few) return window ? 3 : 4;
   if (!SBF16 && LAYOUT == KDA_STATE_V_FIRST) return window ? 7 : 12;
   return window ? 5 : 6;
 }
@@ -857,13 +902,19 @@ constexpr int64_t chunk_from(int window) {
 template <int DK, int DV, bool QBF16, bool SBF16, int LAYOUT>
 hipError_t launch_one(const WindowArgs& args, hipStream_t stream) {
   constexpr int CW = DV < 32 ? DV : 32;
-  const int64_t nwg = static_cast<int64_t>(args.B) * args.HV * (DV / CW);
+  int64_t nwg = static_cast<int64_t>(args.B) * args.HV * (DV / CW);
   void* kargs[] = {const_cast<WindowArgs*>(&args)};
   const void* fn = LAYOUT == KDA_STATE_K_FIRST ? reinterpret_cast<const void*>(&window_kfirst<DK, DV, QBF16, SBF16>)
                                                : reinterpret_cast<const void*>(&window_vfirst<DK, DV, QBF16, SBF16>);
   if constexpr (!kChannel && DK >= 32) {
-    if (static_cast<int64_t>(args.src[args.window].T) >= chunk_from<SBF16, LAYOUT>(args.window) * args.B)
-      fn = reinterpret_cast<const void*>(&window_chunk<DK, DV, QBF16, SBF16, LAYOUT>);
+    const bool few = nwg <= kFewWaves;
+    if (static_cast<int64_t>(args.src[args.window].T) >= chunk_from<SBF16, LAYOUT>(args.window, few) * args.B) {
+      fn = reinterpret_cast<const void*>(&window_chunk<DK, DV, QBF16, SBF16, LAYOUT, 32>);
+      if (DV >= 32 && few) {
+        fn = reinterpret_cast<const void*>(&window_chunk<DK, DV, QBF16, SBF16, LAYOUT, 16>);
+        nwg *= 2;
+      }
+    }
   }
   return hipLaunchKernel(fn, dim3(static_cast<uint32_t>(nwg)), dim3(kWave), kargs, 0, stream);
 }

@@ -243,19 +243,20 @@ def test_many_tokens_match_single_token_calls(torch_cuda):
     b.check("decode", one, "single tokens")
 
 
+@pytest.mark.parametrize("n", [2, 16])
 @pytest.mark.parametrize("layout", LAYOUTS)
-def test_window_equals_decode_of_kept_then_new(torch_cuda, layout):
+def test_window_equals_decode_of_kept_then_new(torch_cuda, layout, n):
     """decode_window = gdr_decode of the kept tokens, then of the window on a
-    copy of the pool.  Same kernels on the same values: the pool bit for bit."""
+    copy of the pool.  Both sides take the same form of the kernel (n tokens a
+    request each time), so the pool is equal bit for bit."""
     torch = torch_cuda
     from gated_delta_rule_82_amd import kda
-    b = Batch(torch, [4, 2], replay=[(0, 3), (3, 2)], layout=layout, seed=3)
+    b = Batch(torch, [n, n], replay=[(0, n), (n, n)], layout=layout, seed=3)
     d, e = b.device(), b.device()
     b.call("window", d)
     rk, rv, rg, rb, begin, count = e["rep"]
-    cu = torch.tensor([0, 3, 5], dtype=torch.int32, device="cuda")
-    n = slice(0, 5)
-    rk, rv, rg, rb = (x[:, n].contiguous() for x in (rk, rv, rg, rb))
+    cu = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+    rk, rv, rg, rb = (x[:, :2 * n].contiguous() for x in (rk, rv, rg, rb))
     kda.gdr_decode(torch.empty_like(rv), rk, rk, rv, rg, rb, e["a_log"], e["bias"], cu, e["pool"], e["idx"], **b.mode)
     kept = e["pool"].clone()
     b.call("decode", e)
