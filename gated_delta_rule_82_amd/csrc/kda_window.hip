@@ -626,13 +626,13 @@ __global__ __launch_bounds__(kWave) void window_chunk(const WindowArgs a) {
           float x[8] = {S[s][0][cs][0], S[s][0][cs][1], S[s][0][cs][2], S[s][0][cs][3],
                         S[s][1][cs][0], S[s][1][cs][1], S[s][1][cs][2], S[s][1][cs][3]};
           if constexpr (SBF16) {
-            if constexpr (STORE) StateIO<true, 8>::store(res, voff, 32 * s * E, x);
-            else StateIO<true, 8>::load(res, voff, 32 * s * E, x);
+            if constexpr (STORE) StateIO<true, 8, 0>::store(res, voff, 32 * s * E, x);
+            else StateIO<true, 8, 0>::load(res, voff, 32 * s * E, x);
           } else {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-              if constexpr (STORE) StateIO<false, 4>::store(res, voff, (32 * s + 4 * b) * E, x + 4 * b);
-              else StateIO<false, 4>::load(res, voff, (32 * s + 4 * b) * E, x + 4 * b);
+              if constexpr (STORE) StateIO<false, 4, 0>::store(res, voff, (32 * s + 4 * b) * E, x + 4 * b);
+              else StateIO<false, 4, 0>::load(res, voff, (32 * s + 4 * b) * E, x + 4 * b);
             }
           }
           if constexpr (!STORE) {
@@ -781,13 +781,31 @@ __global__ __launch_bounds__(kWave) void window_chunk(const WindowArgs a) {
     f32x4 dots[NCS];
 #pragma unroll
     for (int cs = 0; cs < NCS; ++cs) dots[cs] = f32x4{0, 0, 0, 0};
+    // A slab as a bf16 pool holds it goes on the bf16 matrix instruction, the
+    // products as exact as on the fp32 one and an eighth of the time.
+    if (SBF16 && QBF16 && done == 0) {   // uniform
+      if constexpr (SBF16 && QBF16) {
 #pragma unroll
-    for (int s = 0; s < KS; ++s)
+        for (int s = 0; s < KS; ++s)
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
+          for (int cs = 0; cs < NCS; ++cs) {
+            u32x4 w;
 #pragma unroll
-        for (int cs = 0; cs < NCS; ++cs)
-          dots[cs] = __builtin_amdgcn_mfma_f32_16x16x4f32(key_value(s, e), S[s][e / 4][cs][e % 4], dots[cs], 0, 0, 0);
+            for (int e = 0; e < 4; ++e)
+              w[e] = f32x2_to_bf16x2_rne(S[s][e / 2][cs][2 * (e % 2)], S[s][e / 2][cs][2 * (e % 2) + 1]);
+            dots[cs] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xw[s][0]),
+                                                              __builtin_bit_cast(bf16x8, w), dots[cs], 0, 0, 0);
+          }
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+          for (int cs = 0; cs < NCS; ++cs)
+            dots[cs] = __builtin_amdgcn_mfma_f32_16x16x4f32(key_value(s, e), S[s][e / 4][cs][e % 4], dots[cs], 0, 0, 0);
+    }
 
     lds_sync();
     // ---- factors ----
@@ -872,20 +890,22 @@ __global__ __launch_bounds__(kWave) void window_chunk(const WindowArgs a) {
 // dispatch
 // ---------------------------------------------------------------------------
 
-// Tokens per request from which a window goes 8 tokens at a time
-// (window_chunk) rather than token by token.  dk = dv = 128, bf16 q, k, v, us
-// token by token / 8 at a time, for 2, 4 and 8 tokens per request over 96
+// Half tokens per request (on average) from which a window goes 8 tokens at a
+// time (window_chunk) rather than token by token.  dk = dv = 128, bf16 q, k, v,
+// us token by token / 8 at a time, for 2, 4 and 8 tokens per request over 96
 // heads x 256 requests:
-//   decode  f32 key-first      544 / 556    550 / 562    612 / 598
-//           f32 value-first    559 / 682    558 / 684    618 / 732
-//           bf16 key-first     337 / 352    361 / 370    533 / 403
-//           bf16 value-first   285 / 411    328 / 399    527 / 427
-//   window  f32 key-first      542 / 580    569 / 602    786 / 643
-//           f32 value-first    559 / 693    579 / 721    848 / 783
-//           bf16 key-first     351 / 471    466 / 482    743 / 513
-//           bf16 value-first   310 / 498    456 / 512    755 / 540
-// A value-first slab is read in 64-byte pieces of 16 rows there (256 or 512
-// bytes of a row here), which costs 20% of an fp32 pool's streaming rate.
+//   decode  f32 key-first      544 / 556    550 / 561    612 / 597
+//           f32 value-first    559 / 637    558 / 668    618 / 717
+//           bf16 key-first     337 / 338    361 / 355    533 / 386
+//           bf16 value-first   285 / 322    328 / 338    527 / 367
+//   window  f32 key-first      542 / 582    569 / 596    786 / 631
+//           f32 value-first    559 / 660    579 / 691    848 / 748
+//           bf16 key-first     351 / 422    466 / 435    743 / 462
+//           bf16 value-first   310 / 417    456 / 430    755 / 457
+// 1..8 tokens over 32 heads x 128 requests, bf16: 79 / 65 and 72 / 62 us.  A
+// value-first slab is read in 64-byte pieces of 16 rows here (256 or 512 bytes
+// of a row token by token); with the touched-once hint on them the fp32 pool's
+// 637 us are 682 and the bf16 pool's 322 are 407.
 // Few waves (up to half a wave per SIMD) take 16 columns each and are bound by
 // the chain of latencies; 32 heads x 4 requests, fp32 pool, value-first:
 //   decode  2: 5.6 / 7.5   4: 7.7 / 7.8   8: 11.5 / 8.1
@@ -894,9 +914,9 @@ constexpr int64_t kFewWaves = 512;   // 32-column waves: half a wave per SIMD
 
 template <bool SBF16, int LAYOUT>
 constexpr int64_t chunk_from(int window, bool few) {
-  if (few) return window ? 3 : 4;
-  if (!SBF16 && LAYOUT == KDA_STATE_V_FIRST) return window ? 7 : 12;
-  return window ? 5 : 6;
+  if (few) return window ? 6 : 8;
+  if (SBF16) return LAYOUT == KDA_STATE_V_FIRST && !window ? 9 : 8;
+  return LAYOUT == KDA_STATE_V_FIRST ? (window ? 14 : 24) : (window ? 10 : 12);
 }
 
 template <int DK, int DV, bool QBF16, bool SBF16, int LAYOUT>
@@ -908,7 +928,7 @@ hipError_t launch_one(const WindowArgs& args, hipStream_t stream) {
                                                : reinterpret_cast<const void*>(&window_vfirst<DK, DV, QBF16, SBF16>);
   if constexpr (!kChannel && DK >= 32) {
     const bool few = nwg <= kFewWaves;
-    if (static_cast<int64_t>(args.src[args.window].T) >= chunk_from<SBF16, LAYOUT>(args.window, few) * args.B) {
+    if (2 * static_cast<int64_t>(args.src[args.window].T) >= chunk_from<SBF16, LAYOUT>(args.window, few) * args.B) {
       fn = reinterpret_cast<const void*>(&window_chunk<DK, DV, QBF16, SBF16, LAYOUT, 32>);
       if (DV >= 32 && few) {
         fn = reinterpret_cast<const void*>(&window_chunk<DK, DV, QBF16, SBF16, LAYOUT, 16>);
