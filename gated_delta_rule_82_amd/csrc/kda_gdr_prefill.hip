@@ -21,10 +21,8 @@
 //     then is exact in fp16 (but for values below 2^-17 of the norm, off by
 //     at most 2^-25 of it), an fp32 row is taken as hi + lo, 22 bits;
 //   - the state, R = V - diag(e^G) Kh S0 and U are held in a unit 2^sig per
-//     value column and taken as hi + lo; T and P, whose entries are at most 1
-//     in size, as hi + lo.  The unit follows a bound on the state's size
-//     (below); fp16's smallest step, 2^-24, then is at most 2^-25 of the
-//     largest value also where the bound is 2^13 too wide.
+//     value column, which keeps them below 2^14, and taken as hi + lo; T and P,
+//     whose entries are at most 1 in size, as hi + lo.
 // |T_ij| <= 1: T_ij = -beta_i kh_i^T [product of contractions] kh_j.  The
 // lo.lo terms (2^-22) are dropped.  So an operand carries about 22 bits and
 // the result is close to fp32's; two bf16 terms would leave 16 bits.  G is
@@ -63,7 +61,6 @@ namespace {
 constexpr int kHelpers = 4;
 constexpr int kRing = 4;          // chunks of q and k held in LDS
 constexpr int kRingP = 3;         // of P, made a chunk later
-constexpr int kRefresh = 8;       // chunks between looks at the state's true size
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
@@ -137,14 +134,13 @@ __device__ __forceinline__ void split_rows(const f32x4 (&x)[1], float one, h4& h
 // the column in it, comes into [2^13, 2^14), but not below 2^min; returns by
 // how many powers it moved.
 constexpr int kSigMin = -100;
-__device__ __forceinline__ int rescale(float& bound, int& sig, int min) {
+__device__ __forceinline__ int rescale(float bound, int& sig, int min) {
   const int e = static_cast<int>(__float_as_uint(bound) >> 23) - 127;
   int to = sig + e - 13;
   min = min < kSigMin ? kSigMin : min;
   to = to < min ? min : to;
   const int d = to - sig;
   sig = to;
-  bound = __builtin_ldexpf(bound, -d);
   return d;
 }
 
@@ -471,7 +467,7 @@ __device__ __forceinline__ void slab_io(__amdgpu_buffer_rsrc_t res, int layout, 
   }
 }
 
-// max |S| of a column, to the four lanes that hold it.
+// max |S| of the lane's share of a column.
 template <int KB, int NCS>
 __device__ __forceinline__ float largest(const f32x4 (&S)[KB][NCS], int cs) {
   float m = 0.0f;
@@ -479,7 +475,7 @@ __device__ __forceinline__ float largest(const f32x4 (&S)[KB][NCS], int cs) {
   for (int j = 0; j < KB; ++j)
 #pragma unroll
     for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(S[j][cs][r]));
-  return max16_32(m);
+  return m;
 }
 
 struct Tile {
@@ -775,17 +771,15 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
         for (int r = 0; r < 4; ++r) v[rb][r].load(r0, voff[rb][r]);
     };
     load_v(0);
-    // S of column cs is held divided by 2^sig[cs]; |S| <= bound[cs] < 2^14 so held
+    // S of column cs is held divided by 2^sig[cs], below 2^14 in size
     int sig[NCS];
-    float bound[NCS];
     float one = 1.0f;
     asm("" : "+s"(one));
     int third = 0;   // it % kRingP
 #pragma unroll
     for (int cs = 0; cs < NCS; ++cs) {
       sig[cs] = 0;
-      bound[cs] = largest(S, cs);
-      const int d = rescale(bound[cs], sig[cs], kSigMin);
+      const int d = rescale(max16_32(largest(S, cs)), sig[cs], kSigMin);
       const float f = __builtin_ldexpf(1.0f, -d);
 #pragma unroll
       for (int j = 0; j < KB; ++j) S[j][cs] *= f;
@@ -794,10 +788,6 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
     for (int it = -3; it < chunks; ++it) {
       if (it >= 0) {
         const int ring = it % kRing;
-        if (it % kRefresh == kRefresh - 1) {
-#pragma unroll
-          for (int cs = 0; cs < NCS; ++cs) bound[cs] = largest(S, cs);
-        }
         // K S and Q S, the state as hi + lo
         f32x4 ks[NB][NCS], qs[NB][NCS];
 #pragma unroll
@@ -832,49 +822,55 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
             }
           }
         }
-        // R = v - e^G kh^T S, in units of 2^sig (zero past the end)
-        f32x4 R[NCS][NB];
-        float down[NCS], up_old[NCS];
-#pragma unroll
-        for (int cs = 0; cs < NCS; ++cs) {
-          down[cs] = __builtin_ldexpf(1.0f, -sig[cs]);
-          up_old[cs] = __builtin_ldexpf(1.0f, sig[cs]);
-        }
-#pragma unroll
-        for (int rb = 0; rb < NB; ++rb) {
-          const f32x4 ck = *reinterpret_cast<const f32x4*>(&sh.tab[ring][1][16 * rb + 4 * g]);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float x[NCS];
-            v[rb][r].unpack(x);
-#pragma unroll
-            for (int cs = 0; cs < NCS; ++cs)
-              R[cs][rb][r] = fmaf(-ck[r], ks[rb][cs][r], down[cs] * x[cs]);
-          }
-        }
-        if (it + 1 < chunks) load_v(it + 1);
-        // The new state is at most last |S| + sum_j |kh_j| |U_j| in size, and
-        // |U_j| <= 32 max|R|: move the unit so that this bound is in [2^13, 2^14)
+        // The chunk's unit, while these products run.  In one column, a step
+        // S <- alpha (I - beta kh kh^T) S + beta kh v lengthens S by at most
+        // |v|, so S stays within |S0|_2 + C max|v| through the chunk, and the
+        // corrections U_j and R within max|v| more; |S0|_2 <= sqrt(dk) max|S0|.
+        // 2 max(sqrt(dk) max|S0|, (C + 1) max|v|) covers them all.
         const float last = sh.last[ring];
-        f32x4 U[NCS][NB];
-        float keep[NCS], up_new[NCS];
+        f32x4 R[NCS][NB], U[NCS][NB];
+        float keep[NCS], up_old[NCS], up_new[NCS], down[NCS], shift[NCS];
+#pragma unroll
+        for (int cs = 0; cs < NCS; ++cs)
+#pragma unroll
+          for (int rb = 0; rb < NB; ++rb)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              float x[NCS];
+              v[rb][r].unpack(x);
+              R[cs][rb][r] = x[cs];
+            }
 #pragma unroll
         for (int cs = 0; cs < NCS; ++cs) {
+          constexpr float kRoot = DK == 128 ? 11.4f : DK == 64 ? 8.0f : 5.7f;
           float m = 0.0f;
 #pragma unroll
           for (int rb = 0; rb < NB; ++rb)
 #pragma unroll
             for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(R[cs][rb][r]));
-          bound[cs] = fmaf(last, bound[cs], 1024.0f * max16_32(m));
-          const int d = rescale(bound[cs], sig[cs], sig[cs] - 100);
+          m = fmaxf(m * (__builtin_ldexpf(C + 1.0f, -sig[cs])), kRoot * largest(S, cs));
+          up_old[cs] = __builtin_ldexpf(1.0f, sig[cs]);
+          const int d = rescale(2.0f * max16_32(m), sig[cs], sig[cs] - 100);
+          shift[cs] = __builtin_ldexpf(1.0f, -d);   // 0 where the new unit dwarfs all of S
           keep[cs] = __builtin_ldexpf(last, -d);
+          down[cs] = __builtin_ldexpf(1.0f, -sig[cs]);
           up_new[cs] = __builtin_ldexpf(1.0f, sig[cs]);
+        }
+        // R = v - e^G kh^T S, in the new unit (zero past the end)
+#pragma unroll
+        for (int rb = 0; rb < NB; ++rb) {
+          const f32x4 ck = *reinterpret_cast<const f32x4*>(&sh.tab[ring][1][16 * rb + 4 * g]);
+#pragma unroll
+          for (int cs = 0; cs < NCS; ++cs)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              R[cs][rb][r] = fmaf(-ck[r] * shift[cs], ks[rb][cs][r], down[cs] * R[cs][rb][r]);
+        }
+        if (it + 1 < chunks) load_v(it + 1);
+#pragma unroll
+        for (int cs = 0; cs < NCS; ++cs) {
           // U = T R
           ht hi, lo;
-#pragma unroll
-          for (int rb = 0; rb < NB; ++rb)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) R[cs][rb][r] = __builtin_ldexpf(R[cs][rb][r], -d);
           split_rows(R[cs], one, hi, lo);
 #pragma unroll
           for (int rb = 0; rb < NB; ++rb) {
