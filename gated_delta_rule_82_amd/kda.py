@@ -1,9 +1,12 @@
-"""Thin ctypes binding of libkda (argument marshalling only).
+"""Thin binding of libkda (argument marshalling only).
 
-Every step of the decode and of the chunked prefill runs in the HIP library; this module turns torch
-device tensors into ``kda_tensor`` descriptors, passes the current HIP stream
-and raises :class:`KdaError` on a nonzero status.  There is no fallback: if
-the library is missing or a tensor is not on a GPU, the call raises.
+Every step of every operator runs in the HIP library; this module checks that
+torch tensors can be passed, hands them with the current HIP stream to the
+library (through a small extension, csrc/kda_binding.cpp, that turns them into
+``kda_tensor`` descriptors) and raises :class:`KdaError` on a nonzero status.
+The ``call_raw*`` functions call the C ABI on descriptors made here.  There is
+no fallback: if a library is missing or a tensor is not on a GPU, the call
+raises.
 """
 from __future__ import annotations
 
