@@ -265,6 +265,92 @@ def test_window_equals_decode_of_kept_then_new(torch_cuda, layout, n):
     b.check("window", d)
 
 
+@pytest.mark.parametrize("scale", [1, 6])   # token by token, and several at a time
+@pytest.mark.parametrize("channel", [False, True])
+def test_replay_out_of_range_stays_inside(torch_cuda, channel, scale):
+    """begin is clamped to the replay's rows and count to the rows that follow."""
+    torch = torch_cuda
+    b = Batch(torch, [2 * scale, scale, scale], replay=[(0, 4), (1, 2), (0, 5)], channel=channel, seed=4)
+    d = b.device()
+    Tr = d["rep"][0].shape[1]
+    d["rep"][4] = torch.tensor([-3, Tr + 5, Tr - 1], dtype=torch.int32, device="cuda")
+    d["rep"][5] = torch.tensor([999, 4, 7], dtype=torch.int32, device="cuda")
+    b.call("window", d)
+    torch.cuda.synchronize()
+    b.replay = [(0, Tr), (0, 0), (Tr - 1, 1)]
+    b.check("window", d)
+    d = b.device()
+    d["rep"][5] = torch.tensor([-1, -2 ** 31, 0], dtype=torch.int32, device="cuda")
+    b.call("window", d)
+    torch.cuda.synchronize()
+    b.replay = [(0, 0)] * 3
+    b.check("window", d)
+
+
+@pytest.mark.parametrize("entry", ["decode", "window", "prefill"])
+@pytest.mark.parametrize("scale", [1, 9])
+def test_rows_behind_the_last_request_and_bad_offsets(torch_cuda, entry, scale):
+    """Rows past cu_seqlens[B] keep what they held; offsets outside the
+    tensors are clamped to them."""
+    torch = torch_cuda
+    lens = [2 * scale, 3 * scale, 4 * scale]
+    b = Batch(torch, lens, replay=[(0, 1)] * 3, seed=7)
+    d = b.device()
+    d["cu"] = d["cu"].clone()
+    d["cu"][3] = 5 * scale            # the last request has no rows, its tokens lie behind
+    b.call(entry, d)
+    torch.cuda.synchronize()
+    assert torch.isnan(d["out"][:, 5 * scale:]).all()
+    b.cu, b.lens = np.array([0, 2 * scale, 5 * scale, 5 * scale]), lens[:2] + [0]
+    b.check(entry, d)
+    b = Batch(torch, lens, replay=[(0, 1)] * 3, seed=7)
+    d = b.device()
+    d["cu"] = torch.tensor([-7, 2 * scale, 5 * scale, 10 ** 9], dtype=torch.int32, device="cuda")
+    b.call(entry, d)
+    torch.cuda.synchronize()
+    b.check(entry, d)
+
+
+@pytest.mark.parametrize("entry", ["decode", "window", "prefill"])
+def test_given_stream(torch_cuda, entry):
+    """On a stream given by its handle, behind that stream's own work."""
+    torch = torch_cuda
+    from gated_delta_rule_82_amd import kda
+    b = Batch(torch, [3, 40, 7], replay=[(0, 2), (1, 3), (0, 0)], seed=8)
+    d, e = b.device(), b.device()
+    b.call(entry, d)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    q = e["q"].clone()
+    e["q"].zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(10 ** 7)
+        e["q"].copy_(q)
+    call = {"decode": kda.gdr_decode, "prefill": kda.gdr_prefill, "window": kda.decode_window}[entry]
+    call(*b.args(e), *(e["rep"] if entry == "window" else []), stream=side.cuda_stream, **b.mode)
+    torch.cuda.synchronize()
+    assert torch.equal(d["out"], e["out"]) and torch.equal(d["pool"], e["pool"])
+
+
+def test_binding_refuses_what_cannot_be_passed(torch_cuda):
+    torch = torch_cuda
+    from gated_delta_rule_82_amd import kda
+    b = Batch(torch, [2, 1])
+    d = b.device()
+    for name, value, error in (("q", d["q"].half(), ValueError), ("q", d["q"].transpose(1, 2), ValueError),
+                               ("v", d["v"].cpu(), ValueError), ("beta", None, TypeError), ("a_log", 3.0, TypeError),
+                               ("pool", d["pool"][None], ValueError), ("pool", d["pool"][:, :3], ValueError)):
+        with pytest.raises(error, match="out|q|v|beta_logits|a_log|state_pool"):
+            kda.gdr_decode(*b.args(dict(d, **{name: value})), **b.mode)
+    with pytest.raises(kda.KdaError) as e:
+        kda.gdr_decode(*b.args(dict(d, bias=d["bias"][:3].clone())), **b.mode)
+    assert e.value.code == kda.KDA_ERR_SHAPE
+    with pytest.raises(kda.KdaError) as e:
+        kda.gdr_prefill(*b.args(d), **dict(b.mode, gate_mode="lower_bound", lower_bound=-1e39))
+    assert e.value.code == kda.KDA_ERR_MODE
+
+
 def test_offsets_past_32_bits(torch_cuda):
     """A pool of more than 2^31 values: the last slot's tile is found."""
     torch = torch_cuda

@@ -96,6 +96,11 @@ def test_verify_windows(torch_cuda, lens):
         assert len(set(n.tolist())) > 2     # some drafts stand, some fall
 
 
+@pytest.mark.parametrize("draft", [True, False])
+def test_verify_no_tokens_at_all(torch_cuda, draft):
+    check(torch_cuda, Case([0, 0, 0], 77, draft=draft))
+
+
 def test_verify_large_vocabulary(torch_cuda):
     check(torch_cuda, Case([3, 4], 300007, seed=2))
 
