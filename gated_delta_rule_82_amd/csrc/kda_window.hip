@@ -530,6 +530,21 @@ struct ChunkTables {
   float last;                 // e^(G_last)
 };
 
+// Replay and window at once: m replayed and n window tokens of a request with
+// m + 2 n <= 16 rows of k and q and m + n <= kMost tokens.  U runs over all of
+// them from the one state S0; only the replayed ones go into S'.
+constexpr int kMost = 11;
+
+template <int DK, int CW>
+struct JointTables {
+  float dots[16][CW];
+  float u[12][CW];
+  float k[12][DK + 4];
+  float coef[16][12];
+  float row[16], g_hi[16], g_lo[16], beta[16], lead[16], tail[16];
+  float last;
+};
+
 // exp(G_i - G_j) from two-float sums.
 [[maybe_unused]] __device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float lo_j) {
   return exp_f((hi_i - hi_j) + (lo_i - lo_j));
@@ -545,11 +560,20 @@ struct ChunkTables {
   } else if (by == 2) {
     l = __builtin_amdgcn_update_dpp(0, lo, 0x112, 0xf, 0xf, true);
     h = __builtin_amdgcn_update_dpp(0, hi, 0x112, 0xf, 0xf, true);
-  } else {
+  } else if (by == 4) {
     l = __builtin_amdgcn_update_dpp(0, lo, 0x114, 0xf, 0xf, true);
     h = __builtin_amdgcn_update_dpp(0, hi, 0x114, 0xf, 0xf, true);
+  } else {
+    l = __builtin_amdgcn_update_dpp(0, lo, 0x118, 0xf, 0xf, true);
+    h = __builtin_amdgcn_update_dpp(0, hi, 0x118, 0xf, 0xf, true);
   }
   return __builtin_bit_cast(double, static_cast<uint64_t>(h) << 32 | l);
+}
+
+// 8 keys of a slab that hold bf16 values, as an operand.
+[[maybe_unused]] __device__ __forceinline__ bf16x8 pack_slab(const f32x4& x, const f32x4& y) {
+  return __builtin_bit_cast(bf16x8, u32x4{f32x2_to_bf16x2_rne(x[0], x[1]), f32x2_to_bf16x2_rne(x[2], x[3]),
+                                          f32x2_to_bf16x2_rne(y[0], y[1]), f32x2_to_bf16x2_rne(y[2], y[3])});
 }
 
 // Orders the wave's LDS accesses (one wave is the whole workgroup).
@@ -590,14 +614,18 @@ struct ChunkIn {
   }
 };
 
-template <int DK, int DV, bool QBF16, bool SBF16, int LAYOUT, int CWT>
+template <int DK, int DV, bool QBF16, bool SBF16, int LAYOUT, int CWT, bool JOINT>
 __global__ __launch_bounds__(kWave) void window_chunk(const WindowArgs a) {
   constexpr int CW = DV < CWT ? DV : CWT;
   constexpr int SLABS = DV / CW;
   constexpr int NCS = CW / 16;
   constexpr int KS = DK / 32;
   constexpr int E = SBF16 ? 2 : 4;
-  __shared__ __attribute__((aligned(16))) ChunkTables<DK, CW> sh;
+  __shared__ __attribute__((aligned(16))) union {
+    ChunkTables<DK, CW> chunk;
+    std::conditional_t<JOINT, JointTables<DK, CW>, char> joint;
+  } tables;
+  ChunkTables<DK, CW>& sh = tables.chunk;
 
   const int lane = threadIdx.x;
   const int n16 = lane % 16, g = lane / 16;
@@ -681,6 +709,193 @@ __global__ __launch_bounds__(kWave) void window_chunk(const WindowArgs a) {
   const int c = lane % CW;                       // the lane's column in the solve
   constexpr int SHARE = kWave / CW;              // lanes that solve a column; each stores kW / SHARE outputs
   const int part = lane / CW;
+
+  if constexpr (JOINT) {
+    const int m = j.n[0], nw = j.n[1];
+    if (a.window && m > 0 && nw > 0 && m + 2 * nw <= 16 && m + nw <= kMost) {   // uniform
+      JointTables<DK, CW>& jt = tables.joint;
+      const int all = m + nw;
+      const TokenStream& s0 = a.src[0];
+      const TokenStream& s1 = a.src[1];
+      // token t of the joint list: its stream's row
+      const auto row_of = [&](int t) { return static_cast<int64_t>(t < m ? j.first[0] + t : j.first[1] + t - m); };
+      // ---- lane row n16: k of token n16, then q of the window's tokens; keys 32 s + 8 g + 0..7 ----
+      const bool is_k = n16 < all, is_q = !is_k && n16 < all + nw;
+      const int token = is_k ? n16 : is_q ? n16 - nw : 0;   // q row all + i belongs to token m + i
+      const void* const base = is_q ? s1.q : token < m ? s0.k : s1.k;
+      const int64_t off = (row_of(token) * a.H + j.h) * DK + 8 * g;
+      u32x4 xw[KS][QBF16 ? 1 : 2];
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        if constexpr (QBF16) {
+          xw[s][0] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + off + 32 * s);
+        } else {
+          xw[s][0] = *reinterpret_cast<const u32x4*>(static_cast<const float*>(base) + off + 32 * s);
+          xw[s][1] = *reinterpret_cast<const u32x4*>(static_cast<const float*>(base) + off + 32 * s + 4);
+        }
+      }
+      const int gt = n16 < all ? n16 : 0;
+      const int64_t goff = row_of(gt) * a.HV + j.hv;
+      const float gate = gt < m ? s0.raw_gate[goff] : s1.raw_gate[goff];
+      const float bl = gt < m ? s0.beta_logits[goff] : s1.beta_logits[goff];
+      RawRun<QBF16, 1> vw[kMost];
+#pragma unroll
+      for (int i = 0; i < kMost; ++i) {
+        const int t = i < all ? i : 0;
+        vw[i].load(t < m ? s0.v : s1.v, (row_of(t) * a.HV + j.hv) * DV + j.slab * CW + c);
+      }
+
+      // ---- gates, summed in fp64 over the lanes of a row ----
+      {
+        const float x = gate + bias;
+        float gv = a.gate_mode == KDA_GATE_SOFTPLUS ? -amp * softplus_f(x) : a.lower_bound * sigmoid_f(amp * x);
+        gv = gv < -200.0f ? -200.0f : gv;
+        double sum = n16 < all ? static_cast<double>(gv) : 0.0;
+        sum += row_shr_f64(sum, 1);
+        sum += row_shr_f64(sum, 2);
+        sum += row_shr_f64(sum, 4);
+        sum += row_shr_f64(sum, 8);
+        if (lane < 16) {
+          const float hi = static_cast<float>(sum);
+          jt.g_hi[n16] = hi;
+          jt.g_lo[n16] = static_cast<float>(sum - static_cast<double>(hi));
+          jt.beta[n16] = n16 < all ? sigmoid_f(bl) : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int h = 0; h < (QBF16 ? 1 : 2); ++h)
+          if (!is_k && !is_q) xw[s][h] = u32x4{0, 0, 0, 0};
+      const auto key_value = [&](int s, int e) {   // key 32 s + 8 g + e
+        if constexpr (QBF16) return e % 2 ? __uint_as_float(xw[s][0][e / 2] & 0xffff0000u) : __uint_as_float(xw[s][0][e / 2] << 16);
+        else return __uint_as_float(xw[s][e / 4][e % 4]);
+      };
+      float sq = 0.0f;
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sq = fmaf(key_value(s, e), key_value(s, e), sq);
+      sq = swap16_add(sq, sq);
+      sq = swap32_add(sq, sq);
+      if (lane < 16) jt.row[n16] = (is_q ? a.scale : 1.0f) * rsqrt_f(sq + a.l2_eps);
+      if (n16 < 12) {   // k of the replayed tokens, zero past them
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            f32x4 x = {key_value(s, 4 * h), key_value(s, 4 * h + 1), key_value(s, 4 * h + 2), key_value(s, 4 * h + 3)};
+            if (n16 >= m) x = f32x4{0, 0, 0, 0};
+            *reinterpret_cast<f32x4*>(&jt.k[n16][32 * s + 8 * g + 4 * h]) = x;
+          }
+      }
+      // ---- Gram matrix of the rows, rows against the slab ----
+      f32x4 gram = {0, 0, 0, 0}, dots[NCS];
+#pragma unroll
+      for (int cs = 0; cs < NCS; ++cs) dots[cs] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        if constexpr (QBF16) {
+          const bf16x8 x = __builtin_bit_cast(bf16x8, xw[s][0]);
+          gram = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, x, gram, 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            gram = __builtin_amdgcn_mfma_f32_16x16x4f32(key_value(s, e), key_value(s, e), gram, 0, 0, 0);
+        }
+        if constexpr (SBF16 && QBF16) {
+#pragma unroll
+          for (int cs = 0; cs < NCS; ++cs)
+            dots[cs] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xw[s][0]),
+                                                              pack_slab(S[s][0][cs], S[s][1][cs]), dots[cs], 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+#pragma unroll
+            for (int cs = 0; cs < NCS; ++cs)
+              dots[cs] = __builtin_amdgcn_mfma_f32_16x16x4f32(key_value(s, e), S[s][e / 4][cs][e % 4], dots[cs], 0, 0, 0);
+        }
+      }
+      lds_sync();
+      // ---- factors ----
+      if (lane < 16) {
+        const float gh = jt.g_hi[token], gl = jt.g_lo[token];
+        const float eg = exp_f(gh + gl);
+        jt.lead[n16] = eg * jt.row[n16] * (is_k ? jt.beta[n16] : 1.0f);
+        jt.tail[n16] = jt.row[n16] * decay(jt.g_hi[m - 1], jt.g_lo[m - 1], gh, gl);   // of replayed tokens only
+        if (n16 == m - 1) jt.last = eg;
+      }
+      if (n16 < all) {
+        const float gh = jt.g_hi[n16], gl = jt.g_lo[n16], nk = jt.row[n16];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 4 * g + r;
+          const bool k_row = row < all;
+          const int i = k_row ? row : row < all + nw ? row - nw : 0;
+          const float f = nk * jt.row[row] * decay(jt.g_hi[i], jt.g_lo[i], gh, gl) * gram[r];
+          jt.coef[row][n16] = k_row ? (n16 < i ? f * jt.beta[i] : 0.0f) : (n16 <= i ? f : 0.0f);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if constexpr (NCS == 2) *reinterpret_cast<float2*>(&jt.dots[4 * g + r][2 * n16]) = make_float2(dots[0][r], dots[1][r]);
+        else jt.dots[4 * g + r][n16] = dots[0][r];
+      }
+      lds_sync();
+      // ---- the solve, one column per lane ----
+      float U[kMost];
+#pragma unroll
+      for (int i = 0; i < kMost; ++i) {
+        U[i] = 0.0f;
+        if (i < all) {
+          float v[1];
+          vw[i].unpack(v);
+          float acc = fmaf(jt.beta[i], v[0], -jt.lead[i] * jt.dots[i][c]);
+#pragma unroll
+          for (int k = 0; k < i; ++k) acc = fmaf(-jt.coef[i][k], U[k], acc);
+          U[i] = acc;
+        }
+      }
+      if (part == 0) {
+#pragma unroll
+        for (int i = 0; i < 12; ++i) jt.u[i][c] = i < m ? U[i < kMost ? i : 0] * jt.tail[i] : 0.0f;
+      }
+      for (int i = part; i < nw; i += SHARE) {
+        const int row = all + i;
+        float o = jt.lead[row] * jt.dots[row][c];
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) o = k <= m + i ? fmaf(jt.coef[row][k], U[k], o) : o;
+        store_scalar<QBF16>(a.out, (row_of(m + i) * a.HV + j.hv) * DV + j.slab * CW + c, o);
+      }
+      lds_sync();
+      // ---- S' of the replayed tokens ----
+      const float last = jt.last;
+      float ub[3][NCS];
+#pragma unroll
+      for (int h = 0; h < 3; ++h)
+#pragma unroll
+        for (int cs = 0; cs < NCS; ++cs) ub[h][cs] = jt.u[4 * h + g][NCS * n16 + cs];
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int key = 32 * s + 8 * (n16 / 4) + 4 * b + n16 % 4;
+#pragma unroll
+          for (int cs = 0; cs < NCS; ++cs) S[s][b][cs] *= last;
+#pragma unroll
+          for (int h = 0; h < 3; ++h) {
+            if (4 * h < m) {   // uniform
+              const float kv = jt.k[4 * h + g][key];
+#pragma unroll
+              for (int cs = 0; cs < NCS; ++cs)
+                S[s][b][cs] = __builtin_amdgcn_mfma_f32_16x16x4f32(kv, ub[h][cs], S[s][b][cs], 0, 0, 0);
+            }
+          }
+        }
+      slab_io(std::true_type{});
+      return;
+    }
+  }
 
   // With few waves the next chunk's inputs are asked for before this one is
   // worked on; with many, that costs the third wave of a SIMD (184 registers
@@ -789,12 +1004,8 @@ __global__ __launch_bounds__(kWave) void window_chunk(const WindowArgs a) {
         for (int s = 0; s < KS; ++s)
 #pragma unroll
           for (int cs = 0; cs < NCS; ++cs) {
-            u32x4 w;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = f32x2_to_bf16x2_rne(S[s][e / 2][cs][2 * (e % 2)], S[s][e / 2][cs][2 * (e % 2) + 1]);
             dots[cs] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xw[s][0]),
-                                                              __builtin_bit_cast(bf16x8, w), dots[cs], 0, 0, 0);
+                                                              pack_slab(S[s][0][cs], S[s][1][cs]), dots[cs], 0, 0, 0);
           }
       }
     } else {
@@ -906,16 +1117,21 @@ __global__ __launch_bounds__(kWave) void window_chunk(const WindowArgs a) {
 // value-first slab is read in 64-byte pieces of 16 rows here (256 or 512 bytes
 // of a row token by token); with the touched-once hint on them the fp32 pool's
 // 637 us are 682 and the bf16 pool's 322 are 407.
-// Few waves (up to half a wave per SIMD) take 16 columns each and are bound by
-// the chain of latencies; 32 heads x 4 requests, fp32 pool, value-first:
+// Replay and window at once (for requests where they fit) hold 236 registers
+// for 156, which a bf16 pool's short windows gain by and an fp32 pool's do not
+// (96 heads x 256 requests, 4 tokens: bf16 value-first 430 -> 386, key-first
+// 435 -> 390; fp32 key-first 596 -> 751); windows of 8 do not fit (457 -> 570).
+// Few waves (up to half a wave per SIMD) take 16 columns each, replay and
+// window at once, and are bound by the chain of latencies; 32 heads x 4
+// requests, fp32 pool value-first, token by token / 8 at a time / at once:
 //   decode  2: 5.6 / 7.5   4: 7.7 / 7.8   8: 11.5 / 8.1
-//   window  2: 7.4 / 9.9   4: 11.1 / 10.1   8: 18.8 / 10.5
+//   window  2: 7.4 / 9.9 / 8.5   4: 11.1 / 10.1 / 8.8   8: 18.8 / 10.5
 constexpr int64_t kFewWaves = 512;   // 32-column waves: half a wave per SIMD
+constexpr int64_t kJointTo = 11;     // half tokens of a window
 
 template <bool SBF16, int LAYOUT>
-constexpr int64_t chunk_from(int window, bool few) {
-  if (few) return window ? 6 : 8;
-  if (SBF16) return LAYOUT == KDA_STATE_V_FIRST && !window ? 9 : 8;
+constexpr int64_t chunk_from(int window) {
+  if (SBF16) return window ? 6 : LAYOUT == KDA_STATE_V_FIRST ? 9 : 8;
   return LAYOUT == KDA_STATE_V_FIRST ? (window ? 14 : 24) : (window ? 10 : 12);
 }
 
@@ -928,11 +1144,15 @@ hipError_t launch_one(const WindowArgs& args, hipStream_t stream) {
                                                : reinterpret_cast<const void*>(&window_vfirst<DK, DV, QBF16, SBF16>);
   if constexpr (!kChannel && DK >= 32) {
     const bool few = nwg <= kFewWaves;
-    if (2 * static_cast<int64_t>(args.src[args.window].T) >= chunk_from<SBF16, LAYOUT>(args.window, few) * args.B) {
-      fn = reinterpret_cast<const void*>(&window_chunk<DK, DV, QBF16, SBF16, LAYOUT, 32>);
-      if (DV >= 32 && few) {
-        fn = reinterpret_cast<const void*>(&window_chunk<DK, DV, QBF16, SBF16, LAYOUT, 16>);
-        nwg *= 2;
+    const int64_t halves = 2 * static_cast<int64_t>(args.src[args.window].T), B = args.B;
+    if (few ? halves >= (args.window ? 5 : 8) * B : halves >= chunk_from<SBF16, LAYOUT>(args.window) * B) {
+      if (few) {
+        fn = reinterpret_cast<const void*>(&window_chunk<DK, DV, QBF16, SBF16, LAYOUT, 16, true>);
+        if (DV >= 32) nwg *= 2;
+      } else if (SBF16 && args.window && halves <= kJointTo * B) {
+        fn = reinterpret_cast<const void*>(&window_chunk<DK, DV, QBF16, SBF16, LAYOUT, 32, SBF16>);
+      } else {
+        fn = reinterpret_cast<const void*>(&window_chunk<DK, DV, QBF16, SBF16, LAYOUT, 32, false>);
       }
     }
   }

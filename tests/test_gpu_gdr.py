@@ -170,6 +170,39 @@ def test_long_window(torch_cuda, dk, dv, layout, qkv, state):
         state=state)
 
 
+@pytest.mark.parametrize("state", ["f32", "bf16"])
+@pytest.mark.parametrize("qkv", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 32), (32, 16)])
+def test_short_window(torch_cuda, dk, dv, layout, qkv, state):
+    run(torch_cuda, "window", f"short {dk}x{dv}", [1, 2, 0, 3, 1], replay=REPLAYS, dk=dk, dv=dv, layout=layout,
+        qkv=qkv, state=state)
+
+
+@pytest.mark.parametrize("m", range(0, 12))
+def test_replay_and_window_sizes(torch_cuda, m):
+    """Every number of replayed tokens with every window: those that fit go
+    through the state at once (m + 2 n <= 16 rows, m + n <= 11), the others
+    one after the other."""
+    n = list(range(0, 9))
+    for layout, state, qkv in (("v_first", "f32", "bf16"), ("k_first", "bf16", "bf16"), ("k_first", "f32", "f32")):
+        run(torch_cuda, "window", f"{m} replayed", n, replay=[(i, m) for i in n], H=1, HV=2, layout=layout,
+            state=state, qkv=qkv, seed=m)
+
+
+@pytest.mark.parametrize("entry", ["decode", "window"])
+@pytest.mark.parametrize("state", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("lo,hi", [(0, 2), (3, 5), (6, 9), (9, 20)])
+def test_many_requests(torch_cuda, entry, state, layout, lo, hi):
+    """More than half a wave per SIMD: the forms of large batches."""
+    rng = np.random.default_rng(lo)
+    lens = rng.integers(lo, hi + 1, size=44).tolist()
+    replay = [(int(rng.integers(0, 4)), int(rng.integers(0, hi + 1))) for _ in lens]
+    run(torch_cuda, entry, f"{lo}..{hi}", lens, replay=replay if entry == "window" else None, state=state,
+        layout=layout, seed=lo)
+
+
 @pytest.mark.parametrize("entry", ["decode", "window"])
 @pytest.mark.parametrize("H,HV", [(1, 1), (3, 3), (1, 6), (5, 15)])
 @pytest.mark.parametrize("layout", LAYOUTS)
