@@ -26,10 +26,10 @@
 // rows rsub + RPI i and EPL keys.
 //
 // Bound: the state's trip from HBM and back.  With one token a wave is almost
-// all state traffic (96 heads x 256 requests, fp32 pool: 535 us, 6.0 TB/s);
+// all state traffic (96 heads x 256 requests, fp32 pool: 512 us, 6.3 TB/s);
 // with windows the two sweeps per token (2 + 1 FMA per element) come into
-// view, and long ones with one decay per head go 8 tokens at a time
-// (window_chunk below).
+// view, and long ones with one decay per head go 8 tokens at a time, replay
+// and window together where that pays (window_chunk below).
 
 #include <hip/hip_runtime.h>
 
@@ -1129,6 +1129,34 @@ __global__ __launch_bounds__(kWave) void window_chunk(const WindowArgs a) {
 constexpr int64_t kFewWaves = 512;   // 32-column waves: half a wave per SIMD
 constexpr int64_t kJointTo = 11;     // half tokens of a window
 
+// Slabs in flight.  With one or two tokens a wave is a read, a little work and
+// a write, and a CU that holds 16 such waves mixes the reads and writes of too
+// many 16 KB slabs; LDS that nothing uses holds it to 8 or 6 of them.  No claim
+// / 13000 / 16000 / 23000 bytes, dk = dv = 128, us:
+//   f32 key-first, 96 heads x 256 requests, 1 token    534 / 526 / 521 / 512
+//   f32 value-first                                    558 / 558 / 547 / 532
+//   f32 key-first, 32 heads x 128 requests, 1 token    102 /  95 /  92 /  90
+//   f32 key-first, 96 heads x 256 requests, 2 tokens   543 / 528 / 526 / 522
+//   f32 key-first, the same, 4 tokens                  551 / 542 / 546 / 567
+//   bf16 key-first, 96 x 256, 1 token                  331 / 316 / 309 / 312
+//   bf16 value-first                                   275 / 261 / 258 / 267
+//   bf16 key-first, 32 x 128, 1 token                 54.6 /55.0 /54.2 /56.6
+//   bf16 key-first, 32 x 32, 1 token                  11.9 /14.4 /14.6 /15.7
+//   a window of 2 on f32 key-first, 96 x 256           541 / 528 / 527 / 538
+//   per-channel window of 1, f32 key-first             542 / 527 / 525 / 540
+// Longer windows and bf16 pools beyond one token are bound by the waves' own
+// work and lose by it (window of 4, f32 key-first, 572 / 603 / 641 / 709), and
+// so do launches of a few waves per CU, whose last waves then wait (2 tokens,
+// f32 value-first, 20 x 32 heads, 2560 waves: 13.9 none, 17.3 with 16000).
+template <int DK, int DV, bool SBF16>
+uint32_t idle_lds(const WindowArgs& args, int64_t nwg) {
+  if (DK != 128 || DV < 32) return 0;
+  const int64_t T = args.src[args.window].T, B = args.B;
+  if (SBF16) return !kChannel && !args.window && T <= B && nwg >= 16384 ? 16000 : 0;
+  if (T <= B && !kChannel) return nwg >= 4096 ? 23000 : 0;
+  return T <= (kChannel ? 1 : 2) * B && nwg >= 8192 ? 16000 : 0;
+}
+
 template <bool SBF16, int LAYOUT>
 constexpr int64_t chunk_from(int window) {
   if (SBF16) return window ? 6 : LAYOUT == KDA_STATE_V_FIRST ? 9 : 8;
@@ -1139,6 +1167,7 @@ template <int DK, int DV, bool QBF16, bool SBF16, int LAYOUT>
 hipError_t launch_one(const WindowArgs& args, hipStream_t stream) {
   constexpr int CW = DV < 32 ? DV : 32;
   int64_t nwg = static_cast<int64_t>(args.B) * args.HV * (DV / CW);
+  uint32_t lds = idle_lds<DK, DV, SBF16>(args, nwg);
   void* kargs[] = {const_cast<WindowArgs*>(&args)};
   const void* fn = LAYOUT == KDA_STATE_K_FIRST ? reinterpret_cast<const void*>(&window_kfirst<DK, DV, QBF16, SBF16>)
                                                : reinterpret_cast<const void*>(&window_vfirst<DK, DV, QBF16, SBF16>);
@@ -1146,6 +1175,7 @@ hipError_t launch_one(const WindowArgs& args, hipStream_t stream) {
     const bool few = nwg <= kFewWaves;
     const int64_t halves = 2 * static_cast<int64_t>(args.src[args.window].T), B = args.B;
     if (few ? halves >= (args.window ? 5 : 8) * B : halves >= chunk_from<SBF16, LAYOUT>(args.window) * B) {
+      lds = 0;
       if (few) {
         fn = reinterpret_cast<const void*>(&window_chunk<DK, DV, QBF16, SBF16, LAYOUT, 16, true>);
         if (DV >= 32) nwg *= 2;
@@ -1156,7 +1186,7 @@ hipError_t launch_one(const WindowArgs& args, hipStream_t stream) {
       }
     }
   }
-  return hipLaunchKernel(fn, dim3(static_cast<uint32_t>(nwg)), dim3(kWave), kargs, 0, stream);
+  return hipLaunchKernel(fn, dim3(static_cast<uint32_t>(nwg)), dim3(kWave), kargs, lds, stream);
 }
 
 using LaunchFn = hipError_t (*)(const WindowArgs&, hipStream_t);
