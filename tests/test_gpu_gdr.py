@@ -507,3 +507,48 @@ def test_prefill_infinite_gate_input(torch_cuda):
         b.tok.gate[10] = b.tok.gate[70] = b.tok.gate[71] = np.float32(np.inf)
     run(torch_cuda, "prefill", "closed gate", [100], H=1, HV=1, edit=edit)
     run(torch_cuda, "decode", "closed gate", [100], H=1, HV=1, edit=edit)
+
+
+@pytest.mark.parametrize("entry,channel,tokens", [("decode", False, 1), ("decode", False, 2), ("window", False, 1),
+                                                  ("window", False, 2), ("window", True, 1)])
+@pytest.mark.parametrize("state", ["float32", "bfloat16"])
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_large_batch_equals_its_parts(torch_cuda, layout, state, entry, channel, tokens):
+    """128 requests x 32 heads in one call, whose launch holds fewer waves per
+    CU, give bit for bit what calls of 16 requests give: requests do not meet."""
+    torch = torch_cuda
+    from gated_delta_rule_82_amd import kda
+    B, H, D, part = 128, 32, 128, 16
+    T = B * tokens
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def randn(*shape, dtype=torch.float32):
+        return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+    gate_tail = (H, D) if channel else (H,)
+    acts = [[randn(1, T, H, D, dtype=torch.bfloat16) for _ in range(3)] + [randn(1, T, *gate_tail), randn(1, T, H)]
+            for _ in range(2)]
+    par = [randn(H) * 0.3, randn(*gate_tail)]
+    pool0 = (randn(B, H, D, D) * 0.05).to(getattr(torch, state))
+    count = torch.randint(0, tokens + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+
+    def run_groups(size):
+        pool, outs = pool0.clone(), []
+        for b in range(0, B, size):
+            rows = slice(b * tokens, (b + size) * tokens)
+            x, y = ([t[:, rows] for t in a] for a in acts)
+            cu = torch.arange(0, (size + 1) * tokens, tokens, dtype=torch.int32, device="cuda")
+            idx = torch.arange(b, b + size, dtype=torch.int32, device="cuda")
+            out = torch.full_like(x[2], float("nan"))
+            call = [out, *x, *par, cu, pool, idx]
+            if entry == "window":
+                kda.decode_window(*call, *y[1:], cu[:-1].clone(), count[b:b + size].clone(), state_layout=layout)
+            else:
+                kda.gdr_decode(*call, state_layout=layout)
+            outs.append(out)
+        return torch.cat(outs, 1), pool
+
+    (o_all, s_all), (o_part, s_part) = run_groups(B), run_groups(part)
+    assert torch.isfinite(o_all.float()).all()
+    assert torch.equal(o_all, o_part) and torch.equal(s_all, s_part)
+    assert not torch.equal(s_all, pool0)
