@@ -312,10 +312,15 @@ __global__ __launch_bounds__(kWave) void verify_pick(const VerifyArgs a) {
     return;
   }
   const double bar = (u > 0.0f ? static_cast<double>(u) : 0.0) * total;
+  // u of one or more: the last token with mass, whatever the sums round to.
+  // Below that, only a segment with mass of its own can pass the bar: each
+  // lane's prefix rounds in an order of its own, so that of an empty segment
+  // may come out above its neighbours'.
+  const bool to_end = u >= 1.0f;
   double before = 0.0;   // mass of the segments before `seg`
   int64_t seg = -1;
-  const auto search = [&](int64_t s0, double sums) {
-    const uint64_t over = __ballot(before + sums > bar);
+  const auto search = [&](int64_t s0, double own, double sums) {
+    const uint64_t over = __ballot(own > 0.0 && before + sums > bar);
     if (over != 0) {
       const int at = __ffsll(static_cast<unsigned long long>(over)) - 1;
       seg = s0 + at;
@@ -326,9 +331,11 @@ __global__ __launch_bounds__(kWave) void verify_pick(const VerifyArgs a) {
   };
 #pragma unroll
   for (int i = 0; i < kHeld; ++i)
-    if (seg < 0) search(i * kWave, upto[i]);
-  for (int64_t s0 = kHeld * kWave; s0 < nseg && seg < 0; s0 += kWave)
-    search(s0, wave_scan(s0 + lane < nseg ? part[s0 + lane] : 0.0, lane));
+    if (seg < 0 && !to_end) search(i * kWave, held[i], upto[i]);
+  for (int64_t s0 = kHeld * kWave; s0 < nseg && seg < 0 && !to_end; s0 += kWave) {
+    const double x = s0 + lane < nseg ? part[s0 + lane] : 0.0;
+    search(s0, x, wave_scan(x, lane));
+  }
   const bool passes = seg >= 0;   // else the last token with mass
   if (!passes) seg = last;
   Row<BF16> row;

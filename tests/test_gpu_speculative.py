@@ -152,6 +152,31 @@ def test_verify_degenerate(torch_cuda, kind, V):
         check(torch_cuda, Case([4, 1, 3, 0, 6, 2], V, draft=False, seed=4, edit=_edit(kind)))
 
 
+@pytest.mark.parametrize("u", [1.0, 2.0 ** 60, 1.0 - 2.0 ** -24])
+def test_verify_scattered_mass_and_u_of_one(torch_cuda, u):
+    """Rows with a few tokens of mass far apart and of very different size, as
+    top-k leaves them: u of one (or more) gives the last of them.  The running
+    sums of these rows round above their total at segments without mass (found
+    with a model of the lane-wise scan), which must not be picked."""
+    torch = torch_cuda
+    print("[case] scattered mass", u, flush=True)
+    seeds = [2062, 8558, 10831, 11048, 13096, 13829, 14968, 16158, 18980, 22236, 22395, 22648, 23644, 24290, 25312]
+
+    def edit(c):
+        c.target[:] = 0
+        for t, seed in enumerate(seeds):
+            rng = np.random.default_rng(seed)
+            n = int(rng.integers(2, 40))
+            segment = np.sort(rng.choice(128, n, replace=False))
+            c.target[t, segment * 1024 + 500] = np.exp(9 * rng.standard_normal(n)).astype(np.float32)
+        c.u_sample[:] = np.float32(u)
+
+    c = Case([1] * len(seeds), 128 * 1024, draft=False, edit=edit)
+    _, x = check(torch, c)
+    if u >= 1:
+        np.testing.assert_array_equal(x, [np.nonzero(row)[0][-1] for row in c.target])
+
+
 def test_verify_metadata_out_of_range_stays_inside(torch_cuda):
     """cu_seqlens that breaks its precondition is clamped to the rows there are."""
     torch = torch_cuda
