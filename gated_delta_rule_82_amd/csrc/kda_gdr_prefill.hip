@@ -130,25 +130,27 @@ __device__ __forceinline__ void split_rows(const f32x4 (&x)[1], float one, h4& h
   lo = h4{l[0].x, l[0].y, l[1].x, l[1].y};
 }
 
-// The unit of a state column is 2^sig.  Moves it so that `bound`, a bound on
-// the column in it, comes into [2^13, 2^14), but not below 2^min; returns by
-// how many powers it moved.
+// The unit of a state column is 2^sig: the least one in which a bound on the
+// column, 2^e <= bound < 2^(e + 1), is below 2^14, but not below 2^kSigMin nor
+// 2^100 times smaller than the old one (the factors between them stay finite).
+// Bounds are handled by their exponents: a bound on v in the unit of a state
+// that is zero or tiny does not fit fp32.
 constexpr int kSigMin = -100;
-__device__ __forceinline__ int rescale(float bound, int& sig, int min) {
-  const int e = static_cast<int>(__float_as_uint(bound) >> 23) - 127;
-  int to = sig + e - 13;
+
+// floor(log2(x)) of a normal x > 0; -127 for zero and below the normal range.
+__device__ __forceinline__ int exponent(float x) { return static_cast<int>(__float_as_uint(x) >> 23) - 127; }
+
+__device__ __forceinline__ int unit_for(int e, int min) {
+  const int to = e - 13;
   min = min < kSigMin ? kSigMin : min;
-  to = to < min ? min : to;
-  const int d = to - sig;
-  sig = to;
-  return d;
+  return to < min ? min : to;
 }
 
-__device__ __forceinline__ float max16_32(float x) {   // over lanes that share lane % 16
-  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
-  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+__device__ __forceinline__ int max16_32(int x) {   // over lanes that share lane % 16
+  const auto p = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  x = max(static_cast<int>(p[0]), static_cast<int>(p[1]));
+  const auto q = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return max(static_cast<int>(q[0]), static_cast<int>(q[1]));
 }
 
 // A double moved within its row of 16 lanes (0 where none comes in), and
@@ -778,9 +780,8 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
     int third = 0;   // it % kRingP
 #pragma unroll
     for (int cs = 0; cs < NCS; ++cs) {
-      sig[cs] = 0;
-      const int d = rescale(max16_32(largest(S, cs)), sig[cs], kSigMin);
-      const float f = __builtin_ldexpf(1.0f, -d);
+      sig[cs] = unit_for(max16_32(exponent(largest(S, cs))), kSigMin);
+      const float f = __builtin_ldexpf(1.0f, -sig[cs]);
 #pragma unroll
       for (int j = 0; j < KB; ++j) S[j][cs] *= f;
     }
@@ -843,14 +844,18 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
 #pragma unroll
         for (int cs = 0; cs < NCS; ++cs) {
           constexpr float kRoot = DK == 128 ? 11.4f : DK == 64 ? 8.0f : 5.7f;
+          constexpr int kDown = 8;   // the bounds' exponents are taken 2^8 lower: no finite v or S overflows
           float m = 0.0f;
 #pragma unroll
           for (int rb = 0; rb < NB; ++rb)
 #pragma unroll
             for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(R[cs][rb][r]));
-          m = fmaxf(m * (__builtin_ldexpf(C + 1.0f, -sig[cs])), kRoot * largest(S, cs));
+          const int ev = exponent(m * (2.0f * (C + 1) / (1 << kDown)));
+          const int es = exponent(largest(S, cs) * (2.0f * kRoot / (1 << kDown))) + sig[cs];
           up_old[cs] = __builtin_ldexpf(1.0f, sig[cs]);
-          const int d = rescale(2.0f * max16_32(m), sig[cs], sig[cs] - 100);
+          const int to = unit_for(max16_32(max(ev, es)) + kDown, sig[cs] - 100);
+          const int d = to - sig[cs];
+          sig[cs] = to;
           shift[cs] = __builtin_ldexpf(1.0f, -d);   // 0 where the new unit dwarfs all of S
           keep[cs] = __builtin_ldexpf(last, -d);
           down[cs] = __builtin_ldexpf(1.0f, -sig[cs]);

@@ -497,6 +497,24 @@ def test_prefill_degenerate(torch_cuda, kind, qkv, layout):
     run(torch_cuda, "prefill", kind, [150, 5], H=1, HV=2, qkv=qkv, layout=layout, edit=edit, **kw)
 
 
+@pytest.mark.parametrize("qkv", ["f32", "bf16"])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64)])
+@pytest.mark.parametrize("kind", ["fresh state", "after zeros", "tiny state"])
+def test_prefill_large_v_over_nothing(torch_cuda, kind, dk, dv, qkv):
+    """Columns of v from 2^-60 to 2^100 over a state that is zero or far
+    smaller: fresh requests, a column whose v begins after several chunks, and a
+    state of size 2^-90."""
+    def edit(b):
+        size = np.float32(2.0) ** np.resize(np.array([0, 24, 32, 40, 64, 100, -60], dtype=np.float32), b.dv)
+        b.tok.v *= size.astype(np.float32)
+        if kind == "after zeros":
+            b.tok.v[:70, :, ::2] = 0
+        if kind == "tiny state":
+            b.pool[:] *= np.float32(2.0 ** -90)
+    run(torch_cuda, "prefill", kind, [150, 40, 3], H=1, HV=2, dk=dk, dv=dv, qkv=qkv, edit=edit,
+        sigma=1.0 if kind == "tiny state" else 0.0)
+
+
 def test_prefill_long(torch_cuda):
     run(torch_cuda, "prefill", "long", [3000], H=1, HV=1, layout="v_first")
 
