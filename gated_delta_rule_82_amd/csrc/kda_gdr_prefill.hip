@@ -21,13 +21,24 @@
 //     then is exact in fp16 (but for values below 2^-17 of the norm, off by
 //     at most 2^-25 of it), an fp32 row is taken as hi + lo, 22 bits;
 //   - the state, R = V - diag(e^G) Kh S0 and U are held in a unit 2^sig per
-//     value column, which keeps them below 2^14, and taken as hi + lo; T and P,
-//     whose entries are at most 1 in size, as hi + lo.
+//     value column, which keeps them below 2^15, and taken as hi + lo; T and P,
+//     whose entries are at most 1 in size, times 2^14 as hi + lo.
 // |T_ij| <= 1: T_ij = -beta_i kh_i^T [product of contractions] kh_j.  The
 // lo.lo terms (2^-22) are dropped.  So an operand carries about 22 bits and
 // the result is close to fp32's; two bf16 terms would leave 16 bits.  G is
 // kept as a sum of two floats (summed in fp64): only differences of it count
 // and an fp32 sum of strong decays loses them.
+//
+// Range.  hi + lo has the exponents of one fp16: beside the largest value of its
+// column and chunk (the bound X that the unit comes from) a value is off by up to
+// 2^-25 of the unit, 2^-39 X.  R, U and the K^T operand each bring one such rounding
+// in, so what a column holds at a token, M, has an error below 2^-20 M (decode's
+// bound is of that size) while X < 2^17 M.  M is taken as max |v| over a lane's group
+// of tokens, or what the chunk leaves of S0 if that is more.  Where a group is
+// smaller - an outlier beside small tokens, a large state that a gate closes - the
+// state wave takes the chunk token by token in fp32 (`wide` below): 19 us for 1.4
+// (16 columns).  Normal values do not come near that; v of which half is zero does in
+// one chunk of 25 (16384 tokens x 32 heads 0.7 -> 1.2 ms).
 //
 // Work split.  Value columns never interact, so a workgroup owns one
 // (request, value head) tile and NCW * 16 * NCS of its columns.  The chain
@@ -61,6 +72,8 @@ namespace {
 constexpr int kHelpers = 4;
 constexpr int kRing = 4;          // chunks of q and k held in LDS
 constexpr int kRingP = 3;         // of P, made a chunk later
+constexpr float kUnitT = 16384.0f;   // T and P are stored times this
+constexpr int kWide = 17;         // powers of two between a chunk's bound and its smallest group (`wide`)
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
@@ -131,17 +144,18 @@ __device__ __forceinline__ void split_rows(const f32x4 (&x)[1], float one, h4& h
 }
 
 // The unit of a state column is 2^sig: the least one in which a bound on the
-// column, 2^e <= bound < 2^(e + 1), is below 2^14, but not below 2^kSigMin nor
+// column, 2^e <= bound < 2^(e + 1), is below 2^15, but not below 2^kSigMin nor
 // 2^100 times smaller than the old one (the factors between them stay finite).
 // Bounds are handled by their exponents: a bound on v in the unit of a state
 // that is zero or tiny does not fit fp32.
 constexpr int kSigMin = -100;
 
-// floor(log2(x)) of a normal x > 0; -127 for zero and below the normal range.
-__device__ __forceinline__ int exponent(float x) { return static_cast<int>(__float_as_uint(x) >> 23) - 127; }
+// floor(log2(x)) + 127 of a normal x > 0; 0 for zero and below the normal range.
+constexpr int kBias = 127;
+__device__ __forceinline__ int exponent(float x) { return static_cast<int>(__float_as_uint(x) >> 23); }
 
-__device__ __forceinline__ int unit_for(int e, int min) {
-  const int to = e - 13;
+__device__ __forceinline__ int unit_for(int e, int min) {   // e biased
+  const int to = e - kBias - 14;
   min = min < kSigMin ? kSigMin : min;
   return to < min ? min : to;
 }
@@ -201,9 +215,9 @@ struct Shared {
   _Float16 t[2][2][NB][64][TK];                    // T hi, lo, beta included
   float a[2][2 * NB - 1][16][16];                  // A: blocks 00, 11, 10; row-major
   float join[NB][16][16];                          // diagonal blocks of (I + A)^-1, row-major
-  float norm_k[2][C], norm_q[2][C];                // kh = norm_k * stored row
+  float norm_k[kRing][C], norm_q[kRing][C];        // kh = norm_k * stored row
   float g_hi[2][C], g_lo[2][C], beta[2][C];
-  float tab[kRing][4][C];                          // beta; e^G norm_k; scale e^G norm_q; norm_k e^(last - G)
+  float tab[kRing][4][C];                          // 2^14 beta; e^G norm_k; scale e^G norm_q; norm_k e^(last - G)
   float last[kRing];                               // e^(G_last)
 };
 
@@ -485,8 +499,104 @@ struct Tile {
   int t0, n;                  // first row and tokens
 };
 
+// Log decay of a token: raw gate plus bias -> g, at least -200 (exp(-200) is 0 in
+// fp32, and sums stay finite).
+__device__ __forceinline__ float log_decay(const DecodeArgs& a, float x, float amp) {
+  const float g = a.gate_mode == KDA_GATE_SOFTPLUS ? -amp * softplus_f(x) : a.lower_bound * sigmoid_f(amp * x);
+  return g < -200.0f ? -200.0f : g;
+}
+
+// One chunk token by token, in fp32 and without a unit: with the decay applied
+// first, u = v - kh^T S, S += beta kh u^T, o = qh^T S = qh^T S_old + (qh.kh) beta u.
+// q and k come as the helpers left them in LDS.  A lane's keys are 16 j + 4 g + r.
+template <int KB, int NCS, int DK, bool F32>
+__device__ __forceinline__ void walk_chunk(const DecodeArgs& a, const Shared<DK, F32>& sh, const Tile& w, int ring,
+                                           int first, int n, __amdgpu_buffer_rsrc_t rv, __amdgpu_buffer_rsrc_t ro,
+                                           int voff, int stride, int lane, int (&sig)[NCS], f32x4 (&S)[KB][NCS]) {
+  const int g = lane / 16;
+  // the decay of token lane % C (row `first` of the request and on)
+  const int64_t row = static_cast<int64_t>(w.t0) + first + (lane % Shared<DK, F32>::C < n ? lane % Shared<DK, F32>::C : 0);
+  const float decays = exp_f(log_decay(a, a.raw_gate[row * a.HV + w.hv] + a.dt_bias[w.hv], exp_f(a.a_log[w.hv])));
+#pragma unroll
+  for (int cs = 0; cs < NCS; ++cs) {
+    const float f = __builtin_ldexpf(1.0f, sig[cs]);
+#pragma unroll
+    for (int j = 0; j < KB; ++j) S[j][cs] *= f;
+  }
+  Columns<F32, NCS> next;
+  next.load(rv, voff);
+#pragma unroll 1
+  for (int t = 0; t < n; ++t) {
+    float v[NCS];
+    next.unpack(v);
+    if (t + 1 < n) next.load(rv, voff + (t + 1) * stride);
+    const float alpha = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(decays), t));
+    const float nk = sh.norm_k[ring][t], nq = a.scale * sh.norm_q[ring][t];
+    const float beta = sh.tab[ring][0][t] * (1.0f / kUnitT);
+    float qk = 0.0f, ks[NCS], qs[NCS];
+#pragma unroll
+    for (int cs = 0; cs < NCS; ++cs) ks[cs] = qs[cs] = 0.0f;
+    h8 kr[F32 ? 2 : 1][DK / 32], qr[F32 ? 2 : 1][DK / 32];
+#pragma unroll
+    for (int term = 0; term < (F32 ? 2 : 1); ++term)
+#pragma unroll
+      for (int s = 0; s < DK / 32; ++s) {
+        kr[term][s] = *reinterpret_cast<const h8*>(&sh.k[ring][term][t / 16][s][row_slot(s, g, t % 16)][0]);
+        qr[term][s] = *reinterpret_cast<const h8*>(&sh.q[ring][term][t / 16][s][row_slot(s, g, t % 16)][0]);
+      }
+    const auto value = [](const auto& rows, int s, int e) {
+      if constexpr (F32) return static_cast<float>(rows[0][s][e]) + static_cast<float>(rows[1][s][e]);
+      else return static_cast<float>(rows[0][s][e]);
+    };
+#pragma unroll
+    for (int s = 0; s < DK / 32; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float k = value(kr, s, e), q = value(qr, s, e);
+        qk = fmaf(q, k, qk);
+#pragma unroll
+        for (int cs = 0; cs < NCS; ++cs) {
+          const float x = S[2 * s + e / 4][cs][e % 4] * alpha;
+          S[2 * s + e / 4][cs][e % 4] = x;
+          ks[cs] = fmaf(k, x, ks[cs]);
+          qs[cs] = fmaf(q, x, qs[cs]);
+        }
+      }
+    qk = swap16_add(qk, qk);
+    qk = swap32_add(qk, qk);
+    float write[NCS], o[NCS];
+#pragma unroll
+    for (int cs = 0; cs < NCS; ++cs) {
+      ks[cs] = swap16_add(ks[cs], ks[cs]);
+      ks[cs] = swap32_add(ks[cs], ks[cs]);
+      qs[cs] = swap16_add(qs[cs], qs[cs]);
+      qs[cs] = swap32_add(qs[cs], qs[cs]);
+      write[cs] = beta * nk * fmaf(-nk, ks[cs], v[cs]);
+      o[cs] = nq * fmaf(qk, write[cs], qs[cs]);
+    }
+#pragma unroll
+    for (int s = 0; s < DK / 32; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float k = value(kr, s, e);
+#pragma unroll
+        for (int cs = 0; cs < NCS; ++cs) S[2 * s + e / 4][cs][e % 4] = fmaf(k, write[cs], S[2 * s + e / 4][cs][e % 4]);
+      }
+    if (g == 0) Columns<F32, NCS>::store(ro, voff + t * stride, o);
+  }
+#pragma unroll
+  for (int cs = 0; cs < NCS; ++cs) {
+    sig[cs] = unit_for(max16_32(exponent(largest(S, cs))), kSigMin);
+    const float f = __builtin_ldexpf(1.0f, -sig[cs]);
+#pragma unroll
+    for (int j = 0; j < KB; ++j) S[j][cs] *= f;
+  }
+}
+
+// At dk = 32 two workgroups fit a CU where they hold up to 128 registers (128
+// columns, 8 prompts x 1024 tokens x 96 heads: 159 us with 126 and 188 with 131).
 template <int NCW, int NCS, int DK, bool F32>
-__global__ void __launch_bounds__((NCW + kHelpers) * kWave, 1)
+__global__ void __launch_bounds__((NCW + kHelpers) * kWave, DK == 32 ? 4 : 1)
 gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_bf16) {
   constexpr int KS = DK / 32;          // key steps of 32
   constexpr int KB = DK / 16;          // key blocks of 16
@@ -580,14 +690,11 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
         }
         const int ring = c % kRing, two = c % 2;
         if (role == 0) {
-          convert_rows<DK, F32, true>(cur, a.l2_eps, lane, sh.k[ring], sh.kt[ring], sh.norm_k[two]);
+          convert_rows<DK, F32, true>(cur, a.l2_eps, lane, sh.k[ring], sh.kt[ring], sh.norm_k[ring]);
         } else {
-          convert_rows<DK, F32, false>(cur, a.l2_eps, lane, sh.q[ring], nullptr, sh.norm_q[two]);
+          convert_rows<DK, F32, false>(cur, a.l2_eps, lane, sh.q[ring], nullptr, sh.norm_q[ring]);
           const bool live = c * C + tl < w.n;
-          const float x = gb.x + bias;
-          float gv = a.gate_mode == KDA_GATE_SOFTPLUS ? -amp * softplus_f(x) : a.lower_bound * sigmoid_f(amp * x);
-          gv = gv < -200.0f ? -200.0f : gv;   // exp(-200) is 0 in fp32, and sums stay finite
-          double sum = live ? static_cast<double>(gv) : 0.0;
+          double sum = live ? static_cast<double>(log_decay(a, gb.x + bias, amp)) : 0.0;
           sum += dpp_f64<0x111>(sum);   // row_shr 1, 2, 4, 8: zero comes in
           sum += dpp_f64<0x112>(sum);
           sum += dpp_f64<0x114>(sum);
@@ -648,10 +755,10 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
           const int i = m > 0, j = m == 1;
           const int row = 16 * i + lane % 16, col = 16 * j + 4 * g;
           const float gh = sh.g_hi[two][row], gl = sh.g_lo[two][row];
-          const float nq = sh.norm_q[two][row], nk = sh.norm_k[two][row] * sh.beta[two][row];
+          const float nq = kUnitT * sh.norm_q[ring][row], nk = sh.norm_k[ring][row] * sh.beta[two][row];
           const f32x4 ch = *reinterpret_cast<const f32x4*>(&sh.g_hi[two][col]);
           const f32x4 cl = *reinterpret_cast<const f32x4*>(&sh.g_lo[two][col]);
-          const f32x4 ck = *reinterpret_cast<const f32x4*>(&sh.norm_k[two][col]);
+          const f32x4 ck = *reinterpret_cast<const f32x4*>(&sh.norm_k[ring][col]);
           f32x4 y;
           float x[4];
 #pragma unroll
@@ -673,11 +780,11 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
         }
         if (lane < C) {
           const float gh = sh.g_hi[two][lane], gl = sh.g_lo[two][lane];
-          const float nk = sh.norm_k[two][lane], be = sh.beta[two][lane];
+          const float nk = sh.norm_k[ring][lane];
           const float eg = exp_f(gh + gl);
-          sh.tab[ring][0][lane] = be;
+          sh.tab[ring][0][lane] = kUnitT * sh.beta[two][lane];
           sh.tab[ring][1][lane] = eg * nk;
-          sh.tab[ring][2][lane] = a.scale * eg * sh.norm_q[two][lane];
+          sh.tab[ring][2][lane] = a.scale * eg * sh.norm_q[ring][lane];
           sh.tab[ring][3][lane] = nk * exp_f((g_last - gh) + (g_last_lo - gl));
           if (lane == C - 1) sh.last[ring] = eg;
         }
@@ -765,6 +872,9 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
                            dv * E);
     };
     Columns<F32, NCS> v[NB][4];
+    // a last chunk's groups of less than four tokens go with the one before, if there
+    // is one: an exponent that is not the smallest
+    const int past = g > 0 && 4 * g + 4 > w.n - (chunks - 1) * C ? 512 : 0;
     auto load_v = [&](int c) {
       const __amdgpu_buffer_rsrc_t r0 = chunk_rows(a.v, c);
 #pragma unroll
@@ -773,7 +883,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
         for (int r = 0; r < 4; ++r) v[rb][r].load(r0, voff[rb][r]);
     };
     load_v(0);
-    // S of column cs is held divided by 2^sig[cs], below 2^14 in size
+    // S of column cs is held divided by 2^sig[cs], below 2^15 in size
     int sig[NCS];
     float one = 1.0f;
     asm("" : "+s"(one));
@@ -795,30 +905,65 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
         for (int rb = 0; rb < NB; ++rb)
 #pragma unroll
           for (int cs = 0; cs < NCS; ++cs) ks[rb][cs] = qs[rb][cs] = f32x4{0, 0, 0, 0};
+        if constexpr (NCS == 1) {
+          // Operands are read and S is split a step ahead of the products, and products
+          // into one accumulator stand apart (one prompt of 16384 tokens x 32 heads 737 ->
+          // 671 us; with two column sets, as below, the products stand apart by themselves
+          // and this costs 1%).
+          h8 kr[2][TERMS][NB], qr[2][TERMS][NB], hi[2][NCS], lo[2][NCS];
+          const auto stage = [&](int s) {
+            const int at = row_slot(s, g, lane % 16);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          h8 hi[NCS], lo[NCS];
+            for (int term = 0; term < TERMS; ++term)
 #pragma unroll
-          for (int cs = 0; cs < NCS; ++cs) split8(S[2 * s][cs], S[2 * s + 1][cs], one, hi[cs], lo[cs]);
-          const int at = row_slot(s, g, lane % 16);
+              for (int rb = 0; rb < NB; ++rb) {
+                kr[s % 2][term][rb] = *reinterpret_cast<const h8*>(&sh.k[ring][term][rb][s][at][0]);
+                qr[s % 2][term][rb] = *reinterpret_cast<const h8*>(&sh.q[ring][term][rb][s][at][0]);
+              }
 #pragma unroll
-          for (int rb = 0; rb < NB; ++rb) {
-            const h8 k0 = *reinterpret_cast<const h8*>(&sh.k[ring][0][rb][s][at][0]);
-            const h8 q0 = *reinterpret_cast<const h8*>(&sh.q[ring][0][rb][s][at][0]);
+            for (int cs = 0; cs < NCS; ++cs) split8(S[2 * s][cs], S[2 * s + 1][cs], one, hi[s % 2][cs], lo[s % 2][cs]);
+          };
+          stage(0);
 #pragma unroll
-            for (int cs = 0; cs < NCS; ++cs) {
-              ks[rb][cs] = mfma(k0, hi[cs], ks[rb][cs]);
-              qs[rb][cs] = mfma(q0, hi[cs], qs[rb][cs]);
-              ks[rb][cs] = mfma(k0, lo[cs], ks[rb][cs]);
-              qs[rb][cs] = mfma(q0, lo[cs], qs[rb][cs]);
-            }
-            if constexpr (F32) {
-              const h8 k1 = *reinterpret_cast<const h8*>(&sh.k[ring][1][rb][s][at][0]);
-              const h8 q1 = *reinterpret_cast<const h8*>(&sh.q[ring][1][rb][s][at][0]);
+          for (int s = 0; s < KS; ++s) {
+            if (s + 1 < KS) stage(s + 1);
+#pragma unroll
+            for (int part = 0; part < TERMS + 1; ++part)   // hi hi, hi lo, lo hi
+#pragma unroll
+              for (int cs = 0; cs < NCS; ++cs)
+#pragma unroll
+                for (int rb = 0; rb < NB; ++rb) {
+                  const h8 x = part == 1 ? lo[s % 2][cs] : hi[s % 2][cs];
+                  ks[rb][cs] = mfma(kr[s % 2][part == 2 ? TERMS - 1 : 0][rb], x, ks[rb][cs]);
+                  qs[rb][cs] = mfma(qr[s % 2][part == 2 ? TERMS - 1 : 0][rb], x, qs[rb][cs]);
+                }
+          }
+        } else {
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            h8 hi[NCS], lo[NCS];
+#pragma unroll
+            for (int cs = 0; cs < NCS; ++cs) split8(S[2 * s][cs], S[2 * s + 1][cs], one, hi[cs], lo[cs]);
+            const int at = row_slot(s, g, lane % 16);
+#pragma unroll
+            for (int rb = 0; rb < NB; ++rb) {
+              const h8 k0 = *reinterpret_cast<const h8*>(&sh.k[ring][0][rb][s][at][0]);
+              const h8 q0 = *reinterpret_cast<const h8*>(&sh.q[ring][0][rb][s][at][0]);
 #pragma unroll
               for (int cs = 0; cs < NCS; ++cs) {
-                ks[rb][cs] = mfma(k1, hi[cs], ks[rb][cs]);
-                qs[rb][cs] = mfma(q1, hi[cs], qs[rb][cs]);
+                ks[rb][cs] = mfma(k0, hi[cs], ks[rb][cs]);
+                qs[rb][cs] = mfma(q0, hi[cs], qs[rb][cs]);
+                ks[rb][cs] = mfma(k0, lo[cs], ks[rb][cs]);
+                qs[rb][cs] = mfma(q0, lo[cs], qs[rb][cs]);
+              }
+              if constexpr (F32) {
+                const h8 k1 = *reinterpret_cast<const h8*>(&sh.k[ring][1][rb][s][at][0]);
+                const h8 q1 = *reinterpret_cast<const h8*>(&sh.q[ring][1][rb][s][at][0]);
+#pragma unroll
+                for (int cs = 0; cs < NCS; ++cs) {
+                  ks[rb][cs] = mfma(k1, hi[cs], ks[rb][cs]);
+                  qs[rb][cs] = mfma(q1, hi[cs], qs[rb][cs]);
+                }
               }
             }
           }
@@ -830,7 +975,10 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
         // 2 max(sqrt(dk) max|S0|, (C + 1) max|v|) covers them all.
         const float last = sh.last[ring];
         f32x4 R[NCS][NB], U[NCS][NB];
-        float keep[NCS], up_old[NCS], up_new[NCS], down[NCS], shift[NCS];
+        int to[NCS];
+        bool wide = false;
+        const int last_log = exponent(last) - kBias;
+        const int past_now = it == chunks - 1 ? past : 0;
 #pragma unroll
         for (int cs = 0; cs < NCS; ++cs)
 #pragma unroll
@@ -844,22 +992,45 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
 #pragma unroll
         for (int cs = 0; cs < NCS; ++cs) {
           constexpr float kRoot = DK == 128 ? 11.4f : DK == 64 ? 8.0f : 5.7f;
+          constexpr int kRootLog = DK == 128 ? 3 : 4;   // floor(-log2(2 kRoot / 2^kDown))
+          constexpr int kTopLog = NB == 2 ? 1 : 2;      // floor(-log2(2 (C + 1) / 2^kDown))
           constexpr int kDown = 8;   // the bounds' exponents are taken 2^8 lower: no finite v or S overflows
-          float m = 0.0f;
+          float m = 0.0f;            // max |v| of the lane's group of tokens
 #pragma unroll
           for (int rb = 0; rb < NB; ++rb)
 #pragma unroll
             for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(R[cs][rb][r]));
           const int ev = exponent(m * (2.0f * (C + 1) / (1 << kDown)));
           const int es = exponent(largest(S, cs) * (2.0f * kRoot / (1 << kDown))) + sig[cs];
+          const int e = max16_32(max(ev, es));
+          to[cs] = unit_for(e + kDown, sig[cs] - 100);
+          // max |S| of the lane's keys and max |v| of its group, rounded down, by how much
+          // they exceed a state of zero (-1: it is one).  S0 as the chunk's decay leaves
+          // it bounds a group from below; a group without v goes with S0, and gives zero
+          // where that is zero.
+          constexpr int kNone = kSigMin + kRootLog + 1;
+          const int s0 = es + kRootLog - kNone, v0 = ev + kTopLog + past_now - kNone;
+          const int from_s = ev == 0 ? s0 : max(s0 + last_log, 0);
+          const uint32_t least = max(max(static_cast<uint32_t>(v0), static_cast<uint32_t>(from_s)),
+                                     static_cast<uint32_t>(kSigMin + kBias + 1 - kNone));
+          // The old unit counts like the bound that it came from (twice, for the sum over
+          // keys), as S is split in it.
+          wide |= least <= static_cast<uint32_t>(max(e, sig[cs] + kBias + 15 - kDown) - (kWide - kDown) - kNone);
+        }
+        // A chunk that goes token by token runs through the lines below as well, with S
+        // kept as it is, so that the others need not wait for this verdict; its outputs
+        // are overwritten.
+        const bool walks = __any(wide);   // uniform
+        const float scale_u = walks ? 0.0f : 1.0f / kUnitT;
+        float keep[NCS], up_old[NCS], up_new[NCS], down[NCS], shift[NCS];
+#pragma unroll
+        for (int cs = 0; cs < NCS; ++cs) {
+          const int d = to[cs] - sig[cs];
           up_old[cs] = __builtin_ldexpf(1.0f, sig[cs]);
-          const int to = unit_for(max16_32(max(ev, es)) + kDown, sig[cs] - 100);
-          const int d = to - sig[cs];
-          sig[cs] = to;
           shift[cs] = __builtin_ldexpf(1.0f, -d);   // 0 where the new unit dwarfs all of S
-          keep[cs] = __builtin_ldexpf(last, -d);
-          down[cs] = __builtin_ldexpf(1.0f, -sig[cs]);
-          up_new[cs] = __builtin_ldexpf(1.0f, sig[cs]);
+          keep[cs] = walks ? 1.0f : __builtin_ldexpf(last, -d);
+          down[cs] = __builtin_ldexpf(1.0f, -to[cs]);
+          up_new[cs] = __builtin_ldexpf(1.0f / kUnitT, to[cs]);
         }
         // R = v - e^G kh^T S, in the new unit (zero past the end)
 #pragma unroll
@@ -884,9 +1055,11 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
             f32x4 acc = {0, 0, 0, 0};
             acc = mfma(t0l, hi, acc);
             acc = mfma(t0h, lo, acc);
-            U[cs][rb] = mfma(t0h, hi, acc);
+            U[cs][rb] = mfma(t0h, hi, acc) * scale_u;
           }
         }
+#pragma unroll
+        for (int cs = 0; cs < NCS; ++cs) sig[cs] = walks ? sig[cs] : to[cs];
         // S = e^(G_last) S + (diag(e^(G_last - G)) Kh)^T U
 #pragma unroll
         for (int cs = 0; cs < NCS; ++cs) {
@@ -935,6 +1108,13 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
             for (int cs = 0; cs < NCS; ++cs) x[cs] = qs[rb][cs][r];
             Columns<F32, NCS>::store(ro, voff[rb][r], x);
           }
+        if (__builtin_expect(walks, 0)) {
+          constexpr int kVmcnt0 = 0x0f70;   // the stores above are done; and no load of the walk is counted on below
+          __builtin_amdgcn_s_waitcnt(kVmcnt0);
+          walk_chunk<KB, NCS, DK, F32>(a, sh, w, ring, it * C, min(w.n - it * C, C), chunk_rows(a.v, it), ro,
+                                       voff[0][0] - 4 * g * stride, stride, lane, sig, S);
+          __builtin_amdgcn_s_waitcnt(kVmcnt0);
+        }
         third = third == kRingP - 1 ? 0 : third + 1;
       }
       lds_barrier();

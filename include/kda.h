@@ -261,12 +261,18 @@ int kda_gdr_decode(const kda_tensor* out, const kda_tensor* q, const kda_tensor*
  * kda_gdr_prefill - kda_gdr_decode's operation and arguments for whole
  * prompts, in chunks of 32 tokens on the matrix cores; the result equals the
  * token-by-token recurrence up to rounding order, with operands of about 22
- * significant bits and fp32 sums.  No workspace.  dk and dv must each be 32,
- * 64 or 128, T at most 2^31 - 65, B * HV at most 2^23 - 1 and
- * HV * max(dk, dv) below 2^24 (else KDA_ERR_UNSUPPORTED).  Where
- * kda_gdr_decode gives an infinity or NaN from some token on (non-finite
- * inputs, or an overflow), this call may give it from up to 31 tokens
- * earlier: the tokens of a chunk meet in its products.
+ * significant bits and fp32 sums.  An output's error is relative to what its
+ * column holds at that token, |S| and |v|, as kda_gdr_decode's is; but |v|
+ * counts over a group of eight tokens (of every 32 from the request's start,
+ * tokens 4i .. 4i+3 and 16+4i .. 16+4i+3; with less than four of them at the
+ * end, over the group before as well), and |S| undecayed through groups whose
+ * v is all zero.  A chunk of 32 tokens with groups smaller than about 2^-11 of
+ * its largest |v| or |S| is computed token by token, which takes some 14
+ * times as long.  No workspace.  dk and dv must each be 32, 64 or 128, T at
+ * most 2^31 - 65, B * HV at most 2^23 - 1 and HV * max(dk, dv) below 2^24
+ * (else KDA_ERR_UNSUPPORTED).  Where kda_gdr_decode gives an infinity or NaN
+ * from some token on (non-finite inputs, or an overflow), this call may give
+ * it from up to 31 tokens earlier: the tokens of a chunk meet in its products.
  */
 int kda_gdr_prefill(const kda_tensor* out, const kda_tensor* q, const kda_tensor* k,
                     const kda_tensor* v, const kda_tensor* raw_gate,
