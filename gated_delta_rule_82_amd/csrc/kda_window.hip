@@ -1049,10 +1049,10 @@ __global__ __launch_bounds__(kWave) void window_chunk(const WindowArgs a) {
     for (int i = 0; i < kW; ++i) {
       float v[1];
       vw[i].unpack(v);
-      float acc = i < n ? fmaf(sh.beta[i], v[0], -sh.lead[i] * sh.dots[i][c]) : 0.0f;
+      float acc = fmaf(sh.beta[i], v[0], -sh.lead[i] * sh.dots[i][c]);
 #pragma unroll
       for (int k = 0; k < i; ++k) acc = fmaf(-sh.coef[i][k], U[k], acc);
-      U[i] = acc;
+      U[i] = i < n ? acc : 0.0f;   // not 0 * U[k], where a token before is not finite
     }
     if (outputs) {
 #pragma unroll

@@ -190,3 +190,37 @@ def test_ordinary_tokens(torch_cuda, entry, qkv, dk, dv):
     for seed in range(3):
         check(torch_cuda, entry, "ordinary", LENS + [200], H=1, HV=2, dk=dk, dv=dv, qkv=qkv, seed=seed,
               sigma=[0.0, 0.05, 2.0][seed])
+
+
+@pytest.mark.parametrize("entry", ["decode", "window"])
+@pytest.mark.parametrize("n", [1, 5, 8, 11])
+@pytest.mark.parametrize("requests", [2, 44])
+def test_infinite_v_in_the_last_token(torch_cuda, entry, n, requests):
+    """A last token with v = inf in one column leaves that column of the state at
+    infinities of the keys' signs, token by token and several tokens at a time; all
+    other columns stay exact."""
+    torch = torch_cuda
+    print("[case] infinite v", entry, n, requests, flush=True)
+    col = 5
+
+    def edit(b):
+        tok, ends = (b.rep, [a + c - 1 for a, c in b.replay]) if entry == "window" else (b.tok, b.cu[1:] - 1)
+        for t in ends:
+            tok.v[t, :, col] = np.inf
+
+    b = Batch(torch, [n] * requests, H=1, HV=2, layout="v_first", edit=edit,
+              replay=[(i * n, n) for i in range(requests)] if entry == "window" else None)
+    d = b.device()
+    b.call(entry, d)
+    torch.cuda.synchronize()
+    pool = b.host_pool(d)
+    tok = b.rep if entry == "window" else b.tok
+    rest = np.arange(128) != col
+    for r in {0, requests - 1}:
+        rows = range(r * n, r * n + n)
+        for hv in range(2):
+            tok.v[rows[-1], hv, col] = 0
+            S, _, m = R.walk(b.pool[b.slots[r], hv], tok, b.par, hv, rows, 2)
+            got = pool[b.slots[r], hv]
+            R.check_state(got[:, rest], S[:, rest], m[rest], n, False, f"{entry} request {r} head {hv}")
+            np.testing.assert_array_equal(got[:, col], np.sign(tok.k[rows[-1], 0]) * np.inf)
