@@ -2,10 +2,11 @@
 
 Every step of every operator runs in the HIP library; this module checks that
 torch tensors can be passed, hands them with the current HIP stream to the
-library (through a small extension, csrc/kda_binding.cpp, that turns them into
-``kda_tensor`` descriptors) and raises :class:`KdaError` on a nonzero status.
+library and raises :class:`KdaError` on a nonzero status.  A small extension
+(csrc/kda_binding.cpp) turns tensors into ``kda_tensor`` descriptors; where it
+is not built or does not fit the torch that is installed, ctypes does the same.
 The ``call_raw*`` functions call the C ABI on descriptors made here.  There is
-no fallback: if a library is missing or a tensor is not on a GPU, the call
+no fallback: if the library is missing or a tensor is not on a GPU, the call
 raises.
 """
 from __future__ import annotations
@@ -87,7 +88,7 @@ class KdaLibraryMissing(RuntimeError):
 _lib: Optional[ctypes.CDLL] = None
 _torch = None          # set by library()
 _raw_stream = None
-_native = None         # the extension's call()
+_native = None         # the extension's call(), or the same through ctypes; set by the first call
 _ENTRY = {}            # entry point -> its address
 
 
@@ -100,12 +101,11 @@ def library() -> ctypes.CDLL:
     global _lib
     if _lib is not None:
         return _lib
-    for path in (LIB_PATH, BINDING_PATH):
-        if not os.path.exists(path):
-            raise KdaLibraryMissing(
-                f"{path} is not built; run `python -m gated_delta_rule_82_amd.build`")
+    if not os.path.exists(LIB_PATH):
+        raise KdaLibraryMissing(
+            f"{LIB_PATH} is not built; run `python -m gated_delta_rule_82_amd.build`")
     import torch  # (binds the process to torch's HIP runtime first)
-    global _torch, _raw_stream, _native
+    global _torch, _raw_stream
     _torch = torch
     # the current stream's handle without a Stream object (microseconds of a short call)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -134,10 +134,6 @@ def library() -> ctypes.CDLL:
     lib.kda_abi_version.restype = ctypes.c_int
     _ENTRY.update({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
                    for name in EXPORTED_SYMBOLS})
-    spec = importlib.util.spec_from_file_location("_kda_binding", BINDING_PATH)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
-    _native = module.call
     _lib = lib
     return lib
 
@@ -267,6 +263,51 @@ def _device(t, name):
     return dev
 
 
+def _load_native():
+    """Set ``_native``: the extension's call(), which is tied to this torch's and
+    this Python's ABI, or, where it is not built or does not load, its like below."""
+    global _native
+    _native = _described_call
+    if os.path.exists(BINDING_PATH):
+        try:
+            spec = importlib.util.spec_from_file_location("_kda_binding", BINDING_PATH)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            _native = module.call
+        except ImportError:
+            pass
+
+
+def _described_call(kind, entry, tensors, dev, gate_mode, lower_bound, l2_eps, scale, state_layout, matmul, stream):
+    """The extension's call() on descriptors made here (some ten microseconds
+    more a call): the entry point's status, or None if a tensor cannot be passed."""
+    described = []
+    for i, t in enumerate(tensors):
+        if t is None and kind == _VERIFY and i == 3:
+            described.append(None)
+            continue
+        try:
+            d = _descriptor(t, "tensor")
+        except (TypeError, ValueError):
+            return None
+        if t.device.index != dev:
+            return None
+        described.append(d)
+    mode = KdaMode(gate_mode, lower_bound, l2_eps, scale, state_layout)
+    where = next(n for n, address in _ENTRY.items() if address == entry)
+    if kind == _CONV:
+        return call_raw_conv(described[0], KdaConv(*described[1:12]), described[12:], mode, stream)
+    if kind == _WINDOW:
+        return call_raw_window(described[:11], KdaReplay(*described[11:]), mode, stream)
+    if kind == _VERIFY:
+        return call_raw_verify(described, stream)
+    if kind == _PREFILL:
+        return call_raw_prefill(described, mode, matmul, stream)
+    if where == "kda_decode":
+        return call_raw(described, mode, stream)
+    return call_raw_gdr(described, mode, where == "kda_gdr_prefill", stream)
+
+
 def _call(kind, where, tensors, names, dev, stream, gate_mode=0, lower_bound=0.0, l2_eps=0.0, scale=0.0,
           state_layout=0, matmul=0):
     """Call entry point ``where`` with GPU ``dev`` current, on ``stream`` or torch's current one."""
@@ -274,6 +315,8 @@ def _call(kind, where, tensors, names, dev, stream, gate_mode=0, lower_bound=0.0
         with _torch.cuda.device(dev):
             return _call(kind, where, tensors, names, dev, stream, gate_mode, lower_bound, l2_eps, scale,
                          state_layout, matmul)
+    if _native is None:
+        _load_native()
     gm = GATE_MODES[gate_mode] if isinstance(gate_mode, str) else int(gate_mode)
     sl = STATE_LAYOUTS[state_layout] if isinstance(state_layout, str) else int(state_layout)
     rc = _native(kind, _ENTRY[where], tensors, dev, gm, lower_bound, l2_eps, scale, sl, matmul,
