@@ -111,20 +111,16 @@ def library() -> ctypes.CDLL:
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
     lib = ctypes.CDLL(LIB_PATH, mode=ctypes.RTLD_LOCAL)
-    P = ctypes.c_void_p   # tensors and structs go by address
-    lib.kda_decode.argtypes = [P] * 13
-    lib.kda_decode.restype = ctypes.c_int
-    lib.kda_decode_conv.argtypes = [P] * 11
-    lib.kda_decode_conv.restype = ctypes.c_int
-    lib.kda_prefill.argtypes = [P] * 12 + [ctypes.c_int32, P]
-    lib.kda_prefill.restype = ctypes.c_int
-    for fn in (lib.kda_gdr_decode, lib.kda_gdr_prefill):
-        fn.argtypes = [P] * 13
-        fn.restype = ctypes.c_int
-    lib.kda_decode_window.argtypes = [P] * 14
-    lib.kda_decode_window.restype = ctypes.c_int
-    lib.kda_verify.argtypes = [P] * 10
-    lib.kda_verify.restype = ctypes.c_int
+    T, M, stream = ctypes.POINTER(KdaTensor), ctypes.POINTER(KdaMode), ctypes.c_void_p
+    lib.kda_decode.argtypes = [T] * 11 + [M, stream]
+    lib.kda_decode_conv.argtypes = [T, ctypes.POINTER(KdaConv)] + [T] * 7 + [M, stream]
+    lib.kda_prefill.argtypes = [T] * 11 + [M, ctypes.c_int32, stream]
+    lib.kda_gdr_decode.argtypes = lib.kda_gdr_prefill.argtypes = [T] * 11 + [M, stream]
+    lib.kda_decode_window.argtypes = [T] * 11 + [ctypes.POINTER(KdaReplay), M, stream]
+    lib.kda_verify.argtypes = [T] * 9 + [stream]
+    for name in ("kda_decode", "kda_decode_conv", "kda_prefill", "kda_gdr_decode", "kda_gdr_prefill",
+                 "kda_decode_window", "kda_verify"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.kda_check_host.argtypes = [ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32),
                                    ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]
     lib.kda_check_host.restype = ctypes.c_int

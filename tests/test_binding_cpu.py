@@ -58,3 +58,21 @@ def test_extension_loads_where_it_is_built():
     copy.library()
     copy._load_native()
     assert copy._native is not copy._described_call
+
+
+def test_entry_points_take_structs_and_check_their_types():
+    """The entry points of library() take descriptors themselves, by reference or as
+    pointers, and refuse a struct of another type."""
+    lib = kda.library()
+    t, mode = kda.raw_tensor(0x10000, kda.KDA_F32, (3,)), kda.make_mode()
+    by_kind = {"kda_decode": [t] * 11 + [mode, None], "kda_prefill": [t] * 11 + [mode, 0, None],
+               "kda_gdr_decode": [t] * 11 + [mode, None], "kda_gdr_prefill": [t] * 11 + [mode, None],
+               "kda_decode_window": [t] * 11 + [kda.KdaReplay(), mode, None],
+               "kda_decode_conv": [t, kda.KdaConv()] + [t] * 7 + [mode, None], "kda_verify": [t] * 9 + [None]}
+    for name, args in by_kind.items():
+        fn = getattr(lib, name)
+        refs = [ctypes.byref(a) if isinstance(a, ctypes.Structure) else a for a in args]
+        pointers = [ctypes.pointer(a) if isinstance(a, ctypes.Structure) else a for a in args]
+        assert fn(*args) == fn(*refs) == fn(*pointers) < 0, name
+        with pytest.raises(ctypes.ArgumentError):
+            fn(*[ctypes.byref(mode)] * 2, *args[2:])
