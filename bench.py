@@ -67,8 +67,8 @@ HBM_PEAK_GBPS = 8000.0
 MATRIX_PEAK_TFLOPS = {"split_bf16": 2500.0, "f32": 157.3}   # dense bf16 / fp32 matrix
 CSRC = os.path.join(ROOT, "gated_delta_rule_82_amd", "csrc")
 KERNEL_SOURCES = {
-    "kda_decode": [os.path.join(CSRC, "kda_decode.hip"), os.path.join(CSRC, "kda_device.h")],
-    "kda_prefill": [os.path.join(CSRC, "kda_prefill.hip"), os.path.join(CSRC, "kda_device.h")],
+    "kda_decode": [os.path.join(CSRC, n) for n in ("kda_decode.hip", "kda_tile.h", "kda_device.h")],
+    "kda_prefill": [os.path.join(CSRC, n) for n in ("kda_prefill.hip", "kda_device.h")],
 }
 PROFILES = os.path.join(ROOT, "profiles")
 CHUNK = 16
