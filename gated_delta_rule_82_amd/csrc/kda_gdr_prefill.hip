@@ -1148,17 +1148,23 @@ hipError_t launch_form(const DecodeArgs& args, int dv, int layout, int state_bf1
   return hipLaunchKernel(fn, dim3(static_cast<uint32_t>(nwg)), dim3((NCW + kHelpers) * kWave), kargs, lds, stream);
 }
 
-// A workgroup fills a CU (its LDS ring does), so the time is the number of
-// rounds of 256 workgroups times a form's time per chunk.  The fewer columns,
-// the shorter the chain of a chunk, but the more workgroups: the narrowest form
-// that is one round, else the widest.  1024 tokens, dk = dv = 128, us by number
-// of tiles (forms of 16 / 32 / 64 / 128 columns):
-//      8 tiles   52   57   62   86
-//     32         55   60   65   89
-//     64        105   64   67   90
-//    128        202  120   72   93
-//    256        389  230  139  101
-//    768       1169  667  408  306
+// A workgroup takes a CU's issue slots, or all of its LDS, so the time is the number
+// of rounds of 256 workgroups times a form's time per chunk (at dk <= 64 two fit a CU
+// with bf16 rows, but then share its issue slots: 64 tiles below).  The fewer
+// columns, the shorter the chain of a chunk, but the more workgroups: the narrowest
+// form that is one round, else the widest.  1024 tokens, us by number of tiles (forms
+// of 16 / 32 / 64 / 128 columns), bf16 rows:
+//               dk = dv = 128              dk = 64, dv = 128          dk = 32, dv = 128
+//      8 tiles    49   58   65   84         42   43   47   62         45   45   47   57
+//     32          50   60   66   86         42   43   48   63         46   46   47   59
+//     64          96   61   68   86         62   44   50   63         56   47   48   60
+//    128         191  118   72   87        150   67   52   64        109   59   50   60
+//    192         285  174  131   88        204   99   78   65        162   97   70   61
+//    256         381  234  143  100        256  159   84   74        213  114   72   63
+//    384         572  351  208  181        381  225  126  130        315  171  107   96
+//    768        1142  702  436  309        758  457  262  225        624  354  225  167
+// Between rounds the widest may lose a little (fp32 rows, dk = 64, 384 tiles: 179 us
+// with 64 columns, 198 with 128).
 // 16 columns per state wave beat 32 (64 columns in two waves 86 us against 65
 // in four) but for the 128-column form, where eight waves of 16 columns and the
 // helpers are short of registers and issue slots (652 us against 624 on 768
