@@ -1121,6 +1121,20 @@ __global__ __launch_bounds__(kWave) void window_chunk(const WindowArgs a) {
 // for 156, which a bf16 pool's short windows gain by and an fp32 pool's do not
 // (96 heads x 256 requests, 4 tokens: bf16 value-first 430 -> 386, key-first
 // 435 -> 390; fp32 key-first 596 -> 751); windows of 8 do not fit (457 -> 570).
+// The fp32 value-first decode crosses at 12 tokens: 269 / 268 us at 12 and 331 / 277
+// at 16, over 32 heads x 256 requests.  Narrower keys cross earlier, as a token's
+// set-up is the same for less of a slab; 32 heads x 512 requests, dk = dv = 64 and,
+// after the bar, 32, for 2, 4 and 8 tokens:
+//   decode  f32 key-first     103 / 103  109 / 105  133 / 106 |  26 /  31   35 /  32   50 /  33
+//           f32 value-first   101 / 107  105 / 109  135 / 120 |  29 /  32   35 /  32   53 /  34
+//           bf16 key-first     50 /  50   70 /  52  120 /  56 |  20 /  20   31 /  20   54 /  22
+//           bf16 value-first   55 /  52   73 /  54  113 /  58 |  18 /  20   26 /  21   44 /  22
+//   window  f32 key-first     103 / 112  120 / 115  178 / 119 |  33 /  38   45 /  39   74 /  41
+//           f32 value-first   101 / 129  119 / 133  185 / 142 |  34 /  40   46 /  41   77 /  43
+//           bf16 key-first     64 /  61  102 /  67  182 /  89 |  29 /  24   47 /  27   84 /  34
+//           bf16 value-first   67 /  62   98 /  68  168 /  89 |  24 /  25   38 /  27   67 /  34
+// and dk = 64, dv = 128, value-first: decode f32 195 / 232 and 263 / 252 for 4 and 8
+// tokens, bf16 104 / 123 and 137 / 125 for 2 and 4; window bf16 128 / 145 and 191 / 158.
 // Few waves (up to half a wave per SIMD) take 16 columns each, replay and
 // window at once, and are bound by the chain of latencies; 32 heads x 4
 // requests, fp32 pool value-first, token by token / 8 at a time / at once:
@@ -1144,6 +1158,17 @@ constexpr int64_t kJointTo = 11;     // half tokens of a window
 //   bf16 key-first, 32 x 32, 1 token                  11.9 /14.4 /14.6 /15.7
 //   a window of 2 on f32 key-first, 96 x 256           541 / 528 / 527 / 538
 //   per-channel window of 1, f32 key-first             542 / 527 / 525 / 540
+// and where the rules begin, 32 heads (no claim / 16000 / 23000):
+//   f32 key-first, value-first, 1 token, 2048 waves    11.7 / 11.7 / 12.2,   9.9 /  9.9 / 11.5
+//                                        4096 waves    25.4 / 25.0 / 23.7,  23.7 / 23.9 / 23.1
+//                                        8192 waves    52.8 / 48.3 / 46.5,  48.9 / 48.1 / 47.1
+//   the same, 2 tokens, 4096 waves                     24.9 / 25.5 / 26.6,  24.1 / 24.6 / 25.8
+//                       8192 waves                     52.8 / 49.5 / 49.5,  49.7 / 49.5 / 49.3
+//   per-channel window of 1, 4096 waves                26.4 / 25.8 / 26.8,  25.7 / 26.2 / 25.6
+//                            8192 waves                53.3 / 48.9 / 49.6,  51.4 / 49.7 / 49.0
+//   bf16, 1 token, 12288 waves                         30.8 / 31.8 / 33.4,  37.2 / 36.8 / 39.2
+//                  16384 waves                         40.6 / 41.0 / 42.9,  49.3 / 48.3 / 50.8
+//                  32768 waves                         108  / 102  / 108,   95.5 / 90.5 / 93.9
 // Longer windows and bf16 pools beyond one token are bound by the waves' own
 // work and lose by it (window of 4, f32 key-first, 572 / 603 / 641 / 709), and
 // so do launches of a few waves per CU, whose last waves then wait (2 tokens,
@@ -1157,8 +1182,12 @@ uint32_t idle_lds(const WindowArgs& args, int64_t nwg) {
   return T <= (kChannel ? 1 : 2) * B && nwg >= 8192 ? 16000 : 0;
 }
 
-template <bool SBF16, int LAYOUT>
+template <int DK, bool SBF16, int LAYOUT>
 constexpr int64_t chunk_from(int window) {
+  if (DK < 128) {
+    if (SBF16) return LAYOUT == KDA_STATE_V_FIRST ? (window ? 6 : 7) : (window ? 4 : 6);
+    return DK == 64 && LAYOUT == KDA_STATE_V_FIRST ? (window ? 12 : 14) : 8;
+  }
   if (SBF16) return window ? 6 : LAYOUT == KDA_STATE_V_FIRST ? 9 : 8;
   return LAYOUT == KDA_STATE_V_FIRST ? (window ? 14 : 24) : (window ? 10 : 12);
 }
@@ -1174,7 +1203,7 @@ hipError_t launch_one(const WindowArgs& args, hipStream_t stream) {
   if constexpr (!kChannel && DK >= 32) {
     const bool few = nwg <= kFewWaves;
     const int64_t halves = 2 * static_cast<int64_t>(args.src[args.window].T), B = args.B;
-    if (few ? halves >= (args.window ? 5 : 8) * B : halves >= chunk_from<SBF16, LAYOUT>(args.window) * B) {
+    if (few ? halves >= (args.window ? 5 : 8) * B : halves >= chunk_from<DK, SBF16, LAYOUT>(args.window) * B) {
       lds = 0;
       if (few) {
         fn = reinterpret_cast<const void*>(&window_chunk<DK, DV, QBF16, SBF16, LAYOUT, 16, true>);

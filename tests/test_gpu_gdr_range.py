@@ -224,3 +224,20 @@ def test_infinite_v_in_the_last_token(torch_cuda, entry, n, requests):
             got = pool[b.slots[r], hv]
             R.check_state(got[:, rest], S[:, rest], m[rest], n, False, f"{entry} request {r} head {hv}")
             np.testing.assert_array_equal(got[:, col], np.sign(tok.k[rows[-1], 0]) * np.inf)
+
+
+@pytest.mark.parametrize("entry", ["decode", "window"])
+@pytest.mark.parametrize("state", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", ["k_first", "v_first"])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (32, 32), (64, 128)])
+@pytest.mark.parametrize("lo,hi", [(0, 3), (3, 5), (5, 9)])
+def test_many_requests_of_narrow_keys(torch_cuda, entry, state, layout, dk, dv, lo, hi):
+    """The forms that large batches take at dk < 128, on both sides of the lengths at
+    which they change."""
+    from tests.test_gpu_gdr import run
+    rng = np.random.default_rng(hi)
+    HV = 1024 // (44 * (dv // 32)) + 1        # more than 512 waves
+    lens = rng.integers(lo, hi + 1, size=44).tolist()
+    replay = [(int(rng.integers(0, 4)), int(rng.integers(0, hi + 1))) for _ in lens]
+    run(torch_cuda, entry, f"{dk}x{dv} {lo}..{hi}", lens, H=HV, HV=HV, dk=dk, dv=dv, state=state, layout=layout,
+        replay=replay if entry == "window" else None, seed=lo)
