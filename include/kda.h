@@ -265,8 +265,9 @@ int kda_gdr_decode(const kda_tensor* out, const kda_tensor* q, const kda_tensor*
  * column holds at that token, |S| and |v|, as kda_gdr_decode's is; but |v|
  * counts over a group of eight tokens (of every 32 from the request's start,
  * tokens 4i .. 4i+3 and 16+4i .. 16+4i+3; with less than four of them at the
- * end, over the group before as well), and |S| undecayed through groups whose
- * v is all zero.  A chunk of 32 tokens with groups smaller than about 2^-11 of
+ * end, over the group before as well), and where all of a group's v is zero
+ * (or below 2^-120) what the column held in these 32 tokens so far counts
+ * undecayed.  A chunk of 32 tokens with groups smaller than about 2^-11 of
  * its largest |v| or |S| is computed token by token, which takes some 14
  * times as long.  No workspace.  dk and dv must each be 32, 64 or 128, T at
  * most 2^31 - 65, B * HV at most 2^23 - 1 and HV * max(dk, dv) below 2^24

@@ -4,17 +4,20 @@ that is zero for a while.  Bounds are causal here: a token's error is relative
 to what its column holds by then, not to what comes later or has decayed.
 
 A step S' = alpha S + beta kh u passes alpha of the error that S carries and,
-as in tests/gdr_reference.py, adds STEP units of alpha |S| + |v|; the decay's
-exponent g = log alpha comes from fp32 arithmetic of a few units and is an
-exp's argument, which adds up to 8 units of |g| relative to alpha |S|:
-  e_i = alpha_i e_(i-1) + eps (STEP (alpha_i |S| + |v_i|) + 8 |g_i| alpha_i |S|)
+as in tests/gdr_reference.py, adds STEP units of alpha |S| + |v|.  The decay's
+exponent g = log alpha adds up to 16 units of |g| relative to alpha |S|: exp(a_log)
+5 (a hardware exp of one ulp, two units, and its rounded argument), softplus up to 8
+(the sum x, exp, log and reciprocal of an ulp each, two products), their product 1,
+and exp's argument g log2(e) 2:
+  e_i = alpha_i e_(i-1) + eps (STEP (alpha_i |S| + |v_i|) + 16 |g_i| alpha_i |S|)
   |do_i| <= scale (e_i + STEP eps (alpha_i |S| + |v_i|)).
 Below fp32's normal range (2^-126) intermediates may flush to zero.  Deferred
 decays hold a state 2^64 larger at most and multiply by as little again, and a
 column has 128 terms: at most 2^-126 * 2^7 a step, FLOOR = 2^-117 with the
 output's own terms.  kda_gdr_prefill takes |v|
-over groups of tokens, and |S| undecayed through groups whose v is all zero, as
-include/kda.h says; kda_gdr_decode takes the token alone.  Column norms are at
+over groups of tokens and, where a group has no v, what the column held in its 32
+tokens so far, undecayed, as include/kda.h says; kda_gdr_decode takes the token
+alone.  Column norms are at
 most 2^100 here, so nothing overflows."""
 import numpy as np
 import pytest
@@ -24,6 +27,7 @@ from tests.test_gpu_gdr import Batch
 
 pytestmark = pytest.mark.gpu
 FLOOR = 2.0 ** -117
+NO_V = 2.0 ** -120
 
 
 @pytest.fixture(scope="module")
@@ -59,7 +63,6 @@ def walk(S, tok, par, hv, rows, G, grouped):
     v = tok.v[rows, hv].astype(np.float64)
     top = group_max(np.abs(v)) if grouped else np.abs(v)
     out, bound = np.zeros((len(rows), S.shape[1])), np.zeros((len(rows), S.shape[1]))
-    carry = np.linalg.norm(S, axis=0)
     amp = np.exp(np.float64(par.a_log[hv]))
     for i, t in enumerate(rows):
         q, k = tok.q[t, hv // G].astype(np.float64), tok.k[t, hv // G].astype(np.float64)
@@ -68,12 +71,15 @@ def walk(S, tok, par, hv, rows, G, grouped):
         x = np.float64(tok.gate[t, hv]) + par.dt_bias[hv]
         g = -amp * np.logaddexp(0.0, x) if par.gate_mode == "softplus" else par.lower_bound / (1 + np.exp(-amp * x))
         alpha, beta = np.exp(g), 1.0 / (1.0 + np.exp(-np.float64(tok.beta[t, hv])))
+        if i % 32 == 0:
+            so_far = np.linalg.norm(S, axis=0)
         S = alpha * S
         held = np.linalg.norm(S, axis=0)
+        so_far = np.maximum(so_far, np.maximum(held, top[i]))
         if grouped:
-            carry = held = np.where(top[i] > 0, held, np.maximum(carry, held))
+            held = np.where(top[i] > NO_V, held, so_far)
         step = R.STEP * R.EPS * (held + top[i]) + FLOOR
-        e = alpha * e + step + (8 * abs(g) * R.EPS * held if alpha > 0 else 0)
+        e = alpha * e + step + (16 * abs(g) * R.EPS * held if alpha > 0 else 0)
         S = S + np.outer(beta * k, v[i] - k @ S)
         out[i], bound[i] = q @ S, par.scale * (e + step)
     return S, out, e, bound
