@@ -869,7 +869,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
         voff[rb][r] = (16 * rb + 4 * g + r) * stride + (colw + column<NCS>(lane, 0)) * E;
     auto chunk_rows = [&](const void* base, int c) {
       return rows_resource<C>(base, ((static_cast<int64_t>(t0) + c * C) * a.HV + w.hv) * (dv * E), w.n - c * C, stride,
-                           dv * E);
+                              dv * E);
     };
     Columns<F32, NCS> v[NB][4];
     // a last chunk's groups of less than four tokens go with the one before, if there
@@ -1018,8 +1018,8 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
           wide |= least <= static_cast<uint32_t>(max(e, sig[cs] + kBias + 15 - kDown) - (kWide - kDown) - kNone);
         }
         // A chunk that goes token by token runs through the lines below as well, with S
-        // kept as it is, so that the others need not wait for this verdict; its outputs
-        // are overwritten.
+        // kept as it is and no outputs stored, so that the others need not wait for this
+        // verdict.
         const bool walks = __any(wide);   // uniform
         const float scale_u = walks ? 0.0f : 1.0f / kUnitT;
         float keep[NCS], up_old[NCS], up_new[NCS], down[NCS], shift[NCS];
@@ -1099,6 +1099,7 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
           }
         }
         const __amdgpu_buffer_rsrc_t ro = chunk_rows(a.out, it);
+        const int gone = walks ? static_cast<int>(0x80000000u) : 0;   // past every row: dropped
 #pragma unroll
         for (int rb = 0; rb < NB; ++rb)
 #pragma unroll
@@ -1106,14 +1107,12 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
             float x[NCS];
 #pragma unroll
             for (int cs = 0; cs < NCS; ++cs) x[cs] = qs[rb][cs][r];
-            Columns<F32, NCS>::store(ro, voff[rb][r], x);
+            Columns<F32, NCS>::store(ro, voff[rb][r] | gone, x);
           }
         if (__builtin_expect(walks, 0)) {
-          constexpr int kVmcnt0 = 0x0f70;   // the stores above are done; and no load of the walk is counted on below
-          __builtin_amdgcn_s_waitcnt(kVmcnt0);
-          walk_chunk<KB, NCS, DK, F32>(a, sh, w, ring, it * C, min(w.n - it * C, C), chunk_rows(a.v, it), ro,
-                                       voff[0][0] - 4 * g * stride, stride, lane, sig, S);
-          __builtin_amdgcn_s_waitcnt(kVmcnt0);
+          walk_chunk<KB, NCS, DK, F32>(a, sh, w, ring, it * C, min(w.n - it * C, C), chunk_rows(a.v, it),
+                                       ro, voff[0][0] - 4 * g * stride, stride, lane, sig, S);
+          __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): waits of the usual form then count on its own loads alone
         }
         third = third == kRingP - 1 ? 0 : third + 1;
       }

@@ -247,3 +247,18 @@ def test_many_requests_of_narrow_keys(torch_cuda, entry, state, layout, dk, dv, 
     replay = [(int(rng.integers(0, 4)), int(rng.integers(0, hi + 1))) for _ in lens]
     run(torch_cuda, entry, f"{dk}x{dv} {lo}..{hi}", lens, H=HV, HV=HV, dk=dk, dv=dv, state=state, layout=layout,
         replay=replay if entry == "window" else None, seed=lo)
+
+
+@pytest.mark.parametrize("entry", ["prefill", "decode"])
+@pytest.mark.parametrize("qkv", ["bf16", "f32"])
+def test_output_in_place_of_v(torch_cuda, entry, qkv):
+    """out and v may be one tensor: a token's v is read before its output is written,
+    also in chunks that go token by token."""
+    torch = torch_cuda
+    b = Batch(torch, [70, 33, 5], H=2, HV=2, qkv=qkv, edit=scaled(17, 2.0 ** 30), seed=6)
+    d, e = b.device(), b.device()
+    b.call(entry, d)
+    e["out"] = e["v"]
+    b.call(entry, e)
+    torch.cuda.synchronize()
+    assert torch.equal(d["out"], e["out"]) and torch.equal(d["pool"], e["pool"])
