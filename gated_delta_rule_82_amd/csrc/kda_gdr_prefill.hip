@@ -873,8 +873,10 @@ gdr_prefill(const DecodeArgs a, const int dv, const int layout, const int state_
     };
     Columns<F32, NCS> v[NB][4];
     // a last chunk's groups of less than four tokens go with the one before, if there
-    // is one: an exponent that is not the smallest
-    const int past = g > 0 && 4 * g + 4 > w.n - (chunks - 1) * C ? 512 : 0;
+    // is one: an exponent that is not the smallest.  In the second 16 of 32 tokens they
+    // belong to a group of four in the first 16, so only groups without a token do.
+    const int fewest = C * (chunks - 1) % 32 ? 1 : 4;
+    const int past = g > 0 && 4 * g + fewest > w.n - (chunks - 1) * C ? 512 : 0;
     auto load_v = [&](int c) {
       const __amdgpu_buffer_rsrc_t r0 = chunk_rows(a.v, c);
 #pragma unroll

@@ -262,3 +262,21 @@ def test_output_in_place_of_v(torch_cuda, entry, qkv):
     b.call(entry, e)
     torch.cuda.synchronize()
     assert torch.equal(d["out"], e["out"]) and torch.equal(d["pool"], e["pool"])
+
+
+@pytest.mark.parametrize("dk,dv,qkv", [(128, 64, "f32"), (128, 128, "f32"), (128, 128, "bf16"), (64, 64, "f32")])
+def test_few_last_tokens_behind_a_large_one(torch_cuda, dk, dv, qkv):
+    """Small v after a large one that a gate closes, in a request's last tokens: in the
+    first 16 of 32 (11, 38, 13 tokens), where the group before counts as well, and in
+    the second, where these tokens' own group has four in the first."""
+    def edit(b):
+        b.par.a_log[:] = 0
+        b.par.dt_bias[:] = 0
+        b.tok.gate[:] = 0
+        for a, n in zip(b.cu[:-1], b.lens):
+            large, small = (n - 1) // 4 * 4 - 3, (n - 1) // 4 * 4
+            b.tok.v[a + large] *= np.float32(2.0 ** 33)
+            b.tok.gate[a + large + 1:a + small + 1] = 16
+    lens = [23, 22, 21, 54, 87, 118, 11, 38, 67, 13]
+    check(torch_cuda, "prefill", "large v in the group before the last", lens, H=1, HV=2, dk=dk, dv=dv, qkv=qkv,
+          sigma=0.05, edit=edit, seed=11)
