@@ -109,6 +109,9 @@ def build(verbose: bool = True) -> str:
               for i, gate in enumerate(("head", "channel"))]
     units.append(("kda_verify", "kda_verify", []))
     units.append(("kda_gdr_prefill", "kda_gdr_prefill", []))
+    units.append(("kda_ssm_decode", "kda_ssm_decode", []))
+    units += [("kda_ssm_prefill", f"kda_ssm_prefill_dk{dk}", [f"-DKDA_SSM_DK={dk}"]) for dk in (32, 64, 128)]
+    units.append(("kda_norm", "kda_norm", []))
     lib_objs = [os.path.join(BUILD, f"{obj}.o") for _, obj, _ in units]
     bench_o = os.path.join(BUILD, "bench_copy.o")
     units.append(("bench_copy", "bench_copy", []))

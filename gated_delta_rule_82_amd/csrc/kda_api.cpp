@@ -79,6 +79,16 @@ int launch_window(const WindowArgs& args, int dk, int dv, bool qkv_bf16, bool st
                  : launch_window_gate<false>(args, dk, dv, qkv_bf16, state_bf16, state_layout, stream);
 }
 
+int launch_ssm_prefill(const SsmArgs& args, int dk, int dv, bool bf16, bool state_bf16, int state_layout,
+                       hipStream_t stream) {
+  switch (dk) {
+    case 32: return launch_ssm_prefill_dk<32>(args, dv, bf16, state_bf16, state_layout, stream);
+    case 64: return launch_ssm_prefill_dk<64>(args, dv, bf16, state_bf16, state_layout, stream);
+    case 128: return launch_ssm_prefill_dk<128>(args, dv, bf16, state_bf16, state_layout, stream);
+    default: return KDA_ERR_UNSUPPORTED;
+  }
+}
+
 }  // namespace kda
 
 extern "C" {
@@ -546,6 +556,251 @@ int kda_verify(const kda_tensor* n_commit, const kda_tensor* next_token, const k
   a.T = static_cast<int32_t>(T);
   a.V = static_cast<int32_t>(V);
   return kda::launch_verify(a, dt == KDA_BF16, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Every check of a kda_ssm_decode or kda_ssm_prefill call (workspace NULL and
+// not needed for the former).
+struct SsmPlan {
+  kda::SsmArgs args;
+  int dk, dv;
+  bool bf16, state_bf16, empty;
+};
+
+int plan_ssm(const kda_tensor* out, const kda_tensor* xbc, const kda_tensor* dt, const kda_tensor* conv_w,
+             const kda_tensor* conv_b, const kda_tensor* conv_win, const kda_tensor* a_log,
+             const kda_tensor* dt_bias, const kda_tensor* d_skip, const kda_tensor* cu_seqlens,
+             const kda_tensor* state_pool, const kda_tensor* state_indices, const kda_tensor* workspace,
+             bool prefill, int32_t state_layout, SsmPlan* plan) {
+  KDA_TRY(check_tensor(out, 4));
+  KDA_TRY(check_tensor(xbc, 3));
+  KDA_TRY(check_tensor(dt, 3));
+  KDA_TRY(check_tensor(conv_w, 2));
+  if (conv_b != nullptr) KDA_TRY(check_tensor(conv_b, 1));
+  KDA_TRY(check_tensor(conv_win, 3));
+  KDA_TRY(check_tensor(a_log, 1));
+  KDA_TRY(check_tensor(dt_bias, 1));
+  if (d_skip != nullptr) KDA_TRY(check_tensor(d_skip, 1));
+  KDA_TRY(check_tensor(cu_seqlens, 1));
+  KDA_TRY(check_tensor(state_pool, 4));
+  KDA_TRY(check_tensor(state_indices, 1));
+  if (prefill) KDA_TRY(check_tensor(workspace, 1));
+
+  const int32_t act = xbc->dtype, wdt = conv_w->dtype;
+  if ((act != KDA_BF16 && act != KDA_F32) || out->dtype != act) return KDA_ERR_DTYPE;
+  if ((wdt != KDA_BF16 && wdt != KDA_F32) || (conv_b != nullptr && conv_b->dtype != wdt)) return KDA_ERR_DTYPE;
+  if (dt->dtype != KDA_F32 || conv_win->dtype != KDA_F32 || a_log->dtype != KDA_F32 || dt_bias->dtype != KDA_F32 ||
+      (d_skip != nullptr && d_skip->dtype != KDA_F32))
+    return KDA_ERR_DTYPE;
+  if (state_pool->dtype != KDA_F32 && state_pool->dtype != KDA_BF16) return KDA_ERR_DTYPE;
+  if (cu_seqlens->dtype != KDA_I32 || state_indices->dtype != KDA_I32) return KDA_ERR_DTYPE;
+  if (prefill && workspace->dtype != KDA_F32) return KDA_ERR_DTYPE;
+
+  if (state_layout != KDA_STATE_K_FIRST && state_layout != KDA_STATE_V_FIRST) return KDA_ERR_MODE;
+  const bool v_first = state_layout == KDA_STATE_V_FIRST;
+  const int64_t T = xbc->shape[1], C = xbc->shape[2], HV = dt->shape[2], DV = out->shape[3];
+  const int64_t N = state_pool->shape[0], DK = state_pool->shape[v_first ? 3 : 2], B = state_indices->shape[0];
+  const int64_t K = conv_w->shape[0];
+  if (xbc->shape[0] != 1 || dt->shape[0] != 1 || out->shape[0] != 1) return KDA_ERR_SHAPE;
+  if (dt->shape[1] != T || out->shape[1] != T || out->shape[2] != HV) return KDA_ERR_SHAPE;
+  if (state_pool->shape[1] != HV || state_pool->shape[v_first ? 2 : 3] != DV) return KDA_ERR_SHAPE;
+  if (conv_w->shape[1] != C || (conv_b != nullptr && conv_b->shape[0] != C)) return KDA_ERR_SHAPE;
+  if (conv_win->shape[0] != N || conv_win->shape[1] != K - 1 || conv_win->shape[2] != C) return KDA_ERR_SHAPE;
+  if (a_log->shape[0] != HV || dt_bias->shape[0] != HV || (d_skip != nullptr && d_skip->shape[0] != HV))
+    return KDA_ERR_SHAPE;
+  if (cu_seqlens->shape[0] - 1 != B) return KDA_ERR_SHAPE;
+  if (!supported_head_dim(DK) || !supported_head_dim(DV) || DK < 32 || DV < 32) return KDA_ERR_UNSUPPORTED;
+  if (K < 2 || K > 4) return KDA_ERR_UNSUPPORTED;
+  // all further sizes follow from these, within 32 bits
+  constexpr int64_t kI32 = std::numeric_limits<int32_t>::max();
+  if (T > kI32 - 64 || N > kI32 - 64 || B > kI32 - 64 || C >= (1 << 24)) return KDA_ERR_UNSUPPORTED;
+  if (HV < 1 || HV > C / DV) return KDA_ERR_SHAPE;
+  const int64_t keys = C - HV * DV;       // B and C of H groups
+  if (keys < 2 * DK || keys % (2 * DK) != 0) return KDA_ERR_SHAPE;
+  const int64_t H = keys / (2 * DK);
+  if (HV % H != 0) return KDA_ERR_SHAPE;
+  // at most 512 work-items per (request, value head); one per window channel
+  if (product_exceeds({B, HV}, (1 << 22) - 1) || product_exceeds({B, C}, kI32)) return KDA_ERR_UNSUPPORTED;
+
+  const kda_tensor* all[] = {out, xbc, dt, conv_w, conv_win, a_log, dt_bias, cu_seqlens, state_pool, state_indices};
+  for (const kda_tensor* t : all)
+    if (!aligned(t, 16)) return KDA_ERR_UNSUPPORTED;
+  const kda_tensor* optional[] = {conv_b, d_skip, prefill ? workspace : nullptr};
+  for (const kda_tensor* t : optional)
+    if (t != nullptr && !aligned(t, 16)) return KDA_ERR_UNSUPPORTED;
+  if (prefill) {
+    // work-items: 256 per 64 tokens and group, and per four waves of a segment
+    if (product_exceeds({T / KDA_SSM_CHUNK + B, H, 256}, kMaxWorkItems) ||
+        product_exceeds({T / KDA_SSM_CHUNK + B + 8, HV * 2 + 3, 64}, kMaxWorkItems))
+      return KDA_ERR_UNSUPPORTED;
+    if (workspace->shape[0] < KDA_SSM_WORKSPACE(T, B, H, HV, DK, DV, K)) return KDA_ERR_SHAPE;
+  }
+
+  plan->empty = B == 0 || T == 0;
+  plan->dk = static_cast<int>(DK);
+  plan->dv = static_cast<int>(DV);
+  plan->bf16 = act == KDA_BF16;
+  plan->state_bf16 = state_pool->dtype == KDA_BF16;
+  kda::SsmArgs& a = plan->args;
+  a = kda::SsmArgs{};
+  a.out = out->data;
+  a.xbc = xbc->data;
+  a.dt = static_cast<const float*>(dt->data);
+  a.conv_w = conv_w->data;
+  a.conv_b = conv_b != nullptr ? conv_b->data : nullptr;
+  a.conv_win = static_cast<float*>(conv_win->data);
+  a.a_log = static_cast<const float*>(a_log->data);
+  a.dt_bias = static_cast<const float*>(dt_bias->data);
+  a.d_skip = d_skip != nullptr ? static_cast<const float*>(d_skip->data) : nullptr;
+  a.cu_seqlens = static_cast<const int32_t*>(cu_seqlens->data);
+  a.state_pool = state_pool->data;
+  a.state_indices = static_cast<const int32_t*>(state_indices->data);
+  a.workspace = prefill ? static_cast<float*>(workspace->data) : nullptr;
+  a.B = static_cast<int32_t>(B);
+  a.T = static_cast<int32_t>(T);
+  a.H = static_cast<int32_t>(H);
+  a.HV = static_cast<int32_t>(HV);
+  a.G = static_cast<int32_t>(HV / H);
+  a.N = static_cast<int32_t>(N);
+  a.C = static_cast<int32_t>(C);
+  a.K = static_cast<int32_t>(K);
+  a.w_bf16 = wdt == KDA_BF16;
+  return KDA_OK;
+}
+
+// Rows and length of the last dimension; KDA_ERR_* for what the norms refuse.
+int norm_extent(const kda_tensor* t, int64_t* rows, int64_t* D) {
+  if (t == nullptr) return KDA_ERR_NULL;
+  if (t->ndim < 1 || t->ndim > 4) return KDA_ERR_SHAPE;
+  KDA_TRY(check_tensor(t, t->ndim));
+  *D = t->shape[t->ndim - 1];
+  if (*D < 1 || *D > KDA_NORM_MAX) return KDA_ERR_UNSUPPORTED;
+  *rows = 1;
+  for (int i = 0; i + 1 < t->ndim; ++i) {
+    if (product_exceeds({*rows, t->shape[i]}, std::numeric_limits<int32_t>::max())) return KDA_ERR_UNSUPPORTED;
+    *rows *= t->shape[i];
+  }
+  return KDA_OK;
+}
+
+bool same_shape(const kda_tensor* a, const kda_tensor* b) {
+  if (a->ndim != b->ndim) return false;
+  for (int i = 0; i < a->ndim; ++i)
+    if (a->shape[i] != b->shape[i]) return false;
+  return true;
+}
+
+bool activation_dtype(int32_t dtype) { return dtype == KDA_F32 || dtype == KDA_BF16; }
+
+}  // namespace
+
+extern "C" {
+
+int kda_ssm_decode(const kda_tensor* out, const kda_tensor* xbc, const kda_tensor* dt,
+                   const kda_tensor* conv_w, const kda_tensor* conv_b, const kda_tensor* conv_win,
+                   const kda_tensor* a_log, const kda_tensor* dt_bias, const kda_tensor* d_skip,
+                   const kda_tensor* cu_seqlens, const kda_tensor* state_pool,
+                   const kda_tensor* state_indices, int32_t state_layout, hipStream_t stream) {
+  SsmPlan plan;
+  KDA_TRY(plan_ssm(out, xbc, dt, conv_w, conv_b, conv_win, a_log, dt_bias, d_skip, cu_seqlens, state_pool,
+                   state_indices, nullptr, false, state_layout, &plan));
+  if (plan.empty) return KDA_OK;
+  return kda::launch_ssm_decode(plan.args, plan.dk, plan.dv, plan.bf16, plan.state_bf16, state_layout, stream);
+}
+
+int kda_ssm_prefill(const kda_tensor* out, const kda_tensor* xbc, const kda_tensor* dt,
+                    const kda_tensor* conv_w, const kda_tensor* conv_b, const kda_tensor* conv_win,
+                    const kda_tensor* a_log, const kda_tensor* dt_bias, const kda_tensor* d_skip,
+                    const kda_tensor* cu_seqlens, const kda_tensor* state_pool,
+                    const kda_tensor* state_indices, const kda_tensor* workspace, int32_t state_layout,
+                    hipStream_t stream) {
+  SsmPlan plan;
+  KDA_TRY(plan_ssm(out, xbc, dt, conv_w, conv_b, conv_win, a_log, dt_bias, d_skip, cu_seqlens, state_pool,
+                   state_indices, workspace, true, state_layout, &plan));
+  if (plan.empty) return KDA_OK;
+  return kda::launch_ssm_prefill(plan.args, plan.dk, plan.dv, plan.bf16, plan.state_bf16, state_layout, stream);
+}
+
+int kda_norm_residual(const kda_tensor* hidden_out, const kda_tensor* normed, const kda_tensor* hidden,
+                      const kda_tensor* block_out, const kda_tensor* weight, const kda_tensor* post_weight,
+                      const kda_tensor* scale, float eps, hipStream_t stream) {
+  int64_t rows = 0, D = 0, r = 0, d = 0;
+  KDA_TRY(norm_extent(hidden, &rows, &D));
+  const kda_tensor* others[] = {hidden_out, normed, block_out};
+  for (const kda_tensor* t : others) {
+    KDA_TRY(norm_extent(t, &r, &d));
+    if (!same_shape(t, hidden)) return KDA_ERR_SHAPE;
+  }
+  KDA_TRY(check_tensor(weight, 1));
+  if (post_weight != nullptr) KDA_TRY(check_tensor(post_weight, 1));
+  if (scale != nullptr) KDA_TRY(check_tensor(scale, 1));
+  if (!activation_dtype(hidden->dtype) || hidden_out->dtype != hidden->dtype) return KDA_ERR_DTYPE;
+  if (!activation_dtype(block_out->dtype) || normed->dtype != block_out->dtype) return KDA_ERR_DTYPE;
+  if (weight->dtype != KDA_F32 || (post_weight != nullptr && post_weight->dtype != KDA_F32) ||
+      (scale != nullptr && scale->dtype != KDA_F32))
+    return KDA_ERR_DTYPE;
+  if (weight->shape[0] != D || (post_weight != nullptr && post_weight->shape[0] != D)) return KDA_ERR_SHAPE;
+  if (scale != nullptr && scale->shape[0] != D && scale->shape[0] != 1) return KDA_ERR_SHAPE;
+  const kda_tensor* wide[] = {hidden_out, normed, hidden, block_out};
+  for (const kda_tensor* t : wide)
+    if (!aligned(t, 16)) return KDA_ERR_UNSUPPORTED;
+  const kda_tensor* vectors[] = {weight, post_weight, scale};
+  for (const kda_tensor* t : vectors)
+    if (t != nullptr && !aligned(t, 4)) return KDA_ERR_UNSUPPORTED;
+  if (!(std::isfinite(eps) && eps >= 0.0f)) return KDA_ERR_MODE;
+  if (rows == 0) return KDA_OK;
+  kda::ResidualArgs a{};
+  a.hidden_out = hidden_out->data;
+  a.hidden = hidden->data;
+  a.normed = normed->data;
+  a.block_out = block_out->data;
+  a.weight = static_cast<const float*>(weight->data);
+  a.post_weight = post_weight != nullptr ? static_cast<const float*>(post_weight->data) : nullptr;
+  a.scale = scale != nullptr ? static_cast<const float*>(scale->data) : nullptr;
+  a.scale_per_channel = scale != nullptr && scale->shape[0] == D;
+  a.rows = rows;
+  a.D = static_cast<int32_t>(D);
+  a.eps = eps == 0.0f ? 1e-5f : eps;
+  return kda::launch_norm_residual(a, hidden->dtype == KDA_BF16, block_out->dtype == KDA_BF16, stream);
+}
+
+int kda_norm_gate(const kda_tensor* out, const kda_tensor* x, const kda_tensor* gate, const kda_tensor* weight,
+                  int32_t act, int32_t gate_first, float eps, hipStream_t stream) {
+  int64_t rows = 0, D = 0, r = 0, d = 0;
+  KDA_TRY(norm_extent(x, &rows, &D));
+  const kda_tensor* others[] = {out, gate};
+  for (const kda_tensor* t : others) {
+    KDA_TRY(norm_extent(t, &r, &d));
+    if (!same_shape(t, x)) return KDA_ERR_SHAPE;
+  }
+  if (weight == nullptr) return KDA_ERR_NULL;
+  if (weight->ndim != 1 && weight->ndim != 2) return KDA_ERR_SHAPE;
+  KDA_TRY(check_tensor(weight, weight->ndim));
+  if (!activation_dtype(x->dtype) || out->dtype != x->dtype || gate->dtype != x->dtype || weight->dtype != KDA_F32)
+    return KDA_ERR_DTYPE;
+  if (weight->shape[weight->ndim - 1] != D) return KDA_ERR_SHAPE;
+  if (weight->ndim == 2 && (x->ndim < 2 || weight->shape[0] != x->shape[x->ndim - 2])) return KDA_ERR_SHAPE;
+  const kda_tensor* wide[] = {out, x, gate};
+  for (const kda_tensor* t : wide)
+    if (!aligned(t, 16)) return KDA_ERR_UNSUPPORTED;
+  if (!aligned(weight, 4)) return KDA_ERR_UNSUPPORTED;
+  if ((act != KDA_ACT_SIGMOID && act != KDA_ACT_SILU) || (gate_first != 0 && gate_first != 1)) return KDA_ERR_MODE;
+  if (!(std::isfinite(eps) && eps >= 0.0f)) return KDA_ERR_MODE;
+  if (rows == 0) return KDA_OK;
+  kda::GateArgs a{};
+  a.out = out->data;
+  a.x = x->data;
+  a.gate = gate->data;
+  a.weight = static_cast<const float*>(weight->data);
+  a.rows = rows;
+  a.D = static_cast<int32_t>(D);
+  a.groups = weight->ndim == 2 ? static_cast<int32_t>(weight->shape[0]) : 1;
+  a.silu = act == KDA_ACT_SILU;
+  a.eps = eps == 0.0f ? 1e-5f : eps;
+  return kda::launch_norm_gate(a, gate_first == 1, x->dtype == KDA_BF16, stream);
 }
 
 }  // extern "C"

@@ -15,8 +15,20 @@
 
 namespace {
 
-enum Kind { kRecurrence = 0, kPrefill = 1, kConv = 2, kWindow = 3, kVerify = 4 };
-constexpr Py_ssize_t kTensors[] = {11, 11, 19, 17, 9};
+enum Kind {
+  kRecurrence = 0,
+  kPrefill = 1,
+  kConv = 2,
+  kWindow = 3,
+  kVerify = 4,
+  kSsmDecode = 5,
+  kSsmPrefill = 6,
+  kNormResidual = 7,
+  kNormGate = 8
+};
+constexpr Py_ssize_t kTensors[] = {11, 11, 19, 17, 9, 12, 13, 7, 4};
+// tensors that may be None, one bit each
+constexpr unsigned kOptional[] = {0, 0, 0, 0, 1u << 3, 1u << 4 | 1u << 8, 1u << 4 | 1u << 8, 1u << 5 | 1u << 6, 0};
 constexpr int kMost = 19;
 
 bool describe(PyObject* object, int64_t device, kda_tensor* d) {
@@ -38,7 +50,9 @@ bool describe(PyObject* object, int64_t device, kda_tensor* d) {
 
 // call(kind, entry point, tensors, device, gate_mode, lower_bound, l2_eps,
 //      scale, state_layout, matmul, stream) -> status, or None.
-// tensors is a tuple in the entry point's order (None: draft_probs only).
+// tensors is a tuple in the entry point's order (None: see kOptional).  The
+// norms take their eps as l2_eps, the gate's activation as gate_mode and
+// gate_first as matmul.
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != 11 || !PyTuple_Check(args[2])) {
     PyErr_SetString(PyExc_TypeError, "call: 11 arguments, the third a tuple");
@@ -56,7 +70,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const long matmul = PyLong_AsLong(args[9]);
   hipStream_t const stream = static_cast<hipStream_t>(PyLong_AsVoidPtr(args[10]));
   if (PyErr_Occurred()) return nullptr;
-  if (kind < 0 || kind > kVerify || PyTuple_GET_SIZE(args[2]) != kTensors[kind]) {
+  if (kind < 0 || kind > kNormGate || PyTuple_GET_SIZE(args[2]) != kTensors[kind]) {
     PyErr_SetString(PyExc_TypeError, "call: wrong number of tensors");
     return nullptr;
   }
@@ -66,7 +80,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     for (Py_ssize_t i = 0; i < kTensors[kind]; ++i) {
       PyObject* const object = PyTuple_GET_ITEM(args[2], i);
       p[i] = t + i;
-      if (kind == kVerify && i == 3 && object == Py_None) p[i] = nullptr;
+      if (object == Py_None && (kOptional[kind] >> i & 1u) != 0) p[i] = nullptr;
       else if (!describe(object, device, t + i)) Py_RETURN_NONE;
     }
   } catch (...) {   // a tensor without storage of its own
@@ -96,9 +110,26 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                                                      p[8], p[9], p[10], &replay, &mode, stream);
       break;
     }
-    default:
+    case kVerify:
       status = reinterpret_cast<decltype(&kda_verify)>(entry)(p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8],
                                                               stream);
+      break;
+    case kSsmDecode:
+      status = reinterpret_cast<decltype(&kda_ssm_decode)>(entry)(p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7],
+                                                                  p[8], p[9], p[10], p[11], mode.state_layout, stream);
+      break;
+    case kSsmPrefill:
+      status = reinterpret_cast<decltype(&kda_ssm_prefill)>(entry)(p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7],
+                                                                   p[8], p[9], p[10], p[11], p[12], mode.state_layout,
+                                                                   stream);
+      break;
+    case kNormResidual:
+      status = reinterpret_cast<decltype(&kda_norm_residual)>(entry)(p[0], p[1], p[2], p[3], p[4], p[5], p[6],
+                                                                     mode.l2_eps, stream);
+      break;
+    default:
+      status = reinterpret_cast<decltype(&kda_norm_gate)>(entry)(p[0], p[1], p[2], p[3], mode.gate_mode,
+                                                                 static_cast<int32_t>(matmul), mode.l2_eps, stream);
   }
   Py_END_ALLOW_THREADS
   return PyLong_FromLong(status);

@@ -105,6 +105,68 @@ struct VerifyArgs {
 };
 int launch_verify(const VerifyArgs& args, bool bf16, hipStream_t stream);
 
+// Validated, flattened arguments of kda_ssm_decode and kda_ssm_prefill.
+struct SsmArgs {
+  void* out;                    // [T, HV, dv]  bf16 or f32
+  const void* xbc;              // [T, C]       dtype of out
+  const float* dt;              // [T, HV]
+  const void* conv_w;           // [K, C]       f32 or bf16
+  const void* conv_b;           // [C] or NULL, dtype of conv_w
+  float* conv_win;              // [N, K-1, C]
+  const float* a_log;           // [HV]
+  const float* dt_bias;         // [HV]
+  const float* d_skip;          // [HV] or NULL
+  const int32_t* cu_seqlens;    // [B + 1]
+  void* state_pool;             // [N, HV, dk, dv] or [N, HV, dv, dk]
+  const int32_t* state_indices; // [B]
+  float* workspace;             // kda_ssm_prefill only
+  int32_t B, T, H, HV, G, N;
+  int32_t C, K;
+  int32_t w_bf16;               // dtype of conv_w and conv_b
+};
+
+// Enqueue kda_ssm_decode (kda_ssm_decode.hip) and kda_ssm_prefill
+// (kda_ssm_prefill.hip, compiled once per dk with KDA_SSM_DK; kda_api.cpp
+// picks the object).  Return codes as below.
+int launch_ssm_decode(const SsmArgs& args, int dk, int dv, bool bf16, bool state_bf16, int state_layout,
+                      hipStream_t stream);
+template <int DK>
+int launch_ssm_prefill_dk(const SsmArgs& args, int dv, bool bf16, bool state_bf16, int state_layout,
+                          hipStream_t stream);
+template <>
+int launch_ssm_prefill_dk<32>(const SsmArgs&, int, bool, bool, int, hipStream_t);
+template <>
+int launch_ssm_prefill_dk<64>(const SsmArgs&, int, bool, bool, int, hipStream_t);
+template <>
+int launch_ssm_prefill_dk<128>(const SsmArgs&, int, bool, bool, int, hipStream_t);
+
+// kda_norm_residual and kda_norm_gate, flattened (kda_norm.hip).
+struct ResidualArgs {
+  void* hidden_out;             // [rows, D]  bf16 or f32
+  const void* hidden;
+  void* normed;                 // [rows, D]  bf16 or f32
+  const void* block_out;
+  const float* weight;          // [D]
+  const float* post_weight;     // [D] or NULL
+  const float* scale;           // [D], [1] or NULL
+  int32_t scale_per_channel;
+  int64_t rows;
+  int32_t D;
+  float eps;
+};
+struct GateArgs {
+  void* out;                    // [rows, D]  bf16 or f32
+  const void* x;
+  const void* gate;
+  const float* weight;          // [groups, D]; row r takes r % groups
+  int64_t rows;
+  int32_t D, groups;
+  int32_t silu;
+  float eps;
+};
+int launch_norm_residual(const ResidualArgs& args, bool hidden_bf16, bool bf16, hipStream_t stream);
+int launch_norm_gate(const GateArgs& args, bool gate_first, bool bf16, hipStream_t stream);
+
 // The chunked gated delta rule (kda_gdr_prefill): DecodeArgs with raw_gate
 // [T, HV] and dt_bias [HV].  Defined in kda_gdr_prefill.hip.
 int launch_gdr_prefill(const DecodeArgs& args, int dk, int dv, bool qkv_bf16, bool state_bf16,

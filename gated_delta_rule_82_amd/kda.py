@@ -48,8 +48,16 @@ MATMULS = {"split_bf16": KDA_MATMUL_SPLIT_BF16, "f32": KDA_MATMUL_F32}
 
 KDA_VERIFY_SEGMENT = 1024
 
+KDA_SSM_CHUNK = 64
+KDA_SSM_SPLIT = 2048
+
+KDA_ACT_SIGMOID = 0
+KDA_ACT_SILU = 1
+ACTIVATIONS = {"sigmoid": KDA_ACT_SIGMOID, "silu": KDA_ACT_SILU}
+
 EXPORTED_SYMBOLS = ("kda_decode", "kda_decode_conv", "kda_prefill", "kda_gdr_decode",
-                    "kda_gdr_prefill", "kda_decode_window", "kda_verify", "kda_check_host",
+                    "kda_gdr_prefill", "kda_decode_window", "kda_verify", "kda_ssm_decode",
+                    "kda_ssm_prefill", "kda_norm_residual", "kda_norm_gate", "kda_check_host",
                     "kda_status_string", "kda_abi_version")
 CONV_FIELDS = ("x_q", "x_k", "x_v", "w_q", "w_k", "w_v", "win_q", "win_k", "win_v", "q_conv",
                "k_conv")
@@ -118,8 +126,13 @@ def library() -> ctypes.CDLL:
     lib.kda_gdr_decode.argtypes = lib.kda_gdr_prefill.argtypes = [T] * 11 + [M, stream]
     lib.kda_decode_window.argtypes = [T] * 11 + [ctypes.POINTER(KdaReplay), M, stream]
     lib.kda_verify.argtypes = [T] * 9 + [stream]
+    lib.kda_ssm_decode.argtypes = [T] * 12 + [ctypes.c_int32, stream]
+    lib.kda_ssm_prefill.argtypes = [T] * 13 + [ctypes.c_int32, stream]
+    lib.kda_norm_residual.argtypes = [T] * 7 + [ctypes.c_float, stream]
+    lib.kda_norm_gate.argtypes = [T] * 4 + [ctypes.c_int32, ctypes.c_int32, ctypes.c_float, stream]
     for name in ("kda_decode", "kda_decode_conv", "kda_prefill", "kda_gdr_decode", "kda_gdr_prefill",
-                 "kda_decode_window", "kda_verify"):
+                 "kda_decode_window", "kda_verify", "kda_ssm_decode", "kda_ssm_prefill", "kda_norm_residual",
+                 "kda_norm_gate"):
         getattr(lib, name).restype = ctypes.c_int
     lib.kda_check_host.argtypes = [ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32),
                                    ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]
@@ -210,6 +223,31 @@ def call_raw_verify(tensors, stream: int = 0) -> int:
     return library().kda_verify(*[ref(t) for t in tensors], ctypes.c_void_p(stream))
 
 
+def call_raw_ssm(tensors, state_layout: int = KDA_STATE_K_FIRST, stream: int = 0) -> int:
+    """Call kda_ssm_decode on 12 prepared descriptors, or kda_ssm_prefill on 13
+    (None passes NULL); returns the status code without raising."""
+    lib = library()
+    ref = lambda t: ctypes.byref(t) if t is not None else None  # noqa: E731
+    fn = lib.kda_ssm_decode if len(tensors) == 12 else lib.kda_ssm_prefill
+    return fn(*[ref(t) for t in tensors], ctypes.c_int32(state_layout), ctypes.c_void_p(stream))
+
+
+def call_raw_norm_residual(tensors, eps: float = 0.0, stream: int = 0) -> int:
+    """Call kda_norm_residual on 7 prepared descriptors (None passes NULL);
+    returns the status code without raising."""
+    ref = lambda t: ctypes.byref(t) if t is not None else None  # noqa: E731
+    return library().kda_norm_residual(*[ref(t) for t in tensors], ctypes.c_float(eps), ctypes.c_void_p(stream))
+
+
+def call_raw_norm_gate(tensors, act: int = KDA_ACT_SIGMOID, gate_first: int = 0, eps: float = 0.0,
+                       stream: int = 0) -> int:
+    """Call kda_norm_gate on 4 prepared descriptors (None passes NULL); returns
+    the status code without raising."""
+    ref = lambda t: ctypes.byref(t) if t is not None else None  # noqa: E731
+    return library().kda_norm_gate(*[ref(t) for t in tensors], ctypes.c_int32(act), ctypes.c_int32(gate_first),
+                                   ctypes.c_float(eps), ctypes.c_void_p(stream))
+
+
 def _descriptor(t, name):
     import torch
     if not isinstance(t, torch.Tensor):
@@ -235,7 +273,10 @@ ARG_NAMES = ("out", "q", "k", "v", "raw_gate", "beta_logits", "a_log", "dt_bias"
 # ---------------------------------------------------------------------------
 
 # kinds of csrc/kda_binding.cpp
-_RECURRENCE, _PREFILL, _CONV, _WINDOW, _VERIFY = range(5)
+(_RECURRENCE, _PREFILL, _CONV, _WINDOW, _VERIFY, _SSM_DECODE, _SSM_PREFILL, _NORM_RESIDUAL,
+ _NORM_GATE) = range(9)
+# tensors of a kind that may be None
+_OPTIONAL = {_VERIFY: (3,), _SSM_DECODE: (4, 8), _SSM_PREFILL: (4, 8), _NORM_RESIDUAL: (5, 6)}
 
 
 def _refuse(tensors, names, dev):
@@ -279,7 +320,7 @@ def _described_call(kind, entry, tensors, dev, gate_mode, lower_bound, l2_eps, s
     more a call): the entry point's status, or None if a tensor cannot be passed."""
     described = []
     for i, t in enumerate(tensors):
-        if t is None and kind == _VERIFY and i == 3:
+        if t is None and i in _OPTIONAL.get(kind, ()):
             described.append(None)
             continue
         try:
@@ -297,6 +338,12 @@ def _described_call(kind, entry, tensors, dev, gate_mode, lower_bound, l2_eps, s
         return call_raw_window(described[:11], KdaReplay(*described[11:]), mode, stream)
     if kind == _VERIFY:
         return call_raw_verify(described, stream)
+    if kind in (_SSM_DECODE, _SSM_PREFILL):
+        return call_raw_ssm(described, state_layout, stream)
+    if kind == _NORM_RESIDUAL:
+        return call_raw_norm_residual(described, l2_eps, stream)
+    if kind == _NORM_GATE:
+        return call_raw_norm_gate(described, gate_mode, matmul, l2_eps, stream)
     if kind == _PREFILL:
         return call_raw_prefill(described, mode, matmul, stream)
     if where == "kda_decode":
@@ -318,8 +365,9 @@ def _call(kind, where, tensors, names, dev, stream, gate_mode=0, lower_bound=0.0
     rc = _native(kind, _ENTRY[where], tensors, dev, gm, lower_bound, l2_eps, scale, sl, matmul,
                  _raw_stream(dev) if stream is None else stream)
     if rc is None:
-        _refuse([t for t in tensors if t is not None or kind != _VERIFY],
-                [n for t, n in zip(tensors, names) if t is not None or kind != _VERIFY], dev)
+        optional = _OPTIONAL.get(kind, ())
+        given = [(t, n) for i, (t, n) in enumerate(zip(tensors, names)) if t is not None or i not in optional]
+        _refuse([t for t, _ in given], [n for _, n in given], dev)
     if rc != KDA_OK:
         raise KdaError(rc, where)
 
@@ -468,3 +516,80 @@ def verify(n_commit, next_token, target_probs, draft_probs, tokens, u_accept, u_
                                  dtype=_torch.float32, device=target_probs.device)
     _call(_VERIFY, "kda_verify", (n_commit, next_token, target_probs, draft_probs, tokens, u_accept, u_sample,
                                   cu_seqlens, workspace), VERIFY_NAMES, dev, stream)
+
+
+SSM_NAMES = ("out", "xbc", "dt", "conv_w", "conv_b", "conv_win", "a_log", "dt_bias", "d_skip", "cu_seqlens",
+             "state_pool", "state_indices", "workspace")
+
+
+def ssm_prefill_workspace(T: int, B: int, H: int, HV: int, dk: int, dv: int, K: int) -> int:
+    """Floats of :func:`ssm_prefill`'s workspace (KDA_SSM_WORKSPACE)."""
+    return ((T // KDA_SSM_CHUNK + B) * H * (192 * dk + 4096) + B * (K - 1) * (HV * dv + 2 * H * dk)
+            + (KDA_SSM_SPLIT * 64 + B * HV * dv) * dk + 2 * KDA_SSM_SPLIT + B * HV + 64)
+
+
+def ssm_decode(out, xbc, dt, conv_w, conv_b, conv_win, a_log, dt_bias, d_skip, cu_seqlens, state_pool,
+               state_indices, *, state_layout="k_first", stream: Optional[int] = None) -> None:
+    """The selective state space scan of a batch's next tokens, with its short
+    causal convolution (kda_ssm_decode in include/kda.h): xbc [1, T, C] holds
+    the channels x | B | C before the convolution, dt [1, T, HV] the time steps
+    before dt_bias; conv_w [K, C], conv_b [C] or None; conv_win [N, K-1, C] and
+    state_pool are updated in place; d_skip [HV] or None."""
+    library()
+    tensors = (out, xbc, dt, conv_w, conv_b, conv_win, a_log, dt_bias, d_skip, cu_seqlens, state_pool, state_indices)
+    _call(_SSM_DECODE, "kda_ssm_decode", tensors, SSM_NAMES, _device(xbc, "xbc"), stream, state_layout=state_layout)
+
+
+def ssm_prefill(out, xbc, dt, conv_w, conv_b, conv_win, a_log, dt_bias, d_skip, cu_seqlens, state_pool,
+                state_indices, *, state_layout="k_first", workspace=None, stream: Optional[int] = None) -> None:
+    """:func:`ssm_decode` for whole prompts (kda_ssm_prefill in include/kda.h):
+    same tensors and result.  ``workspace`` (float32, at least
+    ``ssm_prefill_workspace(...)`` values) is taken from torch's allocator if
+    not given; with ``stream`` given it has to be too, since that memory
+    belongs to torch's current stream."""
+    library()
+    dev = _device(xbc, "xbc")
+    if workspace is None:
+        if stream is not None:
+            raise ValueError("workspace: required with an explicit stream")
+        for t, n, dims in ((out, "out", 4), (xbc, "xbc", 3), (dt, "dt", 3), (conv_w, "conv_w", 2),
+                           (state_pool, "state_pool", 4), (state_indices, "state_indices", 1)):
+            _descriptor(t, n)
+            if t.dim() != dims:
+                raise KdaError(KDA_ERR_SHAPE, "kda_ssm_prefill")
+        T, C, HV, dv = xbc.shape[1], xbc.shape[2], dt.shape[2], out.shape[3]
+        sl = STATE_LAYOUTS[state_layout] if isinstance(state_layout, str) else int(state_layout)
+        dk = state_pool.shape[3 if sl == KDA_STATE_V_FIRST else 2]
+        H = (C - HV * dv) // (2 * dk) if dk > 0 else 0
+        if H < 1:
+            raise KdaError(KDA_ERR_SHAPE, "kda_ssm_prefill")
+        workspace = _torch.empty(ssm_prefill_workspace(T, state_indices.shape[0], H, HV, dk, dv, conv_w.shape[0]),
+                                 dtype=_torch.float32, device=xbc.device)
+    tensors = (out, xbc, dt, conv_w, conv_b, conv_win, a_log, dt_bias, d_skip, cu_seqlens, state_pool, state_indices,
+               workspace)
+    _call(_SSM_PREFILL, "kda_ssm_prefill", tensors, SSM_NAMES, dev, stream, state_layout=state_layout)
+
+
+def norm_residual(hidden_out, normed, hidden, block_out, weight, *, post_weight=None, scale=None, eps=0.0,
+                  stream: Optional[int] = None) -> None:
+    """In front of a block (kda_norm_residual in include/kda.h): hidden_out =
+    hidden + scale * block_out (``post_weight`` given: block_out normalised
+    first), normed = RMS norm of that.  ``hidden_out`` may be ``hidden`` and
+    ``normed`` may be ``block_out``; scale is [D], [1] or None."""
+    library()
+    _call(_NORM_RESIDUAL, "kda_norm_residual", (hidden_out, normed, hidden, block_out, weight, post_weight, scale),
+          ("hidden_out", "normed", "hidden", "block_out", "weight", "post_weight", "scale"),
+          _device(hidden, "hidden"), stream, l2_eps=eps)
+
+
+def norm_gate(out, x, gate, weight, *, activation="sigmoid", gate_first=False, eps=0.0,
+              stream: Optional[int] = None) -> None:
+    """Behind a recurrence (kda_norm_gate in include/kda.h): the RMS norm of x
+    over its last dimension times the activation of ``gate`` ("sigmoid" or
+    "silu"); with ``gate_first`` x is gated before it is normalised.  weight is
+    [D], or [R, D] with R x's second-last extent; ``out`` may be ``x`` or
+    ``gate``."""
+    library()
+    act = ACTIVATIONS[activation] if isinstance(activation, str) else int(activation)
+    _call(_NORM_GATE, "kda_norm_gate", (out, x, gate, weight), ("out", "x", "gate", "weight"), _device(x, "x"),
+          stream, act, l2_eps=eps, matmul=int(gate_first))

@@ -376,6 +376,134 @@ int kda_verify(const kda_tensor* n_commit, const kda_tensor* next_token, const k
                hipStream_t stream);
 
 /*
+ * The selective state space scan with its short causal convolution
+ * (kda_ssm_decode, kda_ssm_prefill), on slots as kda_decode_conv has them.
+ * A token's channels are packed [x | B | C], C = HV*dv + 2*H*dk of them:
+ * x of HV value heads, then B (the write key) and C (the read key) of H
+ * groups, each shared by G = HV / H value heads.  Per token t of a request,
+ * with the K-1 inputs before its first token taken from the slot's window:
+ *     y_t[c] = SiLU(conv_b[c] + sum_{j<K} conv_w[j][c] * xbc_{t-K+1+j}[c])
+ *     step   = softplus(dt[t,hv] + dt_bias[hv])
+ *     S[k][:] = exp(-exp(a_log[hv]) * step) * S[k][:] + step * B[k] * x[:]
+ *     out[t,hv] = C^T S + d_skip[hv] * x
+ * The convolved channels enter the scan in fp32, unrounded; steps, decays and
+ * the state are fp32; out is rounded once (to nearest-even).  Afterwards the
+ * state and the window (the last K-1 inputs) are those after the request's
+ * last token.
+ *
+ * Arguments (B requests, T packed tokens, N slots, K taps):
+ *   out           [1, T, HV, dv]  bf16 or f32, dtype of xbc.  Must not overlap
+ *                                 an input.
+ *   xbc           [1, T, C]       bf16 or f32, before the convolution.
+ *   dt            [1, T, HV]      f32, before dt_bias.
+ *   conv_w        [K, C]          taps, 2 <= K <= 4; f32 or bf16.
+ *   conv_b        [C]             dtype of conv_w; NULL: none.
+ *   conv_win      [N, K-1, C]     f32, oldest input first, IN/OUT.
+ *   a_log, dt_bias [HV]           f32.
+ *   d_skip        [HV]            f32; NULL: none.
+ *   cu_seqlens    [B + 1]         i32, device resident.
+ *   state_pool    [N, HV, dk, dv] or [N, HV, dv, dk], f32 or bf16, IN/OUT.
+ *   state_indices [B]             i32, device resident.
+ *   state_layout  enum kda_state_layout.
+ * H is (C - HV*dv) / (2*dk) and must divide HV.  dk and dv must each be 32,
+ * 64 or 128 (KDA_ERR_UNSUPPORTED); T, N and B stay below 2^31 - 64, B * HV
+ * below 2^22, C below 2^24 and B * C below 2^31 (KDA_ERR_UNSUPPORTED).  Data
+ * are 16-byte aligned.  Preconditions, conventions (a negative index skips a
+ * request: zero rows in out, state and window kept; an empty request changes
+ * nothing) and errors are those of kda_decode.
+ */
+
+/*
+ * kda_ssm_decode - token by token: a batch's next tokens, one or a few per
+ * request.  Two kernels are enqueued on `stream`.
+ */
+int kda_ssm_decode(const kda_tensor* out, const kda_tensor* xbc, const kda_tensor* dt,
+                   const kda_tensor* conv_w, const kda_tensor* conv_b, const kda_tensor* conv_win,
+                   const kda_tensor* a_log, const kda_tensor* dt_bias, const kda_tensor* d_skip,
+                   const kda_tensor* cu_seqlens, const kda_tensor* state_pool,
+                   const kda_tensor* state_indices, int32_t state_layout, hipStream_t stream);
+
+/* Floats of kda_ssm_prefill's workspace, for the sizes of its arguments: the
+ * convolved keys and their products per 64 tokens and group, the windows as
+ * they were, and the states where a long request is split. */
+#define KDA_SSM_CHUNK 64
+#define KDA_SSM_SPLIT 2048
+#define KDA_SSM_WORKSPACE(T, B, H, HV, dk, dv, K)                                                   \
+  (((int64_t)(T) / KDA_SSM_CHUNK + (B)) * (H) * (192 * (int64_t)(dk) + 4096) +                      \
+   (int64_t)(B) * ((K)-1) * ((int64_t)(HV) * (dv) + 2 * (int64_t)(H) * (dk)) +                      \
+   ((int64_t)KDA_SSM_SPLIT * 64 + (int64_t)(B) * (HV) * (dv)) * (dk) + 2 * (int64_t)KDA_SSM_SPLIT + \
+   (int64_t)(B) * (HV) + 64)
+
+/*
+ * kda_ssm_prefill - the same operation for whole prompts, in chunks of 64
+ * tokens on the matrix cores; the result equals the token-by-token scan up to
+ * rounding order.  Operands are split into bf16 terms without loss of range:
+ * three terms for an fp32 pool's state and for f32 outputs (a product is good
+ * to 2^-20), two for bf16 pools and outputs of a bf16 call (2^-13).  Errors are relative to
+ * the sum of the magnitudes of what is added up.  Where the scan has an
+ * infinity or NaN, this call may have NaN, and from up to 63 tokens earlier
+ * of the same request.
+ *   workspace     [>= KDA_SSM_WORKSPACE(...)]  f32; its contents before and
+ *                 after mean nothing.  Calls that may run at the same time
+ *                 need one each.
+ */
+int kda_ssm_prefill(const kda_tensor* out, const kda_tensor* xbc, const kda_tensor* dt,
+                    const kda_tensor* conv_w, const kda_tensor* conv_b, const kda_tensor* conv_win,
+                    const kda_tensor* a_log, const kda_tensor* dt_bias, const kda_tensor* d_skip,
+                    const kda_tensor* cu_seqlens, const kda_tensor* state_pool,
+                    const kda_tensor* state_indices, const kda_tensor* workspace, int32_t state_layout,
+                    hipStream_t stream);
+
+/* Longest row of kda_norm_residual and kda_norm_gate. */
+#define KDA_NORM_MAX 16384
+
+/*
+ * kda_norm_residual - in front of a block: the last block's output enters the
+ * residual stream, and the stream is normalised for the next block.  Per row
+ *     y = block_out,  or  post_weight * block_out * r(block_out)
+ *     h = hidden + scale * y                         -> hidden_out (rounded)
+ *     normed = weight * h * r(h)                     (from the unrounded h)
+ * with r(x) = 1 / sqrt(mean(x^2) + eps), all in fp32.  Sums of squares do not
+ * overflow or underflow.
+ *   hidden_out, hidden  [rows, D]  bf16 or f32, the same; may be one tensor.
+ *   normed, block_out   [rows, D]  bf16 or f32, the same; may be one tensor.
+ *   weight              [D]        f32.
+ *   post_weight         [D]        f32; NULL: block_out is not normalised.
+ *   scale               [D] or [1] f32; NULL: one.
+ *   eps                 finite, >= 0; 0 selects 1e-5.
+ * Leading dimensions may be up to three (row-major); D is the last, 1 to
+ * KDA_NORM_MAX, and at most 2^24 - 1 workgroups take the rows, 32 each for D
+ * up to 64, 16 up to 128, 4 up to 2048 and else one (KDA_ERR_UNSUPPORTED).
+ * Other overlaps are not allowed.  hidden, block_out and the outputs need 16-byte alignment, the
+ * vectors 4 (KDA_ERR_UNSUPPORTED).
+ */
+int kda_norm_residual(const kda_tensor* hidden_out, const kda_tensor* normed, const kda_tensor* hidden,
+                      const kda_tensor* block_out, const kda_tensor* weight, const kda_tensor* post_weight,
+                      const kda_tensor* scale, float eps, hipStream_t stream);
+
+/* Activation of kda_norm_gate's gate. */
+enum kda_norm_act {
+  KDA_ACT_SIGMOID = 0,
+  KDA_ACT_SILU = 1
+};
+
+/*
+ * kda_norm_gate - behind a recurrence: its output normalised and gated.  Per
+ * row (the last dimension)
+ *     out = weight * x * r(x) * act(gate)                    (gate_first 0)
+ *     u = x * act(gate),  out = weight * u * r(u)            (gate_first 1)
+ * with r as above, all in fp32.
+ *   out, x, gate  [..., D]  bf16 or f32, one dtype and shape, 1 to 4
+ *                           dimensions; out may be x or gate.
+ *   weight        [D], or [R, D] with R the second-last extent (a norm of its
+ *                 own per head or group); f32.
+ *   act           enum kda_norm_act;  gate_first 0 or 1 (else KDA_ERR_MODE).
+ * D, rows, eps, overlaps and alignment as for kda_norm_residual.
+ */
+int kda_norm_gate(const kda_tensor* out, const kda_tensor* x, const kda_tensor* gate, const kda_tensor* weight,
+                  int32_t act, int32_t gate_first, float eps, hipStream_t stream);
+
+/*
  * kda_check_host - validate host copies of the decode metadata.  This is a
  * convention of this library, not an operation of the pages: it checks the
  * preconditions of the "KdaDecode" tensor contract (cu_seqlens varlen
