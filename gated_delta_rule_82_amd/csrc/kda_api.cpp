@@ -616,14 +616,15 @@ int plan_ssm(const kda_tensor* out, const kda_tensor* xbc, const kda_tensor* dt,
   if (K < 2 || K > 4) return KDA_ERR_UNSUPPORTED;
   // all further sizes follow from these, within 32 bits
   constexpr int64_t kI32 = std::numeric_limits<int32_t>::max();
-  if (T > kI32 - 64 || N > kI32 - 64 || B > kI32 - 64 || C >= (1 << 24)) return KDA_ERR_UNSUPPORTED;
+  if (T > kI32 - 64 || N > kI32 - 64 || B > kI32 - 64 || C >= (1 << 22)) return KDA_ERR_UNSUPPORTED;
   if (HV < 1 || HV > C / DV) return KDA_ERR_SHAPE;
   const int64_t keys = C - HV * DV;       // B and C of H groups
   if (keys < 2 * DK || keys % (2 * DK) != 0) return KDA_ERR_SHAPE;
   const int64_t H = keys / (2 * DK);
   if (HV % H != 0) return KDA_ERR_SHAPE;
-  // at most 512 work-items per (request, value head); one per window channel
-  if (product_exceeds({B, HV}, (1 << 22) - 1) || product_exceeds({B, C}, kI32)) return KDA_ERR_UNSUPPORTED;
+  // at most 512 work-items per (request, value head) or pair of heads and
+  // segment; one per window channel
+  if (product_exceeds({B, HV}, (1 << 21) - 1) || product_exceeds({B, C}, kI32)) return KDA_ERR_UNSUPPORTED;
 
   const kda_tensor* all[] = {out, xbc, dt, conv_w, conv_win, a_log, dt_bias, cu_seqlens, state_pool, state_indices};
   for (const kda_tensor* t : all)
@@ -632,10 +633,7 @@ int plan_ssm(const kda_tensor* out, const kda_tensor* xbc, const kda_tensor* dt,
   for (const kda_tensor* t : optional)
     if (t != nullptr && !aligned(t, 16)) return KDA_ERR_UNSUPPORTED;
   if (prefill) {
-    // work-items: 256 per 64 tokens and group, and per four waves of a segment
-    if (product_exceeds({T / KDA_SSM_CHUNK + B, H, 256}, kMaxWorkItems) ||
-        product_exceeds({T / KDA_SSM_CHUNK + B + 8, HV * 2 + 3, 64}, kMaxWorkItems))
-      return KDA_ERR_UNSUPPORTED;
+    if (product_exceeds({T / KDA_SSM_CHUNK + B, H, 256}, kMaxWorkItems)) return KDA_ERR_UNSUPPORTED;
     if (workspace->shape[0] < KDA_SSM_WORKSPACE(T, B, H, HV, DK, DV, K)) return KDA_ERR_SHAPE;
   }
 

@@ -47,7 +47,6 @@ constexpr int DK = KDA_SSM_DK;
 constexpr int Q = kSsmChunk;
 constexpr int kKeySteps = DK / 32;      // matrix steps of 32 over the keys
 constexpr int kKeyTiles = DK / 16;
-constexpr int kWaves = 4;               // per workgroup
 constexpr int kMostTerms = 3;
 constexpr int kMinSegment = 256;        // tokens
 
@@ -61,7 +60,9 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 struct Keys {
   u32x4 b[kMostTerms][kKeyTiles][2][kWave];   // rows: 16 keys; 32 tokens
   u32x4 c[kMostTerms][4][kKeySteps][kWave];   // rows: 16 tokens; 32 keys in the accumulators' order
-  f32x4 pairs[4][2][2][kWave];                // rows: 16 tokens t; 32 tokens s; C_t.B_s
+  f32x4 pairs[6][2][kWave];                   // rows: 16 tokens t; 32 tokens s; C_t.B_s.  Tile mt of the first
+                                              // 32 s at mt, tiles 2 and 3 of the second at 4 and 5
+  f32x4 rest[2][2][kWave];                    // (so that whole workgroups copy the pairs)
 };
 static_assert(sizeof(Keys) == 4 * (192 * DK + 4096), "KDA_SSM_WORKSPACE");
 
@@ -163,8 +164,9 @@ __device__ void set_windows(const Plan& p, const Range& range, int b, int slot, 
   }
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(256) ssm_keys(Plan p) {
+// TY terms of C, and of the pairs' operands; TS of B.
+template <bool BF16, int TY, int TS>
+__global__ void __launch_bounds__(256) ssm_keys(Plan p, bool, bool) {
   const SsmArgs& a = p.a;
   constexpr int STRIDE = DK + 2;        // rows 8 apart start 16 banks apart
   __shared__ __attribute__((aligned(16))) float rows[2][Q][STRIDE];   // B, C
@@ -214,15 +216,15 @@ __global__ void __launch_bounds__(256) ssm_keys(Plan p) {
   Keys& out = p.keys[(static_cast<int64_t>(range.t0 / Q) + u.b + u.i) * a.H + h];
   const int col = lane % 16, quad = lane / 16;
 #pragma unroll
-  for (int f = 0; f < kKeyTiles * 2 / kWaves; ++f) {
-    const int tile = (f * kWaves + wave) / 2, step = (f * kWaves + wave) % 2;
+  for (int f = 0; f < kKeyTiles * 2 / 4; ++f) {
+    const int tile = (f * 4 + wave) / 2, step = (f * 4 + wave) % 2;
     float x[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = rows[0][step * 32 + quad * 8 + j][tile * 16 + col];
-    u32x4 term[kMostTerms];
+    u32x4 term[TS];
     split(x, term);
 #pragma unroll
-    for (int n = 0; n < kMostTerms; ++n) out.b[n][tile][step][lane] = term[n];
+    for (int n = 0; n < TS; ++n) out.b[n][tile][step][lane] = term[n];
   }
   f32x4 pairs[4];
 #pragma unroll
@@ -230,20 +232,20 @@ __global__ void __launch_bounds__(256) ssm_keys(Plan p) {
 #pragma unroll
   for (int step = 0; step < kKeySteps; ++step) {
     // 32 keys in the accumulators' order: four of each of two tiles
-    auto fragment = [&](const float (&row)[STRIDE], u32x4 (&term)[kMostTerms]) {
+    auto fragment = [&](const float (&row)[STRIDE], u32x4 (&term)[TY]) {
       float x[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = row[step * 32 + (j / 4) * 16 + quad * 4 + j % 4];
       split(x, term);
     };
-    u32x4 c[kMostTerms];
+    u32x4 c[TY];
     fragment(rows[1][wave * 16 + col], c);
 #pragma unroll
-    for (int n = 0; n < kMostTerms; ++n) out.c[n][wave][step][lane] = c[n];
+    for (int n = 0; n < TY; ++n) out.c[n][wave][step][lane] = c[n];
 #pragma unroll
     for (int st = 0; st < 4; ++st) {
       if (st > wave) break;
-      u32x4 b[kMostTerms];
+      u32x4 b[TY];
       fragment(rows[0][st * 16 + col], b);
       pairs[st] = product(c, b, pairs[st]);
     }
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(256) ssm_keys(Plan p) {
   for (int step = 0; step < 2; ++step)
 #pragma unroll
     for (int half = 0; half < 2; ++half)
-      out.pairs[wave][step][half][lane] =
+      if (wave >= 2 * step) out.pairs[wave + 2 * step][half][lane] =
           *reinterpret_cast<const f32x4*>(square + (wave * 16 + col) * PSTRIDE + step * 32 + quad * 8 + half * 4);
 }
 
@@ -272,66 +274,191 @@ __global__ void __launch_bounds__(256) ssm_keys(Plan p) {
 
 enum Mode { kWhole, kSegment, kJoined };
 
-// NT values per lane of one row of x: adjacent columns.
-template <int NT, bool BF16>
-__device__ __forceinline__ void load_row(const void* base, int64_t at, float (&x)[NT]) {
-  if constexpr (BF16) {
-    const uint16_t* const p = static_cast<const uint16_t*>(base) + at;
-    if constexpr (NT == 4) {
-      const u32x2 w = *reinterpret_cast<const u32x2*>(p);
-      x[0] = bf16_to_f32(w.x & 0xffffu);
-      x[1] = __uint_as_float(w.x & 0xffff0000u);
-      x[2] = bf16_to_f32(w.y & 0xffffu);
-      x[3] = __uint_as_float(w.y & 0xffff0000u);
-    } else {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-      x[0] = bf16_to_f32(w & 0xffffu);
-      x[1] = __uint_as_float(w & 0xffff0000u);
-    }
-  } else {
-    const float* const p = static_cast<const float*>(base) + at;
-    if constexpr (NT == 4) {
-      const f32x4 w = *reinterpret_cast<const f32x4*>(p);
+constexpr int NT = 2;                   // 16-column tiles of a wave; a lane's columns are adjacent
+constexpr int kColumns = NT * 16;
+constexpr int kWaves = 8;               // of a workgroup, all of one group
+constexpr int kThreads = kWaves * kWave;
+
+// A workgroup's LDS: the chunk's operands, each read by all waves, and each
+// wave's own step sizes and decays.
+template <int TY, int TS>
+struct Shared {
+  u32x4 b[TS][kKeyTiles][2][kWave];
+  u32x4 c[TY][4][kKeySteps][kWave];
+  f32x4 pairs[8][2][kWave];             // the last two are not used
+  struct {
+    float hi[Q], lo[Q];                 // c in two parts, base 2
+    float decay[Q];                     // exp(g_t)
+    float from[Q];                      // exp(c_t)
+    float step[Q];
+  } wave[kWaves];
+};
+
+// N pieces of 16 bytes, from memory to LDS by way of the threads' registers.
+template <int N>
+struct Staged {
+  static constexpr int PER = (N + kThreads - 1) / kThreads;
+  u32x4 w[PER];
+  __device__ __forceinline__ void load(const u32x4* from) {
 #pragma unroll
-      for (int n = 0; n < 4; ++n) x[n] = w[n];
+    for (int i = 0; i < PER; ++i) {
+      const int at = i * kThreads + static_cast<int>(threadIdx.x);
+      if (N % kThreads == 0 || at < N) w[i] = from[at];
+    }
+  }
+  __device__ __forceinline__ void store(u32x4* to) const {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int at = i * kThreads + static_cast<int>(threadIdx.x);
+      if (N % kThreads == 0 || at < N) to[at] = w[i];
+    }
+  }
+};
+
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// A lane's inputs of a chunk: tokens 32 step + 8 quad + 0 .. 7 and the three
+// before them, its two columns.
+template <bool BF16>
+struct Inputs {
+  static constexpr int ROWS = 8 + kPast;
+  uint32_t w[2][ROWS][BF16 ? 1 : 2];
+
+  // Rows t0 - 3 .. t0 + valid - 1 of the request, through a resource of just
+  // these: others read as zero.  Before the first token there are none.
+  __device__ __forceinline__ void load(const SsmArgs& a, const Range& range, int t0, int valid, int quad, int column) {
+    constexpr int E = BF16 ? 2 : 4;
+    const int before = t0 > 0 ? kPast : 0;
+    const int stride = a.C * E;
+    const char* const base =
+        static_cast<const char*>(a.xbc) + (static_cast<int64_t>(range.t0) + t0 - before) * a.C * E;
+    const __amdgpu_buffer_rsrc_t r = tile_resource(const_cast<char*>(base), (valid + before) * stride);
+    const int first = (quad * 8 - kPast + before) * stride + column * E;
+#pragma unroll
+    for (int step = 0; step < 2; ++step)
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+        const int at = first + (step * 32 + j) * stride;    // below zero: out of range as an unsigned offset
+        if constexpr (BF16) {
+          w[step][j][0] = __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
+        } else {
+          const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0);
+          w[step][j][0] = x.x;
+          w[step][j][1] = x.y;
+        }
+      }
+  }
+  __device__ __forceinline__ float get(int step, int j, int n) const {
+    if constexpr (BF16) return n == 0 ? __uint_as_float(w[step][j][0] << 16) : __uint_as_float(w[step][j][0] & 0xffff0000u);
+    else return __uint_as_float(w[step][j][n]);
+  }
+};
+
+// A wave's part of a state tile [DK][dv] or [dv][DK] at `tile`: keys
+// kt * 16 + quad * 4 + i, columns v + n.
+template <bool SBF16, bool VFIRST, bool STORE>
+__device__ __forceinline__ void move_state(__amdgpu_buffer_rsrc_t tile, int dv, int quad, int v,
+                                           f32x4 (&S)[kKeyTiles][NT]) {
+  constexpr int E = SBF16 ? 2 : 4;
+#pragma unroll
+  for (int kt = 0; kt < kKeyTiles; ++kt) {
+    if constexpr (VFIRST) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int at = ((v + n) * DK + kt * 16 + quad * 4) * E;
+        float x[4];
+        if constexpr (STORE) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = S[kt][n][i];
+          StateIO<SBF16, 4>::store(tile, at, 0, x);
+        } else {
+          StateIO<SBF16, 4>::load(tile, at, 0, x);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) S[kt][n][i] = x[i];
+        }
+      }
     } else {
-      const float2 w = *reinterpret_cast<const float2*>(p);
-      x[0] = w.x;
-      x[1] = w.y;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = ((kt * 16 + quad * 4 + i) * dv + v) * E;
+        if constexpr (STORE) {
+          if constexpr (SBF16) {
+            __builtin_amdgcn_raw_buffer_store_b32(f32x2_to_bf16x2_rne(S[kt][0][i], S[kt][1][i]), tile, at, 0, 0);
+          } else {
+            const u32x2 w = {__float_as_uint(S[kt][0][i]), __float_as_uint(S[kt][1][i])};
+            __builtin_amdgcn_raw_buffer_store_b64(w, tile, at, 0, 0);
+          }
+        } else if constexpr (SBF16) {
+          const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(tile, at, 0, 0);
+          S[kt][0][i] = bf16_to_f32(w & 0xffffu);
+          S[kt][1][i] = __uint_as_float(w & 0xffff0000u);
+        } else {
+          const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(tile, at, 0, 0);
+          S[kt][0][i] = __uint_as_float(w.x);
+          S[kt][1][i] = __uint_as_float(w.y);
+        }
+      }
     }
   }
 }
 
-template <int NT, bool BF16>
-__device__ __forceinline__ void store_row(void* base, int64_t at, const float (&x)[NT]) {
-#pragma unroll
-  for (int n = 0; n < NT; n += 2) store_pair<BF16>(base, at + n, x[n], x[n + 1]);
+template <bool STORE>
+__device__ __forceinline__ void move_pool(__amdgpu_buffer_rsrc_t tile, bool state_bf16, bool v_first, int dv, int quad,
+                                          int v, f32x4 (&S)[kKeyTiles][NT]) {
+  if (state_bf16) {
+    if (v_first) move_state<true, true, STORE>(tile, dv, quad, v, S);
+    else move_state<true, false, STORE>(tile, dv, quad, v, S);
+  } else {
+    if (v_first) move_state<false, true, STORE>(tile, dv, quad, v, S);
+    else move_state<false, false, STORE>(tile, dv, quad, v, S);
+  }
 }
 
-template <int NT, bool BF16, int TY, int TS, int MODE>
-__global__ void __launch_bounds__(256, 1) ssm_scan(Plan p, bool state_bf16, bool v_first) {
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_from(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, ROWS, 0xf, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, ROWS, 0xf, true);
+  return x + __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// Sum over this lane and those before it: within rows of 16, then the rows'
+// last lanes to the rows behind.
+__device__ __forceinline__ double running_sum(double x) {
+  x = add_from<0x111, 0xf>(x);
+  x = add_from<0x112, 0xf>(x);
+  x = add_from<0x114, 0xf>(x);
+  x = add_from<0x118, 0xf>(x);
+  x = add_from<0x142, 0xa>(x);
+  return add_from<0x143, 0xc>(x);
+}
+
+template <bool BF16, int TY, int TS, int MODE>
+__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) ssm_scan(Plan p, bool state_bf16, bool v_first) {
   const SsmArgs& a = p.a;
-  constexpr int COLS = NT * 16;
-  __shared__ __attribute__((aligned(16))) float sums[kWaves][3][Q];   // c in two parts (base 2), step
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  Shared<TY, TS>& sh = *reinterpret_cast<Shared<TY, TS>*>(lds);
   const int dv = (a.C - 2 * a.H * DK) / a.HV;
-  const int slabs = dv / COLS;
-  const int waves = a.HV * slabs, blocks = (waves + kWaves - 1) / kWaves;
+  const int slabs = dv / kColumns;
+  const int waves = a.G * slabs, blocks = (waves + kWaves - 1) / kWaves;    // of a group
 
-  // workgroups of a unit share its keys: on one XCD, where there are units
-  // for all of them
-  int unit, block;
-  if (p.units >= kXcds) {
-    const int xcd = blockIdx.x % kXcds, i = blockIdx.x / kXcds;
-    unit = i / blocks * kXcds + xcd;
+  // the workgroups of a unit's group share its keys: on one XCD, where there
+  // are groups for all of them
+  const int groups = p.units * a.H;
+  int group = blockIdx.x / blocks, block = blockIdx.x % blocks;
+  if (groups >= kXcds) {
+    const int i = blockIdx.x / kXcds;
+    group = i / blocks * kXcds + blockIdx.x % kXcds;
     block = i % blocks;
-  } else {
-    unit = blockIdx.x / blocks;
-    block = blockIdx.x % blocks;
+    if (group >= groups) return;
   }
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int w = block * kWaves + wave;
-  if (unit >= p.units || w >= waves) return;
-  const int hv = w / slabs, slab = w % slabs;
+  const int unit = group / a.H, h = group % a.H;
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);    // a scalar
   Unit u = {unit, 0};
   if constexpr (MODE != kWhole) u = find_unit(a, unit, p.segment);
   const Range range = request_range(a, u.b);
@@ -341,47 +468,39 @@ __global__ void __launch_bounds__(256, 1) ssm_scan(Plan p, bool state_bf16, bool
   if (u.i < 0 || wide_begin >= range.n) return;
   const int begin = static_cast<int>(wide_begin);
   const int end = MODE == kWhole || range.n - begin < p.segment ? range.n : begin + p.segment;
+
+  // waves behind the group's last help with its operands
+  const int w = block * kWaves + wave;
+  const bool works = w < waves;
+  const int hv = h * a.G + (works ? w / slabs : 0), slab = works ? w % slabs : 0;
   const int col = lane % 16, quad = lane / 16;
-  const int column = hv * dv + slab * COLS + col * NT;      // the lane's first column: of out, and channel of x
-  const int64_t out_row = static_cast<int64_t>(a.HV) * dv;
+  const int v = slab * kColumns + col * NT;       // the lane's first column of the head
+  const int column = hv * dv + v;                 // ... of out, and its channel of x
+  const int out_row = a.HV * dv;
+  constexpr int E = BF16 ? 2 : 4;
   if (slot < 0) {
-    if constexpr (MODE != kSegment) {
-      const float zero[NT] = {};
+    if (MODE != kSegment && works) {
       for (int t = begin + quad; t < end; t += 4)
-        store_row<NT, BF16>(a.out, (static_cast<int64_t>(range.t0) + t) * out_row + column, zero);
+        store_pair<BF16>(a.out, (static_cast<int64_t>(range.t0) + t) * out_row + column, 0.0f, 0.0f);
     }
     return;
   }
 
-  // state tile: keys kt * 16 + quad * 4 + i, columns col * NT + n
   f32x4 S[kKeyTiles][NT];
-  const int64_t tile = (static_cast<int64_t>(slot) * a.HV + hv) * DK * dv;
-  const int vcol = slab * COLS + col * NT;
-  const int64_t here = static_cast<int64_t>(range.t0 / (MODE == kWhole ? 1 : p.segment)) + u.b + u.i;
-  float* const kept = MODE == kWhole ? nullptr : p.states + (here * a.HV + hv) * DK * dv;
+  const int64_t here = MODE == kWhole ? 0 : static_cast<int64_t>(range.t0 / p.segment) + u.b + u.i;
+  const int tile_bytes = DK * dv * (MODE == kWhole && state_bf16 ? 2 : 4);
+  char* const tile =
+      MODE == kWhole ? static_cast<char*>(a.state_pool) + (static_cast<int64_t>(slot) * a.HV + hv) * tile_bytes
+                     : reinterpret_cast<char*>(p.states) + (here * a.HV + hv) * tile_bytes;
   if constexpr (MODE == kWhole) {
-#pragma unroll
-    for (int kt = 0; kt < kKeyTiles; ++kt)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = kt * 16 + quad * 4 + i;
-          const int64_t at = tile + (v_first ? static_cast<int64_t>(vcol + n) * DK + k
-                                             : static_cast<int64_t>(k) * dv + vcol + n);
-          S[kt][n][i] = state_bf16 ? load_scalar<true>(a.state_pool, at) : load_scalar<false>(a.state_pool, at);
-        }
+    move_pool<false>(tile_resource(tile, tile_bytes), state_bf16, v_first, dv, quad, v, S);
+  } else if constexpr (MODE == kJoined) {
+    move_state<false, false, false>(tile_resource(tile, tile_bytes), dv, quad, v, S);
   } else {
 #pragma unroll
     for (int kt = 0; kt < kKeyTiles; ++kt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float x[NT] = {};
-        if constexpr (MODE == kJoined)
-          load_row<NT, false>(kept, static_cast<int64_t>(kt * 16 + quad * 4 + i) * dv + vcol, x);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) S[kt][n][i] = x[n];
-      }
+      for (int n = 0; n < NT; ++n) S[kt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
   Taps taps[NT];
@@ -389,212 +508,251 @@ __global__ void __launch_bounds__(256, 1) ssm_scan(Plan p, bool state_bf16, bool
   for (int n = 0; n < NT; ++n) taps[n].load(a, column + n);
   const float amp = exp_f(a.a_log[hv]), bias = a.dt_bias[hv];
   const float skip = a.d_skip != nullptr ? a.d_skip[hv] : 0.0f;
-  const int h = hv / a.G;
-  const int64_t first_key = static_cast<int64_t>(range.t0 / Q) + u.b;
-  float* const hi = sums[wave][0];
-  float* const lo = sums[wave][1];
-  float* const steps = sums[wave][2];
-  double gone = 0.0;                    // log2 of the segment's decay
+  auto& own = sh.wave[wave];
+  float gone = 1.0f;                    // the segment's decay
 
-  for (int t0 = begin; t0 < end; t0 += Q) {
+  const Keys* keys = p.keys + (static_cast<int64_t>(range.t0 / Q) + u.b + begin / Q) * a.H + h;
+  // the first rows of c, then pairs, follow each other in Keys and here
+  constexpr int kC = TY * 4 * kKeySteps * kWave, kPairs = 8 * 2 * kWave, kB = TS * kKeyTiles * 2 * kWave;
+  Staged<kC> stage_c;
+  Staged<kPairs> stage_pairs;
+  Staged<kB> stage_b;
+  Inputs<BF16> in;
+  auto load_step = [&](int t0, int valid) {
+    const int64_t t = static_cast<int64_t>(range.t0) + t0 + min(lane, valid - 1);
+    return a.dt[t * a.HV + hv];
+  };
+  float dt = load_step(begin, min(Q, end - begin));
+  in.load(a, range, begin, min(Q, end - begin), quad, column);
+  if constexpr (MODE != kSegment) {
+    stage_c.load(&keys->c[0][0][0][0]);
+    stage_pairs.load(reinterpret_cast<const u32x4*>(&keys->pairs[0][0][0]));
+    stage_c.store(&sh.c[0][0][0][0]);
+    stage_pairs.store(reinterpret_cast<u32x4*>(&sh.pairs[0][0][0]));
+  }
+
+  for (int t0 = begin; t0 < end; t0 += Q, keys += a.H) {
     const int valid = min(Q, end - t0);
-    const Keys& keys = p.keys[(first_key + t0 / Q) * a.H + h];
-    // steps and the running sum of the decays, one token per lane
-    double c;
-    {
-      const int64_t t = static_cast<int64_t>(range.t0) + t0 + min(lane, valid - 1);
-      const float step = lane < valid ? softplus_f(a.dt[t * a.HV + hv] + bias) : 0.0f;
-      c = static_cast<double>(step) * static_cast<double>(-amp) * 1.4426950408889634;
-#pragma unroll
-      for (int d = 1; d < kWave; d *= 2) {
-        const double before = __shfl_up(c, d);
-        if (lane >= d) c += before;
-      }
-      const float part = static_cast<float>(c);
-      __builtin_amdgcn_wave_barrier();
-      hi[lane] = part;
-      lo[lane] = static_cast<float>(c - static_cast<double>(part));
-      steps[lane] = step;
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-    }
-    const double total = __shfl(c, kWave - 1);
-    gone += total;
-    const float total_hi = static_cast<float>(total);
-    const float total_lo = static_cast<float>(total - static_cast<double>(total_hi));
-
-    f32x4 y[4][NT];
-    if constexpr (MODE != kSegment) {
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) y[mt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      // C^T S0
-#pragma unroll
-      for (int step = 0; step < kKeySteps; ++step) {
-        u32x4 s[NT][TY];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float x[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = S[2 * step + j / 4][n][j % 4];
-          split(x, s[n]);
-        }
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-          u32x4 ck[TY];
-#pragma unroll
-          for (int m = 0; m < TY; ++m) ck[m] = keys.c[m][mt][step][lane];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) y[mt][n] = product(ck, s[n], y[mt][n]);
-        }
-      }
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        const f32x4 ch = *reinterpret_cast<const f32x4*>(hi + mt * 16 + quad * 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float f = __builtin_amdgcn_exp2f(ch[i]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) y[mt][n][i] *= f;
-        }
-      }
-    }
+    // The lane's place, anew in every chunk: addresses and comparisons made of
+    // it would otherwise be kept in registers through all of them.
+    int col = lane % 16, quad = lane / 16;
+    asm volatile("" : "+v"(col), "+v"(quad));
+    const int column = hv * dv + slab * kColumns + col * NT;
+    lds_barrier();            // c and pairs are there, and b has been read
     const bool update = MODE != kJoined || t0 + Q < end;     // a joined segment's last state is not used
+    stage_b.load(&keys->b[0][0][0][0]);
+
+    // steps and the running sum of the decays, one token per lane
+    float total;              // the chunk's decay
     {
-      const float f = __builtin_amdgcn_exp2f(total_hi);
-#pragma unroll
-      for (int kt = 0; kt < kKeyTiles; ++kt)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) S[kt][n] *= f;
+      const float step = lane < valid ? softplus_f(dt + bias) : 0.0f;
+      const double g = static_cast<double>(step) * static_cast<double>(-amp) * 1.4426950408889634;
+      const double c = running_sum(g);
+      const float part = static_cast<float>(c);
+      own.hi[lane] = part;
+      own.lo[lane] = static_cast<float>(c - static_cast<double>(part));
+      own.decay[lane] = __builtin_amdgcn_exp2f(static_cast<float>(g));
+      const float from = __builtin_amdgcn_exp2f(part);
+      own.from[lane] = from;
+      own.step[lane] = step;
+      total = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(from), kWave - 1));
+      gone *= total;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+      __builtin_amdgcn_wave_barrier();
     }
 
+    // the lane's columns, convolved
+    float x[2][8][NT];
 #pragma unroll
-    for (int step = 0; step < 2; ++step) {
-      const int first = step * 32 + quad * 8;       // the lane's eight tokens of the chunk
-      if (step * 32 >= valid) break;
-      float x[8][NT];
-      {
-        float in[8 + kPast][NT];
+    for (int step = 0; step < 2; ++step)
 #pragma unroll
-        for (int j = 0; j < 8 + kPast; ++j) {
-          const int t = min(max(t0 + first + j - kPast, 0), end - 1);
-          load_row<NT, BF16>(a.xbc, (static_cast<int64_t>(range.t0) + t) * a.C + column, in[j]);
+      for (int n = 0; n < NT; ++n) {
+        float past[kPast];
+#pragma unroll
+        for (int j = 0; j < kPast; ++j) {
+          past[j] = in.get(step, j, n);
+          const int r = a.K - 1 - kPast + j;
+          if (step == 0 && t0 == 0 && quad == 0 && r >= 0)    // the window of before
+            past[j] = p.windows[(static_cast<int64_t>(u.b) * (a.K - 1) + r) * a.C + column + n];
         }
-        if (t0 == 0 && step == 0) {                 // the window of before
 #pragma unroll
-          for (int j = 0; j < kPast; ++j) {
-            const int r = a.K - 1 - kPast + j;
-            if (quad == 0) {
-              if (r >= 0)
-                load_row<NT, false>(p.windows, (static_cast<int64_t>(u.b) * (a.K - 1) + r) * a.C + column, in[j]);
-            }
-          }
+        for (int j = 0; j < 8; ++j) {
+          const float next = in.get(step, j + kPast, n);
+          x[step][j][n] = silu_f(taps[n].dot(a.K, past[0], past[1], past[2], next));
+          past[0] = past[1];
+          past[1] = past[2];
+          past[2] = next;
         }
+      }
+    if (valid < Q) {
+#pragma unroll
+      for (int step = 0; step < 2; ++step)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
+          for (int n = 0; n < NT; ++n)
+            if (step * 32 + quad * 8 + j >= valid) x[step][j][n] = 0.0f;
+    }
+
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (MODE != kSegment) {
+      if (works) {
+        f32x4 y[4][NT];
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) y[mt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        // C^T S0
+#pragma unroll
+        for (int step = 0; step < kKeySteps; ++step) {
+          u32x4 s[NT][TY];
+#pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const float z = silu_f(taps[n].dot(a.K, in[j][n], in[j + 1][n], in[j + 2][n], in[j + 3][n]));
-            x[j][n] = first + j < valid ? z : 0.0f;
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = S[2 * step + j / 4][n][j % 4];
+            split(f, s[n]);
+          }
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            u32x4 ck[TY];
+#pragma unroll
+            for (int m = 0; m < TY; ++m) ck[m] = sh.c[m][mt][step][lane];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) y[mt][n] = product(ck, s[n], y[mt][n]);
+          }
+        }
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+          const f32x4 f = *reinterpret_cast<const f32x4*>(own.from + mt * 16 + quad * 4);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) y[mt][n] *= f;
+        }
+        // the chunk's own tokens
+#pragma unroll
+        for (int step = 0; step < 2; ++step) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (step * 32 >= valid) break;
+          u32x4 xs[NT][TY];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = x[step][j][n];
+            split(f, xs[n]);
+          }
+          const int first = step * 32 + quad * 8;       // the lane's eight tokens s
+          const float last_hi = own.hi[first + 7], last_lo = own.lo[first + 7];
+          float decay[8], d[8];
+#pragma unroll
+          for (int j = 0; j < 8; j += 4) {
+            const f32x4 e = *reinterpret_cast<const f32x4*>(own.decay + first + j);
+            const f32x4 s = *reinterpret_cast<const f32x4*>(own.step + first + j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              decay[j + i] = e[i];
+              d[j + i] = s[i];
+            }
+          }
+#pragma unroll
+          for (int mt = 2 * step; mt < 4; ++mt) {
+            const int t = mt * 16 + col;
+            const bool diagonal = mt < 2 * step + 2;
+            const f32x4 p0 = sh.pairs[mt + 2 * step][0][lane], p1 = sh.pairs[mt + 2 * step][1][lane];
+            // exp(c_t - c_s), from the last s backwards; one where s >= t
+            float f = __builtin_amdgcn_exp2f(
+                fminf((own.hi[t] - last_hi) + (own.lo[t] - last_lo), 0.0f));
+            float m[8];
+#pragma unroll
+            for (int j = 7; j >= 0; --j) {
+              if (j < 7) f *= !diagonal || first + j + 1 <= t ? decay[j + 1] : 1.0f;
+              const float pair = (j < 4 ? p0[j % 4] : p1[j % 4]) * d[j];
+              m[j] = pair * f;
+              if (diagonal) m[j] = first + j < t ? m[j] : (first + j == t ? pair + skip : 0.0f);
+            }
+            u32x4 ms[TY];
+            split(m, ms);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) y[mt][n] = product(ms, xs[n], y[mt][n]);
+          }
+        }
+        const __amdgpu_buffer_rsrc_t out = tile_resource(
+            static_cast<char*>(a.out) + (static_cast<int64_t>(range.t0) + t0) * out_row * E, valid * out_row * E);
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = ((mt * 16 + quad * 4 + i) * out_row + column) * E;     // rows behind the last are dropped
+            if constexpr (BF16) {
+              __builtin_amdgcn_raw_buffer_store_b32(f32x2_to_bf16x2_rne(y[mt][0][i], y[mt][1][i]), out, at, 0, 0);
+            } else {
+              const u32x2 o = {__float_as_uint(y[mt][0][i]), __float_as_uint(y[mt][1][i])};
+              __builtin_amdgcn_raw_buffer_store_b64(o, out, at, 0, 0);
+            }
           }
       }
-      const f32x4 h0 = *reinterpret_cast<const f32x4*>(hi + first), h1 = *reinterpret_cast<const f32x4*>(hi + first + 4);
-      const f32x4 l0 = *reinterpret_cast<const f32x4*>(lo + first), l1 = *reinterpret_cast<const f32x4*>(lo + first + 4);
-      const f32x4 d0 = *reinterpret_cast<const f32x4*>(steps + first);
-      const f32x4 d1 = *reinterpret_cast<const f32x4*>(steps + first + 4);
+    }
+    stage_b.store(&sh.b[0][0][0][0]);
+    lds_barrier();            // b is there, and c and pairs have been read
+
+    const int next = t0 + Q;
+    if (next < end) {
+      dt = load_step(next, min(Q, end - next));
+      in.load(a, range, next, min(Q, end - next), quad, column);
       if constexpr (MODE != kSegment) {
-        u32x4 xs[NT][TY];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float v[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = x[j][n];
-          split(v, xs[n]);
-        }
-#pragma unroll
-        for (int mt = 2 * step; mt < 4; ++mt) {
-          const int t = mt * 16 + col;
-          const float th = hi[t], tl = lo[t];
-          const f32x4 p0 = keys.pairs[mt][step][0][lane], p1 = keys.pairs[mt][step][1][lane];
-          float m[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float ch = j < 4 ? h0[j % 4] : h1[j % 4], cl = j < 4 ? l0[j % 4] : l1[j % 4];
-            const float pair = (j < 4 ? p0[j % 4] : p1[j % 4]) * (j < 4 ? d0[j % 4] : d1[j % 4]);
-            const float f = pair * __builtin_amdgcn_exp2f((th - ch) + (tl - cl));
-            m[j] = first + j < t ? f : (first + j == t ? pair + skip : 0.0f);
-          }
-          u32x4 ms[TY];
-          split(m, ms);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) y[mt][n] = product(ms, xs[n], y[mt][n]);
-        }
+        stage_c.load(&(keys + a.H)->c[0][0][0][0]);
+        stage_pairs.load(reinterpret_cast<const u32x4*>(&(keys + a.H)->pairs[0][0][0]));
       }
-      if (update) {
-        float f[8];
+    }
+    if (update && works) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float ch = j < 4 ? h0[j % 4] : h1[j % 4], cl = j < 4 ? l0[j % 4] : l1[j % 4];
-          f[j] = __builtin_amdgcn_exp2f((total_hi - ch) + (total_lo - cl)) * (j < 4 ? d0[j % 4] : d1[j % 4]);
+      for (int kt = 0; kt < kKeyTiles; ++kt)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) S[kt][n] *= total;
+#pragma unroll
+      for (int step = 0; step < 2; ++step) {
+        if (step * 32 >= valid) break;
+        const int first = step * 32 + quad * 8;
+        // step_s exp(c_last - c_s), from the last s backwards
+        float f = __builtin_amdgcn_exp2f((own.hi[Q - 1] - own.hi[first + 7]) + (own.lo[Q - 1] - own.lo[first + 7]));
+        float g[8];
+#pragma unroll
+        for (int j = 7; j >= 0; --j) {
+          if (j < 7) f *= own.decay[first + j + 1];
+          g[j] = f * own.step[first + j];
         }
         u32x4 xs[NT][TS];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          float v[8];
+          float e[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = x[j][n] * f[j];
-          split(v, xs[n]);
+          for (int j = 0; j < 8; ++j) e[j] = x[step][j][n] * g[j];
+          split(e, xs[n]);
         }
 #pragma unroll
         for (int kt = 0; kt < kKeyTiles; ++kt) {
           u32x4 bk[TS];
 #pragma unroll
-          for (int m = 0; m < TS; ++m) bk[m] = keys.b[m][kt][step][lane];
+          for (int m = 0; m < TS; ++m) bk[m] = sh.b[m][kt][step][lane];
 #pragma unroll
           for (int n = 0; n < NT; ++n) S[kt][n] = product(bk, xs[n], S[kt][n]);
         }
       }
     }
     if constexpr (MODE != kSegment) {
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = mt * 16 + quad * 4 + i;
-          float o[NT];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) o[n] = y[mt][n][i];
-          if (t < valid)
-            store_row<NT, BF16>(a.out, (static_cast<int64_t>(range.t0) + t0 + t) * out_row + column, o);
-        }
+      if (next < end) {
+        stage_c.store(&sh.c[0][0][0][0]);
+        stage_pairs.store(reinterpret_cast<u32x4*>(&sh.pairs[0][0][0]));
+      }
     }
   }
 
+  if (!works) return;
   if constexpr (MODE == kWhole) {
-#pragma unroll
-    for (int kt = 0; kt < kKeyTiles; ++kt)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = kt * 16 + quad * 4 + i;
-          const int64_t at = tile + (v_first ? static_cast<int64_t>(vcol + n) * DK + k
-                                             : static_cast<int64_t>(k) * dv + vcol + n);
-          if (state_bf16) store_scalar<true>(a.state_pool, at, S[kt][n][i]);
-          else store_scalar<false>(a.state_pool, at, S[kt][n][i]);
-        }
+    move_pool<true>(tile_resource(tile, tile_bytes), state_bf16, v_first, dv, quad, v, S);
   } else if constexpr (MODE == kSegment) {
-#pragma unroll
-    for (int kt = 0; kt < kKeyTiles; ++kt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float o[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) o[n] = S[kt][n][i];
-        store_row<NT, false>(kept, static_cast<int64_t>(kt * 16 + quad * 4 + i) * dv + vcol, o);
-      }
-    if (slab == 0 && lane == 0) p.decays[here * a.HV + hv] = static_cast<float>(exp2(gone));
+    move_state<false, false, true>(tile_resource(tile, tile_bytes), dv, quad, v, S);
+    if (slab == 0 && lane == 0) p.decays[here * a.HV + hv] = gone;
   }
 }
 
@@ -644,34 +802,37 @@ __global__ void __launch_bounds__(256) ssm_join(Plan p, bool state_bf16, bool v_
 // launch
 // ---------------------------------------------------------------------------
 
-template <int NT, bool BF16, int TY, int TS, int MODE>
+template <bool BF16, int TY, int TS, int MODE>
 hipError_t scan(const Plan& plan, int dv, bool state_bf16, bool v_first, hipStream_t stream) {
-  const int64_t blocks = (static_cast<int64_t>(plan.a.HV) * (dv / (NT * 16)) + kWaves - 1) / kWaves;
-  const int64_t units = plan.units >= kXcds ? (plan.units + kXcds - 1) / kXcds * kXcds : plan.units;
+  const void* const fn = reinterpret_cast<const void*>(&ssm_scan<BF16, TY, TS, MODE>);
+  constexpr int bytes = sizeof(Shared<TY, TS>);
+  if constexpr (bytes > 65536) {        // beyond the default limit of dynamic LDS
+    const hipError_t rc = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (rc != hipSuccess) return rc;
+  }
+  const int64_t blocks = (static_cast<int64_t>(plan.a.G) * (dv / kColumns) + kWaves - 1) / kWaves;
+  int64_t groups = static_cast<int64_t>(plan.units) * plan.a.H;
+  if (groups >= kXcds) groups = (groups + kXcds - 1) / kXcds * kXcds;
   void* kargs[] = {const_cast<Plan*>(&plan), &state_bf16, &v_first};
-  return hipLaunchKernel(reinterpret_cast<const void*>(&ssm_scan<NT, BF16, TY, TS, MODE>),
-                         dim3(static_cast<uint32_t>(units * blocks)), dim3(kWaves * kWave), kargs, 0, stream);
+  return hipLaunchKernel(fn, dim3(static_cast<uint32_t>(groups * blocks)), dim3(kThreads), kargs, bytes, stream);
 }
 
-template <int NT, bool BF16, int TY, int TS>
-hipError_t scans(const Plan& plan, int dv, bool state_bf16, bool v_first, hipStream_t stream) {
-  if (plan.segment == 0) return scan<NT, BF16, TY, TS, kWhole>(plan, dv, state_bf16, v_first, stream);
-  hipError_t rc = scan<NT, BF16, TY, TS, kSegment>(plan, dv, state_bf16, v_first, stream);
-  if (rc != hipSuccess) return rc;
+template <bool BF16, int TY, int TS>
+hipError_t run(const Plan& plan, int dv, bool state_bf16, bool v_first, hipStream_t stream) {
   void* kargs[] = {const_cast<Plan*>(&plan), &state_bf16, &v_first};
+  const int64_t chunks = static_cast<int64_t>(plan.a.T) / Q + plan.a.B;
+  hipError_t rc = hipLaunchKernel(reinterpret_cast<const void*>(&ssm_keys<BF16, TY, TS>),
+                                  dim3(static_cast<uint32_t>(chunks * plan.a.H)), dim3(256), kargs, 0, stream);
+  if (rc != hipSuccess) return rc;
+  if (plan.segment == 0) return scan<BF16, TY, TS, kWhole>(plan, dv, state_bf16, v_first, stream);
+  rc = scan<BF16, TY, TS, kSegment>(plan, dv, state_bf16, v_first, stream);
+  if (rc != hipSuccess) return rc;
   const int64_t blocks = static_cast<int64_t>(plan.a.B) * plan.a.HV * (DK * dv / 1024);
   rc = hipLaunchKernel(reinterpret_cast<const void*>(&ssm_join), dim3(static_cast<uint32_t>(blocks)), dim3(256), kargs,
                        0, stream);
   if (rc != hipSuccess) return rc;
   // the state of a joined segment only reaches its outputs
-  return scan<NT, BF16, TY, TY, kJoined>(plan, dv, state_bf16, v_first, stream);
-}
-
-template <int NT>
-hipError_t scans(const Plan& plan, int dv, bool bf16, bool state_bf16, bool v_first, hipStream_t stream) {
-  if (!bf16) return scans<NT, false, 3, 3>(plan, dv, state_bf16, v_first, stream);
-  if (state_bf16) return scans<NT, true, 2, 2>(plan, dv, state_bf16, v_first, stream);
-  return scans<NT, true, 2, 3>(plan, dv, state_bf16, v_first, stream);
+  return scan<BF16, TY, TY, kJoined>(plan, dv, state_bf16, v_first, stream);
 }
 
 }  // namespace
@@ -698,15 +859,11 @@ int launch_ssm_prefill_dk<DK>(const SsmArgs& args, int dv, bool bf16, bool state
       plan.decays = plan.states + static_cast<int64_t>(plan.units) * args.HV * DK * dv;
     }
   }
-  void* kargs[] = {&plan};
-  const uint32_t blocks = static_cast<uint32_t>(chunks * args.H);
-  hipError_t rc = hipLaunchKernel(bf16 ? reinterpret_cast<const void*>(&ssm_keys<true>)
-                                       : reinterpret_cast<const void*>(&ssm_keys<false>),
-                                  dim3(blocks), dim3(256), kargs, 0, stream);
-  if (rc != hipSuccess) return KDA_ERR_LAUNCH;
   const bool v_first = state_layout == KDA_STATE_V_FIRST;
-  rc = dv == 32 ? scans<2>(plan, dv, bf16, state_bf16, v_first, stream)
-                : scans<4>(plan, dv, bf16, state_bf16, v_first, stream);
+  hipError_t rc;
+  if (!bf16) rc = run<false, 3, 3>(plan, dv, state_bf16, v_first, stream);
+  else if (state_bf16) rc = run<true, 2, 2>(plan, dv, state_bf16, v_first, stream);
+  else rc = run<true, 2, 3>(plan, dv, state_bf16, v_first, stream);
   return rc == hipSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }
 
