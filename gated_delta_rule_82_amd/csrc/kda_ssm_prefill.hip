@@ -56,19 +56,18 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 // workspace
 // ---------------------------------------------------------------------------
 
-// What ssm_keys leaves of a chunk and group: fragments of 64 lanes x 16 bytes.
+// What ssm_keys leaves of 32 tokens and a group: fragments of 64 lanes x 16
+// bytes.
 struct Keys {
-  u32x4 b[kMostTerms][kKeyTiles][2][kWave];   // rows: 16 keys; 32 tokens
-  u32x4 c[kMostTerms][4][kKeySteps][kWave];   // rows: 16 tokens; 32 keys in the accumulators' order
-  f32x4 pairs[6][2][kWave];                   // rows: 16 tokens t; 32 tokens s; C_t.B_s.  Tile mt of the first
-                                              // 32 s at mt, tiles 2 and 3 of the second at 4 and 5
-  f32x4 rest[2][2][kWave];                    // (so that whole workgroups copy the pairs)
+  u32x4 b[kMostTerms][kKeyTiles][kWave];      // rows: 16 keys; 32 tokens
+  u32x4 c[kMostTerms][2][kKeySteps][kWave];   // rows: 16 tokens; 32 keys in the accumulators' order
+  f32x4 pairs[2][2][kWave];                   // rows: 16 tokens t; 32 tokens s; C_t.B_s
 };
-static_assert(sizeof(Keys) == 4 * (192 * DK + 4096), "KDA_SSM_WORKSPACE");
+static_assert(sizeof(Keys) == 4 * (96 * DK + 1024), "KDA_SSM_WORKSPACE");
 
 struct Plan {
   SsmArgs a;
-  Keys* keys;           // [chunk slot][H]
+  Keys* keys;           // [chunk slot][H][2]
   float* windows;       // [B][K-1][C], as they were
   float* states;        // [segment slot][HV][DK][DV]: what a segment adds, then the state before it
   float* decays;        // [segment slot][HV]
@@ -213,7 +212,7 @@ __global__ void __launch_bounds__(256) ssm_keys(Plan p, bool, bool) {
   __syncthreads();
   if (u.i == 0) set_windows<BF16>(p, range, u.b, slot, h);
 
-  Keys& out = p.keys[(static_cast<int64_t>(range.t0 / Q) + u.b + u.i) * a.H + h];
+  Keys* const out = p.keys + ((static_cast<int64_t>(range.t0 / Q) + u.b + u.i) * a.H + h) * 2;
   const int col = lane % 16, quad = lane / 16;
 #pragma unroll
   for (int f = 0; f < kKeyTiles * 2 / 4; ++f) {
@@ -224,11 +223,13 @@ __global__ void __launch_bounds__(256) ssm_keys(Plan p, bool, bool) {
     u32x4 term[TS];
     split(x, term);
 #pragma unroll
-    for (int n = 0; n < TS; ++n) out.b[n][tile][step][lane] = term[n];
+    for (int n = 0; n < TS; ++n) out[step].b[n][tile][lane] = term[n];
   }
-  f32x4 pairs[4];
+  // pairs of the wave's 16 tokens t with the 32 tokens s of its half
+  const int half = wave / 2, mt = wave % 2;
+  f32x4 pairs[2];
 #pragma unroll
-  for (int st = 0; st < 4; ++st) pairs[st] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int st = 0; st < 2; ++st) pairs[st] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int step = 0; step < kKeySteps; ++step) {
     // 32 keys in the accumulators' order: four of each of two tiles
@@ -241,31 +242,28 @@ __global__ void __launch_bounds__(256) ssm_keys(Plan p, bool, bool) {
     u32x4 c[TY];
     fragment(rows[1][wave * 16 + col], c);
 #pragma unroll
-    for (int n = 0; n < TY; ++n) out.c[n][wave][step][lane] = c[n];
+    for (int n = 0; n < TY; ++n) out[half].c[n][mt][step][lane] = c[n];
 #pragma unroll
-    for (int st = 0; st < 4; ++st) {
-      if (st > wave) break;
+    for (int st = 0; st < 2; ++st) {
+      if (st > mt) break;
       u32x4 b[TY];
-      fragment(rows[0][st * 16 + col], b);
+      fragment(rows[0][half * 32 + st * 16 + col], b);
       pairs[st] = product(c, b, pairs[st]);
     }
   }
   // rows t, columns s -> operand order, through LDS
   __syncthreads();
-  constexpr int PSTRIDE = Q + 4;
-  float* const square = &rows[0][0][0];
+  constexpr int PSTRIDE = 32 + 4;
+  float* const square = &rows[0][0][0] + wave * 16 * PSTRIDE;
   static_assert(Q * PSTRIDE <= 2 * Q * STRIDE, "the pairs fit where B and C were");
 #pragma unroll
-  for (int st = 0; st < 4; ++st)
+  for (int st = 0; st < 2; ++st)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) square[(wave * 16 + quad * 4 + i) * PSTRIDE + st * 16 + col] = pairs[st][i];
+    for (int i = 0; i < 4; ++i) square[(quad * 4 + i) * PSTRIDE + st * 16 + col] = pairs[st][i];
   __syncthreads();
 #pragma unroll
-  for (int step = 0; step < 2; ++step)
-#pragma unroll
-    for (int half = 0; half < 2; ++half)
-      if (wave >= 2 * step) out.pairs[wave + 2 * step][half][lane] =
-          *reinterpret_cast<const f32x4*>(square + (wave * 16 + col) * PSTRIDE + step * 32 + quad * 8 + half * 4);
+  for (int part = 0; part < 2; ++part)
+    out[half].pairs[mt][part][lane] = *reinterpret_cast<const f32x4*>(square + col * PSTRIDE + quad * 8 + part * 4);
 }
 
 // ---------------------------------------------------------------------------
@@ -276,21 +274,22 @@ enum Mode { kWhole, kSegment, kJoined };
 
 constexpr int NT = 2;                   // 16-column tiles of a wave; a lane's columns are adjacent
 constexpr int kColumns = NT * 16;
-constexpr int kWaves = 8;               // of a workgroup, all of one group
+constexpr int kWaves = 4;               // of a workgroup, all of one group
+constexpr int R = 32;                   // tokens at a time
 constexpr int kThreads = kWaves * kWave;
 
 // A workgroup's LDS: the chunk's operands, each read by all waves, and each
 // wave's own step sizes and decays.
 template <int TY, int TS>
 struct Shared {
-  u32x4 b[TS][kKeyTiles][2][kWave];
-  u32x4 c[TY][4][kKeySteps][kWave];
-  f32x4 pairs[8][2][kWave];             // the last two are not used
+  u32x4 b[TS][kKeyTiles][kWave];
+  u32x4 c[TY][2][kKeySteps][kWave];
+  f32x4 pairs[2][2][kWave];
   struct {
-    float hi[Q], lo[Q];                 // c in two parts, base 2
-    float decay[Q];                     // exp(g_t)
-    float from[Q];                      // exp(c_t)
-    float step[Q];
+    float hi[R], lo[R];                 // c in two parts, base 2
+    float decay[R];                     // exp(g_t)
+    float from[R];                      // exp(c_t)
+    float step[R];
   } wave[kWaves];
 };
 
@@ -321,12 +320,12 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// A lane's inputs of a chunk: tokens 32 step + 8 quad + 0 .. 7 and the three
-// before them, its two columns.
+// A lane's inputs: tokens 8 quad + 0 .. 7 and the three before them, its two
+// columns.
 template <bool BF16>
 struct Inputs {
   static constexpr int ROWS = 8 + kPast;
-  uint32_t w[2][ROWS][BF16 ? 1 : 2];
+  uint32_t w[ROWS][BF16 ? 1 : 2];
 
   // Rows t0 - 3 .. t0 + valid - 1 of the request, through a resource of just
   // these: others read as zero.  Before the first token there are none.
@@ -339,22 +338,20 @@ struct Inputs {
     const __amdgpu_buffer_rsrc_t r = tile_resource(const_cast<char*>(base), (valid + before) * stride);
     const int first = (quad * 8 - kPast + before) * stride + column * E;
 #pragma unroll
-    for (int step = 0; step < 2; ++step)
-#pragma unroll
-      for (int j = 0; j < ROWS; ++j) {
-        const int at = first + (step * 32 + j) * stride;    // below zero: out of range as an unsigned offset
-        if constexpr (BF16) {
-          w[step][j][0] = __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
-        } else {
-          const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0);
-          w[step][j][0] = x.x;
-          w[step][j][1] = x.y;
-        }
+    for (int j = 0; j < ROWS; ++j) {
+      const int at = first + j * stride;        // below zero: out of range as an unsigned offset
+      if constexpr (BF16) {
+        w[j][0] = __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
+      } else {
+        const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0);
+        w[j][0] = x.x;
+        w[j][1] = x.y;
       }
+    }
   }
-  __device__ __forceinline__ float get(int step, int j, int n) const {
-    if constexpr (BF16) return n == 0 ? __uint_as_float(w[step][j][0] << 16) : __uint_as_float(w[step][j][0] & 0xffff0000u);
-    else return __uint_as_float(w[step][j][n]);
+  __device__ __forceinline__ float get(int j, int n) const {
+    if constexpr (BF16) return n == 0 ? __uint_as_float(w[j][0] << 16) : __uint_as_float(w[j][0] & 0xffff0000u);
+    else return __uint_as_float(w[j][n]);
   }
 };
 
@@ -438,7 +435,7 @@ __device__ __forceinline__ double running_sum(double x) {
 }
 
 template <bool BF16, int TY, int TS, int MODE>
-__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) ssm_scan(Plan p, bool state_bf16, bool v_first) {
+__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(MODE == kSegment ? 3 : 2, MODE == kSegment ? 3 : 2))) ssm_scan(Plan p, bool state_bf16, bool v_first) {
   const SsmArgs& a = p.a;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   Shared<TY, TS>& sh = *reinterpret_cast<Shared<TY, TS>*>(lds);
@@ -511,95 +508,113 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
   auto& own = sh.wave[wave];
   float gone = 1.0f;                    // the segment's decay
 
-  const Keys* keys = p.keys + (static_cast<int64_t>(range.t0 / Q) + u.b + begin / Q) * a.H + h;
-  // the first rows of c, then pairs, follow each other in Keys and here
-  constexpr int kC = TY * 4 * kKeySteps * kWave, kPairs = 8 * 2 * kWave, kB = TS * kKeyTiles * 2 * kWave;
+  constexpr int kC = TY * 2 * kKeySteps * kWave, kPairs = 2 * 2 * kWave, kB = TS * kKeyTiles * kWave;
   Staged<kC> stage_c;
   Staged<kPairs> stage_pairs;
   Staged<kB> stage_b;
   Inputs<BF16> in;
-  auto load_step = [&](int t0, int valid) {
+  float dt;
+  const Keys* const first_keys = p.keys + ((static_cast<int64_t>(range.t0 / Q) + u.b) * a.H + h) * 2;
+  auto keys_at = [&](int t0) { return first_keys + static_cast<int64_t>(t0 / Q) * a.H * 2 + t0 / R % 2; };
+  auto load = [&](int t0, int quad, int column) {
+    const int valid = min(R, end - t0);
     const int64_t t = static_cast<int64_t>(range.t0) + t0 + min(lane, valid - 1);
-    return a.dt[t * a.HV + hv];
+    dt = a.dt[t * a.HV + hv];
+    in.load(a, range, t0, valid, quad, column);
+    if constexpr (MODE != kSegment) {
+      const Keys* const keys = keys_at(t0);
+      stage_c.load(&keys->c[0][0][0][0]);
+      stage_pairs.load(reinterpret_cast<const u32x4*>(&keys->pairs[0][0][0]));
+    }
   };
-  float dt = load_step(begin, min(Q, end - begin));
-  in.load(a, range, begin, min(Q, end - begin), quad, column);
-  if constexpr (MODE != kSegment) {
-    stage_c.load(&keys->c[0][0][0][0]);
-    stage_pairs.load(reinterpret_cast<const u32x4*>(&keys->pairs[0][0][0]));
-    stage_c.store(&sh.c[0][0][0][0]);
-    stage_pairs.store(reinterpret_cast<u32x4*>(&sh.pairs[0][0][0]));
-  }
+  auto store = [&]() {
+    if constexpr (MODE != kSegment) {
+      stage_c.store(&sh.c[0][0][0][0]);
+      stage_pairs.store(reinterpret_cast<u32x4*>(&sh.pairs[0][0][0]));
+    }
+  };
+  load(begin, quad, column);
+  store();
 
-  for (int t0 = begin; t0 < end; t0 += Q, keys += a.H) {
-    const int valid = min(Q, end - t0);
-    // The lane's place, anew in every chunk: addresses and comparisons made of
-    // it would otherwise be kept in registers through all of them.
+  for (int t0 = begin; t0 < end; t0 += R) {
+    const int valid = min(R, end - t0);
+    // The lane's place, anew for every 32 tokens: addresses and comparisons
+    // made of it would otherwise be kept in registers through all of them.
     int col = lane % 16, quad = lane / 16;
     asm volatile("" : "+v"(col), "+v"(quad));
     const int column = hv * dv + slab * kColumns + col * NT;
     lds_barrier();            // c and pairs are there, and b has been read
-    const bool update = MODE != kJoined || t0 + Q < end;     // a joined segment's last state is not used
-    stage_b.load(&keys->b[0][0][0][0]);
+    const bool update = MODE != kJoined || t0 + R < end;     // a joined segment's last state is not used
+    stage_b.load(&keys_at(t0)->b[0][0][0]);
 
     // steps and the running sum of the decays, one token per lane
-    float total;              // the chunk's decay
+    float total;              // the decay over all 32
     {
       const float step = lane < valid ? softplus_f(dt + bias) : 0.0f;
       const double g = static_cast<double>(step) * static_cast<double>(-amp) * 1.4426950408889634;
       const double c = running_sum(g);
       const float part = static_cast<float>(c);
-      own.hi[lane] = part;
-      own.lo[lane] = static_cast<float>(c - static_cast<double>(part));
-      own.decay[lane] = __builtin_amdgcn_exp2f(static_cast<float>(g));
       const float from = __builtin_amdgcn_exp2f(part);
-      own.from[lane] = from;
-      own.step[lane] = step;
-      total = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(from), kWave - 1));
+      if (lane < R) {
+        own.hi[lane] = part;
+        own.lo[lane] = static_cast<float>(c - static_cast<double>(part));
+        own.decay[lane] = __builtin_amdgcn_exp2f(static_cast<float>(g));
+        own.from[lane] = from;
+        own.step[lane] = step;
+      }
+      total = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(from), R - 1));
       gone *= total;
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
       __builtin_amdgcn_wave_barrier();
     }
 
     // the lane's columns, convolved
-    float x[2][8][NT];
+    float x[8][NT];
 #pragma unroll
-    for (int step = 0; step < 2; ++step)
+    for (int n = 0; n < NT; ++n) {
+      float past[kPast];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float past[kPast];
-#pragma unroll
-        for (int j = 0; j < kPast; ++j) {
-          past[j] = in.get(step, j, n);
-          const int r = a.K - 1 - kPast + j;
-          if (step == 0 && t0 == 0 && quad == 0 && r >= 0)    // the window of before
-            past[j] = p.windows[(static_cast<int64_t>(u.b) * (a.K - 1) + r) * a.C + column + n];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float next = in.get(step, j + kPast, n);
-          x[step][j][n] = silu_f(taps[n].dot(a.K, past[0], past[1], past[2], next));
-          past[0] = past[1];
-          past[1] = past[2];
-          past[2] = next;
-        }
+      for (int j = 0; j < kPast; ++j) {
+        past[j] = in.get(j, n);
+        const int r = a.K - 1 - kPast + j;
+        if (t0 == 0 && quad == 0 && r >= 0)     // the window of before
+          past[j] = p.windows[(static_cast<int64_t>(u.b) * (a.K - 1) + r) * a.C + column + n];
       }
-    if (valid < Q) {
 #pragma unroll
-      for (int step = 0; step < 2; ++step)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            if (step * 32 + quad * 8 + j >= valid) x[step][j][n] = 0.0f;
+      for (int j = 0; j < 8; ++j) {
+        const float next = in.get(j + kPast, n);
+        x[j][n] = silu_f(taps[n].dot(a.K, past[0], past[1], past[2], next));
+        past[0] = past[1];
+        past[1] = past[2];
+        past[2] = next;
+      }
     }
+    if (valid < R) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          if (quad * 8 + j >= valid) x[j][n] = 0.0f;
+    }
+    const int first = quad * 8;         // the lane's eight tokens s
+    float decay[8], d[8];
+#pragma unroll
+    for (int j = 0; j < 8; j += 4) {
+      const f32x4 e = *reinterpret_cast<const f32x4*>(own.decay + first + j);
+      const f32x4 f = *reinterpret_cast<const f32x4*>(own.step + first + j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        decay[j + i] = e[i];
+        d[j + i] = f[i];
+      }
+    }
+    const float last_hi = own.hi[first + 7], last_lo = own.lo[first + 7];
 
-    __builtin_amdgcn_sched_barrier(0);
     if constexpr (MODE != kSegment) {
       if (works) {
-        f32x4 y[4][NT];
+        f32x4 y[2][NT];
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int n = 0; n < NT; ++n) y[mt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         // C^T S0
@@ -614,7 +629,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
             split(f, s[n]);
           }
 #pragma unroll
-          for (int mt = 0; mt < 4; ++mt) {
+          for (int mt = 0; mt < 2; ++mt) {
             u32x4 ck[TY];
 #pragma unroll
             for (int m = 0; m < TY; ++m) ck[m] = sh.c[m][mt][step][lane];
@@ -623,63 +638,42 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
           }
         }
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
+        for (int mt = 0; mt < 2; ++mt) {
           const f32x4 f = *reinterpret_cast<const f32x4*>(own.from + mt * 16 + quad * 4);
 #pragma unroll
           for (int n = 0; n < NT; ++n) y[mt][n] *= f;
         }
-        // the chunk's own tokens
+        // the 32 tokens' own
+        u32x4 xs[NT][TY];
 #pragma unroll
-        for (int step = 0; step < 2; ++step) {
-          __builtin_amdgcn_sched_barrier(0);
-          if (step * 32 >= valid) break;
-          u32x4 xs[NT][TY];
+        for (int n = 0; n < NT; ++n) {
+          float f[8];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float f[8];
+          for (int j = 0; j < 8; ++j) f[j] = x[j][n];
+          split(f, xs[n]);
+        }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = x[step][j][n];
-            split(f, xs[n]);
+        for (int mt = 0; mt < 2; ++mt) {
+          const int t = mt * 16 + col;
+          const f32x4 p0 = sh.pairs[mt][0][lane], p1 = sh.pairs[mt][1][lane];
+          // exp(c_t - c_s), from the last s backwards; one where s >= t
+          float f = __builtin_amdgcn_exp2f(fminf((own.hi[t] - last_hi) + (own.lo[t] - last_lo), 0.0f));
+          float m[8];
+#pragma unroll
+          for (int j = 7; j >= 0; --j) {
+            if (j < 7) f *= first + j + 1 <= t ? decay[j + 1] : 1.0f;
+            const float pair = (j < 4 ? p0[j % 4] : p1[j % 4]) * d[j];
+            m[j] = first + j < t ? pair * f : (first + j == t ? pair + skip : 0.0f);
           }
-          const int first = step * 32 + quad * 8;       // the lane's eight tokens s
-          const float last_hi = own.hi[first + 7], last_lo = own.lo[first + 7];
-          float decay[8], d[8];
+          u32x4 ms[TY];
+          split(m, ms);
 #pragma unroll
-          for (int j = 0; j < 8; j += 4) {
-            const f32x4 e = *reinterpret_cast<const f32x4*>(own.decay + first + j);
-            const f32x4 s = *reinterpret_cast<const f32x4*>(own.step + first + j);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              decay[j + i] = e[i];
-              d[j + i] = s[i];
-            }
-          }
-#pragma unroll
-          for (int mt = 2 * step; mt < 4; ++mt) {
-            const int t = mt * 16 + col;
-            const bool diagonal = mt < 2 * step + 2;
-            const f32x4 p0 = sh.pairs[mt + 2 * step][0][lane], p1 = sh.pairs[mt + 2 * step][1][lane];
-            // exp(c_t - c_s), from the last s backwards; one where s >= t
-            float f = __builtin_amdgcn_exp2f(
-                fminf((own.hi[t] - last_hi) + (own.lo[t] - last_lo), 0.0f));
-            float m[8];
-#pragma unroll
-            for (int j = 7; j >= 0; --j) {
-              if (j < 7) f *= !diagonal || first + j + 1 <= t ? decay[j + 1] : 1.0f;
-              const float pair = (j < 4 ? p0[j % 4] : p1[j % 4]) * d[j];
-              m[j] = pair * f;
-              if (diagonal) m[j] = first + j < t ? m[j] : (first + j == t ? pair + skip : 0.0f);
-            }
-            u32x4 ms[TY];
-            split(m, ms);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) y[mt][n] = product(ms, xs[n], y[mt][n]);
-          }
+          for (int n = 0; n < NT; ++n) y[mt][n] = product(ms, xs[n], y[mt][n]);
         }
         const __amdgpu_buffer_rsrc_t out = tile_resource(
             static_cast<char*>(a.out) + (static_cast<int64_t>(range.t0) + t0) * out_row * E, valid * out_row * E);
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int at = ((mt * 16 + quad * 4 + i) * out_row + column) * E;     // rows behind the last are dropped
@@ -692,59 +686,38 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
           }
       }
     }
-    stage_b.store(&sh.b[0][0][0][0]);
+    stage_b.store(&sh.b[0][0][0]);
     lds_barrier();            // b is there, and c and pairs have been read
 
-    const int next = t0 + Q;
-    if (next < end) {
-      dt = load_step(next, min(Q, end - next));
-      in.load(a, range, next, min(Q, end - next), quad, column);
-      if constexpr (MODE != kSegment) {
-        stage_c.load(&(keys + a.H)->c[0][0][0][0]);
-        stage_pairs.load(reinterpret_cast<const u32x4*>(&(keys + a.H)->pairs[0][0][0]));
-      }
-    }
+    const int next = t0 + R;
+    if (next < end) load(next, quad, column);
     if (update && works) {
+      // step_s exp(c_last - c_s), from the last s backwards
+      float f = __builtin_amdgcn_exp2f((own.hi[R - 1] - last_hi) + (own.lo[R - 1] - last_lo));
+      float g[8];
 #pragma unroll
-      for (int kt = 0; kt < kKeyTiles; ++kt)
+      for (int j = 7; j >= 0; --j) {
+        if (j < 7) f *= decay[j + 1];
+        g[j] = f * d[j];
+      }
+      u32x4 xs[NT][TS];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) S[kt][n] *= total;
+      for (int n = 0; n < NT; ++n) {
+        float e[8];
 #pragma unroll
-      for (int step = 0; step < 2; ++step) {
-        if (step * 32 >= valid) break;
-        const int first = step * 32 + quad * 8;
-        // step_s exp(c_last - c_s), from the last s backwards
-        float f = __builtin_amdgcn_exp2f((own.hi[Q - 1] - own.hi[first + 7]) + (own.lo[Q - 1] - own.lo[first + 7]));
-        float g[8];
+        for (int j = 0; j < 8; ++j) e[j] = x[j][n] * g[j];
+        split(e, xs[n]);
+      }
 #pragma unroll
-        for (int j = 7; j >= 0; --j) {
-          if (j < 7) f *= own.decay[first + j + 1];
-          g[j] = f * own.step[first + j];
-        }
-        u32x4 xs[NT][TS];
+      for (int kt = 0; kt < kKeyTiles; ++kt) {
+        u32x4 bk[TS];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float e[8];
+        for (int m = 0; m < TS; ++m) bk[m] = sh.b[m][kt][lane];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) e[j] = x[step][j][n] * g[j];
-          split(e, xs[n]);
-        }
-#pragma unroll
-        for (int kt = 0; kt < kKeyTiles; ++kt) {
-          u32x4 bk[TS];
-#pragma unroll
-          for (int m = 0; m < TS; ++m) bk[m] = sh.b[m][kt][step][lane];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) S[kt][n] = product(bk, xs[n], S[kt][n]);
-        }
+        for (int n = 0; n < NT; ++n) S[kt][n] = product(bk, xs[n], S[kt][n] * total);
       }
     }
-    if constexpr (MODE != kSegment) {
-      if (next < end) {
-        stage_c.store(&sh.c[0][0][0][0]);
-        stage_pairs.store(reinterpret_cast<u32x4*>(&sh.pairs[0][0][0]));
-      }
-    }
+    if (next < end) store();
   }
 
   if (!works) return;
@@ -844,7 +817,7 @@ int launch_ssm_prefill_dk<DK>(const SsmArgs& args, int dv, bool bf16, bool state
   plan.a = args;
   const int64_t chunks = static_cast<int64_t>(args.T) / Q + args.B;
   plan.keys = reinterpret_cast<Keys*>(args.workspace);
-  plan.windows = reinterpret_cast<float*>(plan.keys + chunks * args.H);
+  plan.windows = reinterpret_cast<float*>(plan.keys + chunks * args.H * 2);
   plan.states = plan.windows + static_cast<int64_t>(args.B) * (args.K - 1) * args.C;
   const int64_t waves = static_cast<int64_t>(args.HV) * (dv > 64 ? 2 : 1);
   plan.units = args.B;
