@@ -1,5 +1,5 @@
 // kda_ssm_prefill.hip - the selective state space scan over whole prompts
-// (kda_ssm_prefill), in chunks of 64 tokens on the matrix cores.
+// (kda_ssm_prefill), in chunks of 32 tokens on the matrix cores.
 //
 // With g_t = -exp(a_log) step_t and c_t its running sum since the chunk's
 // start, S0 the state before the chunk and x', B, C the convolved channels:
@@ -67,12 +67,13 @@ static_assert(sizeof(Keys) == 4 * (96 * DK + 1024), "KDA_SSM_WORKSPACE");
 
 struct Plan {
   SsmArgs a;
-  Keys* keys;           // [chunk slot][H][2]
+  Keys* keys;           // [chunk slot][H]
   float* windows;       // [B][K-1][C], as they were
   float* states;        // [segment slot][HV][DK][DV]: what a segment adds, then the state before it
   float* decays;        // [segment slot][HV]
   int32_t segment;      // tokens per segment, 0: not split
   int32_t units;        // segment slots, or B
+  uint32_t key_blocks;  // workgroups of ssm_keys that have a chunk
 };
 
 // Requests' chunks (or segments) are numbered through: request b's begin at
@@ -123,6 +124,19 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
                                                  0);
 }
 
+// c[i][n] += a[i] b[n] in N terms each, small products first; term by term over
+// all of c, so that an instruction does not wait for the one before it.
+template <int M, int N, int L>
+__device__ __forceinline__ void products(const u32x4 (&a)[M][N], const u32x4 (&b)[L][N], f32x4 (&c)[M][L]) {
+  constexpr int kOrder[6][2] = {{0, 2}, {2, 0}, {1, 1}, {0, 1}, {1, 0}, {0, 0}};
+#pragma unroll
+  for (int o = N == 3 ? 0 : 3; o < 6; ++o)
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+#pragma unroll
+      for (int n = 0; n < L; ++n) c[i][n] = mfma(a[i][kOrder[o][0]], b[n][kOrder[o][1]], c[i][n]);
+}
+
 // c += a b in N terms each, small products first.
 template <int N>
 __device__ __forceinline__ f32x4 product(const u32x4 (&a)[N], const u32x4 (&b)[N], f32x4 c) {
@@ -140,26 +154,25 @@ __device__ __forceinline__ f32x4 product(const u32x4 (&a)[N], const u32x4 (&b)[N
 // keys
 // ---------------------------------------------------------------------------
 
-// The workgroup of a request's first chunk keeps the old windows of its
-// group's channels and sets the new ones; no other reads them.
+// The new window of request b's channel c; `kept`, if given, takes the old one.
 template <bool BF16>
-__device__ void set_windows(const Plan& p, const Range& range, int b, int slot, int h) {
+__device__ __forceinline__ void set_window(const Plan& p, const Range& range, int b, int slot, int c, bool keep) {
   const SsmArgs& a = p.a;
-  const int dv = (a.C - 2 * a.H * DK) / a.HV;
-  const int mine = a.G * dv;
-  for (int i = threadIdx.x; i < mine + 2 * DK; i += 256) {
-    const int keys = a.HV * dv + h * DK;
-    const int c = i < mine ? h * mine + i : (i < mine + DK ? keys + (i - mine) : keys + a.H * DK + (i - mine - DK));
-    float* const win = a.conv_win + static_cast<int64_t>(slot) * (a.K - 1) * a.C + c;
-    float* const kept = p.windows + static_cast<int64_t>(b) * (a.K - 1) * a.C + c;
-    float x[kPast];
-    for (int j = 0; j < a.K - 1; ++j) kept[static_cast<int64_t>(j) * a.C] = win[static_cast<int64_t>(j) * a.C];
-    for (int j = 0; j < a.K - 1; ++j) {
-      const int t = range.n - (a.K - 1) + j;
-      x[j] = t >= 0 ? load_scalar<BF16>(a.xbc, (static_cast<int64_t>(range.t0) + t) * a.C + c)
-                    : win[static_cast<int64_t>(a.K - 1 + t) * a.C];
-    }
-    for (int j = 0; j < a.K - 1; ++j) win[static_cast<int64_t>(j) * a.C] = x[j];
+  float* const win = a.conv_win + static_cast<int64_t>(slot) * (a.K - 1) * a.C + c;
+  float old[kPast], next[kPast];
+#pragma unroll
+  for (int j = 0; j < kPast; ++j) {
+    if (j >= a.K - 1) continue;
+    const int t = range.n - (a.K - 1) + j;      // of the request; below zero: of the old window
+    old[j] = win[static_cast<int64_t>(j) * a.C];
+    next[j] = t >= 0 ? load_scalar<BF16>(a.xbc, (static_cast<int64_t>(range.t0) + t) * a.C + c)
+                     : win[static_cast<int64_t>(a.K - 1 + t) * a.C];
+  }
+#pragma unroll
+  for (int j = 0; j < kPast; ++j) {
+    if (j >= a.K - 1) continue;
+    if (keep) p.windows[(static_cast<int64_t>(b) * (a.K - 1) + j) * a.C + c] = old[j];
+    win[static_cast<int64_t>(j) * a.C] = next[j];
   }
 }
 
@@ -169,69 +182,92 @@ __global__ void __launch_bounds__(256) ssm_keys(Plan p, bool, bool) {
   const SsmArgs& a = p.a;
   constexpr int STRIDE = DK + 2;        // rows 8 apart start 16 banks apart
   __shared__ __attribute__((aligned(16))) float rows[2][Q][STRIDE];   // B, C
+  constexpr int PSTRIDE = Q + 4;
+  __shared__ __attribute__((aligned(16))) float squares[2][Q][PSTRIDE];
+  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int channels = a.C - 2 * a.H * DK;      // of x
+  if (blockIdx.x >= p.key_blocks) {
+    // windows of x, which ssm_scan finds in the workspace
+    const int blocks = (channels + 255) / 256;
+    const int i = blockIdx.x - p.key_blocks, b = i / blocks, c = i % blocks * 256 + tid;
+    const Range range = request_range(a, b);
+    const int slot = request_slot(a, b);
+    if (slot >= 0 && range.n > 0 && c < channels) set_window<BF16>(p, range, b, slot, c, true);
+    return;
+  }
   const int h = blockIdx.x % a.H;
   const Unit u = find_unit(a, blockIdx.x / a.H, Q);
   const Range range = request_range(a, u.b);
   const int slot = request_slot(a, u.b);
   if (slot < 0 || u.i < 0 || static_cast<int64_t>(u.i) * Q >= range.n) return;
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int begin = u.i * Q, valid = min(Q, range.n - begin);
 
-  // a channel per thread, over all tokens or a part of them
+  // two adjacent channels per thread, over a part of the tokens
   {
-    constexpr int PARTS = 256 / (2 * DK), TOKENS = Q / PARTS;
-    const int i = tid % (2 * DK), part = tid / (2 * DK);
+    constexpr int PARTS = 256 / DK, TOKENS = Q / PARTS;
+    const int i = tid % DK * 2, part = tid / DK;
     const int which = i / DK, k = i % DK;
-    const int c = a.C - 2 * a.H * DK + which * a.H * DK + h * DK + k;
-    Taps taps;
-    taps.load(a, c);
-    float past[kPast];
+    const int c = channels + which * a.H * DK + h * DK + k;
+    Taps taps[2];
+    taps[0].load(a, c);
+    taps[1].load(a, c + 1);
+    float in[TOKENS + kPast][2];
 #pragma unroll
-    for (int j = 0; j < kPast; ++j) {
+    for (int j = 0; j < TOKENS + kPast; ++j) {
       const int t = begin + part * TOKENS - kPast + j;      // of the request
-      float x = 0.0f;
-      if (t >= 0) {
-        if (t < range.n) x = load_scalar<BF16>(a.xbc, (static_cast<int64_t>(range.t0) + t) * a.C + c);
-      } else if (a.K - 1 + t >= 0) {
-        x = a.conv_win[(static_cast<int64_t>(slot) * (a.K - 1) + a.K - 1 + t) * a.C + c];
+      const int64_t at = (static_cast<int64_t>(range.t0) + min(max(t, 0), range.n - 1)) * a.C + c;
+      if constexpr (BF16) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.xbc) + at);
+        in[j][0] = bf16_to_f32(w & 0xffffu);
+        in[j][1] = __uint_as_float(w & 0xffff0000u);
+      } else {
+        const float2 w = *reinterpret_cast<const float2*>(static_cast<const float*>(a.xbc) + at);
+        in[j][0] = w.x;
+        in[j][1] = w.y;
       }
-      past[j] = x;
     }
-    const int64_t at = (static_cast<int64_t>(range.t0) + begin) * a.C + c;
-#pragma unroll 16
+    if (begin == 0 && part * TOKENS < kPast) {              // the window of before
+#pragma unroll
+      for (int j = 0; j < kPast; ++j) {
+        const int r = a.K - 1 - kPast + part * TOKENS + j;  // its row, if below the last
+        if (part * TOKENS + j < kPast) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            in[j][n] = r >= 0 ? a.conv_win[(static_cast<int64_t>(slot) * (a.K - 1) + r) * a.C + c + n] : 0.0f;
+        }
+      }
+    }
+#pragma unroll
     for (int j = 0; j < TOKENS; ++j) {
       const int t = part * TOKENS + j;
-      const float x = load_scalar<BF16>(a.xbc, at + static_cast<int64_t>(min(t, valid - 1)) * a.C);
-      const float y = silu_f(taps.dot(a.K, past[0], past[1], past[2], x));
-      past[0] = past[1];
-      past[1] = past[2];
-      past[2] = x;
-      rows[which][t][k] = t < valid ? y : 0.0f;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const float y = silu_f(taps[n].dot(a.K, in[j][n], in[j + 1][n], in[j + 2][n], in[j + 3][n]));
+        rows[which][t][k + n] = t < valid ? y : 0.0f;
+      }
     }
   }
   __syncthreads();
-  if (u.i == 0) set_windows<BF16>(p, range, u.b, slot, h);
+  if (u.i == 0 && tid < 2 * DK)         // this workgroup alone has read them
+    set_window<BF16>(p, range, u.b, slot, channels + tid / DK * a.H * DK + h * DK + tid % DK, false);
 
-  Keys* const out = p.keys + ((static_cast<int64_t>(range.t0 / Q) + u.b + u.i) * a.H + h) * 2;
+  Keys& out = p.keys[(static_cast<int64_t>(range.t0 / Q) + u.b + u.i) * a.H + h];
   const int col = lane % 16, quad = lane / 16;
-#pragma unroll
-  for (int f = 0; f < kKeyTiles * 2 / 4; ++f) {
-    const int tile = (f * 4 + wave) / 2, step = (f * 4 + wave) % 2;
+  for (int tile = wave; tile < kKeyTiles; tile += 4) {
     float x[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = rows[0][step * 32 + quad * 8 + j][tile * 16 + col];
+    for (int j = 0; j < 8; ++j) x[j] = rows[0][quad * 8 + j][tile * 16 + col];
     u32x4 term[TS];
     split(x, term);
 #pragma unroll
-    for (int n = 0; n < TS; ++n) out[step].b[n][tile][lane] = term[n];
+    for (int n = 0; n < TS; ++n) out.b[n][tile][lane] = term[n];
   }
-  // pairs of the wave's 16 tokens t with the 32 tokens s of its half
-  const int half = wave / 2, mt = wave % 2;
+  // C and the pairs: 16 tokens t and every other step over the keys per wave
+  const int mt = wave % 2;
   f32x4 pairs[2];
 #pragma unroll
   for (int st = 0; st < 2; ++st) pairs[st] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int step = 0; step < kKeySteps; ++step) {
+  for (int step = wave / 2; step < kKeySteps; step += 2) {
     // 32 keys in the accumulators' order: four of each of two tiles
     auto fragment = [&](const float (&row)[STRIDE], u32x4 (&term)[TY]) {
       float x[8];
@@ -240,30 +276,28 @@ __global__ void __launch_bounds__(256) ssm_keys(Plan p, bool, bool) {
       split(x, term);
     };
     u32x4 c[TY];
-    fragment(rows[1][wave * 16 + col], c);
+    fragment(rows[1][mt * 16 + col], c);
 #pragma unroll
-    for (int n = 0; n < TY; ++n) out[half].c[n][mt][step][lane] = c[n];
+    for (int n = 0; n < TY; ++n) out.c[n][mt][step][lane] = c[n];
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
       if (st > mt) break;
       u32x4 b[TY];
-      fragment(rows[0][half * 32 + st * 16 + col], b);
+      fragment(rows[0][st * 16 + col], b);
       pairs[st] = product(c, b, pairs[st]);
     }
   }
-  // rows t, columns s -> operand order, through LDS
-  __syncthreads();
-  constexpr int PSTRIDE = 32 + 4;
-  float* const square = &rows[0][0][0] + wave * 16 * PSTRIDE;
-  static_assert(Q * PSTRIDE <= 2 * Q * STRIDE, "the pairs fit where B and C were");
+  // rows t, columns s -> operand order, and the sum of both waves, through LDS
 #pragma unroll
   for (int st = 0; st < 2; ++st)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) square[(quad * 4 + i) * PSTRIDE + st * 16 + col] = pairs[st][i];
+    for (int i = 0; i < 4; ++i) squares[wave / 2][mt * 16 + quad * 4 + i][st * 16 + col] = pairs[st][i];
   __syncthreads();
-#pragma unroll
-  for (int part = 0; part < 2; ++part)
-    out[half].pairs[mt][part][lane] = *reinterpret_cast<const f32x4*>(square + col * PSTRIDE + quad * 8 + part * 4);
+  {
+    const int part = wave / 2, t = mt * 16 + col, s = quad * 8 + part * 4;
+    out.pairs[mt][part][lane] = *reinterpret_cast<const f32x4*>(&squares[0][t][s]) +
+                                *reinterpret_cast<const f32x4*>(&squares[1][t][s]);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -275,7 +309,6 @@ enum Mode { kWhole, kSegment, kJoined };
 constexpr int NT = 2;                   // 16-column tiles of a wave; a lane's columns are adjacent
 constexpr int kColumns = NT * 16;
 constexpr int kWaves = 4;               // of a workgroup, all of one group
-constexpr int R = 32;                   // tokens at a time
 constexpr int kThreads = kWaves * kWave;
 
 // A workgroup's LDS: the chunk's operands, each read by all waves, and each
@@ -286,10 +319,10 @@ struct Shared {
   u32x4 c[TY][2][kKeySteps][kWave];
   f32x4 pairs[2][2][kWave];
   struct {
-    float hi[R], lo[R];                 // c in two parts, base 2
-    float decay[R];                     // exp(g_t)
-    float from[R];                      // exp(c_t)
-    float step[R];
+    float hi[Q], lo[Q];                 // c in two parts, base 2
+    float decay[Q];                     // exp(g_t)
+    float from[Q];                      // exp(c_t)
+    float step[Q];
   } wave[kWaves];
 };
 
@@ -434,6 +467,18 @@ __device__ __forceinline__ double running_sum(double x) {
   return add_from<0x143, 0xc>(x);
 }
 
+// The lanes 16 quad + col whose token t = 16 mt + col is at or behind token
+// 8 quad + j: constants, one per use.
+__device__ __forceinline__ constexpr uint64_t lanes_from(int mt, int j) {
+  uint64_t lanes = 0;
+  for (int quad = 0; quad < 4; ++quad) {
+    const int from = quad * 8 + j - mt * 16;
+    const uint64_t row = from <= 0 ? 0xffffu : (from >= 16 ? 0u : 0xffffu << from & 0xffffu);
+    lanes |= row << (16 * quad);
+  }
+  return lanes;
+}
+
 template <bool BF16, int TY, int TS, int MODE>
 __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(MODE == kSegment ? 3 : 2, MODE == kSegment ? 3 : 2))) ssm_scan(Plan p, bool state_bf16, bool v_first) {
   const SsmArgs& a = p.a;
@@ -514,10 +559,10 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(M
   Staged<kB> stage_b;
   Inputs<BF16> in;
   float dt;
-  const Keys* const first_keys = p.keys + ((static_cast<int64_t>(range.t0 / Q) + u.b) * a.H + h) * 2;
-  auto keys_at = [&](int t0) { return first_keys + static_cast<int64_t>(t0 / Q) * a.H * 2 + t0 / R % 2; };
+  const Keys* const first_keys = p.keys + (static_cast<int64_t>(range.t0 / Q) + u.b) * a.H + h;
+  auto keys_at = [&](int t0) { return first_keys + static_cast<int64_t>(t0 / Q) * a.H; };
   auto load = [&](int t0, int quad, int column) {
-    const int valid = min(R, end - t0);
+    const int valid = min(Q, end - t0);
     const int64_t t = static_cast<int64_t>(range.t0) + t0 + min(lane, valid - 1);
     dt = a.dt[t * a.HV + hv];
     in.load(a, range, t0, valid, quad, column);
@@ -536,15 +581,15 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(M
   load(begin, quad, column);
   store();
 
-  for (int t0 = begin; t0 < end; t0 += R) {
-    const int valid = min(R, end - t0);
+  for (int t0 = begin; t0 < end; t0 += Q) {
+    const int valid = min(Q, end - t0);
     // The lane's place, anew for every 32 tokens: addresses and comparisons
     // made of it would otherwise be kept in registers through all of them.
     int col = lane % 16, quad = lane / 16;
     asm volatile("" : "+v"(col), "+v"(quad));
     const int column = hv * dv + slab * kColumns + col * NT;
     lds_barrier();            // c and pairs are there, and b has been read
-    const bool update = MODE != kJoined || t0 + R < end;     // a joined segment's last state is not used
+    const bool update = MODE != kJoined || t0 + Q < end;     // a joined segment's last state is not used
     stage_b.load(&keys_at(t0)->b[0][0][0]);
 
     // steps and the running sum of the decays, one token per lane
@@ -555,41 +600,48 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(M
       const double c = running_sum(g);
       const float part = static_cast<float>(c);
       const float from = __builtin_amdgcn_exp2f(part);
-      if (lane < R) {
+      if (lane < Q) {
         own.hi[lane] = part;
         own.lo[lane] = static_cast<float>(c - static_cast<double>(part));
         own.decay[lane] = __builtin_amdgcn_exp2f(static_cast<float>(g));
         own.from[lane] = from;
         own.step[lane] = step;
       }
-      total = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(from), R - 1));
+      total = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(from), Q - 1));
       gone *= total;
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
       __builtin_amdgcn_wave_barrier();
     }
 
     // the lane's columns, convolved
-    float x[8][NT];
+    float x[8][NT], past[kPast][NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float past[kPast];
+    for (int j = 0; j < kPast; ++j)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) past[j][n] = in.get(j, n);
+    if (t0 == 0) {                      // the window of before
 #pragma unroll
       for (int j = 0; j < kPast; ++j) {
-        past[j] = in.get(j, n);
         const int r = a.K - 1 - kPast + j;
-        if (t0 == 0 && quad == 0 && r >= 0)     // the window of before
-          past[j] = p.windows[(static_cast<int64_t>(u.b) * (a.K - 1) + r) * a.C + column + n];
-      }
+        if (r >= 0 && quad == 0) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float next = in.get(j + kPast, n);
-        x[j][n] = silu_f(taps[n].dot(a.K, past[0], past[1], past[2], next));
-        past[0] = past[1];
-        past[1] = past[2];
-        past[2] = next;
+          for (int n = 0; n < NT; ++n)
+            past[j][n] = p.windows[(static_cast<int64_t>(u.b) * (a.K - 1) + r) * a.C + column + n];
+        }
       }
     }
-    if (valid < R) {
+    auto convolve = [&](int K) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          auto at = [&](int i) { return i < kPast ? past[i][n] : in.get(i, n); };
+          x[j][n] = silu_f(taps[n].dot(K, at(j), at(j + 1), at(j + 2), at(j + 3)));
+        }
+    };
+    if (a.K == kTaps) convolve(kTaps);  // all taps: no choice per value
+    else convolve(a.K);
+    if (valid < Q) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -628,14 +680,12 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(M
             for (int j = 0; j < 8; ++j) f[j] = S[2 * step + j / 4][n][j % 4];
             split(f, s[n]);
           }
+          u32x4 ck[2][TY];
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
-            u32x4 ck[TY];
+          for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-            for (int m = 0; m < TY; ++m) ck[m] = sh.c[m][mt][step][lane];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) y[mt][n] = product(ck, s[n], y[mt][n]);
-          }
+            for (int m = 0; m < TY; ++m) ck[mt][m] = sh.c[m][mt][step][lane];
+          products(ck, s, y);
         }
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
@@ -652,6 +702,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(M
           for (int j = 0; j < 8; ++j) f[j] = x[j][n];
           split(f, xs[n]);
         }
+        u32x4 ms[2][TY];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
           const int t = mt * 16 + col;
@@ -661,15 +712,15 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(M
           float m[8];
 #pragma unroll
           for (int j = 7; j >= 0; --j) {
-            if (j < 7) f *= first + j + 1 <= t ? decay[j + 1] : 1.0f;
+            const uint64_t reached = lanes_from(mt, j), passed = lanes_from(mt, j + 1);     // s <= t, s < t
+            if (j < 7) f *= __builtin_amdgcn_inverse_ballot_w64(passed) ? decay[j + 1] : 1.0f;
             const float pair = (j < 4 ? p0[j % 4] : p1[j % 4]) * d[j];
-            m[j] = first + j < t ? pair * f : (first + j == t ? pair + skip : 0.0f);
+            m[j] = fmaf(pair, __builtin_amdgcn_inverse_ballot_w64(reached) ? f : 0.0f,
+                        __builtin_amdgcn_inverse_ballot_w64(reached & ~passed) ? skip : 0.0f);
           }
-          u32x4 ms[TY];
-          split(m, ms);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) y[mt][n] = product(ms, xs[n], y[mt][n]);
+          split(m, ms[mt]);
         }
+        products(ms, xs, y);
         const __amdgpu_buffer_rsrc_t out = tile_resource(
             static_cast<char*>(a.out) + (static_cast<int64_t>(range.t0) + t0) * out_row * E, valid * out_row * E);
 #pragma unroll
@@ -689,11 +740,11 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(M
     stage_b.store(&sh.b[0][0][0]);
     lds_barrier();            // b is there, and c and pairs have been read
 
-    const int next = t0 + R;
+    const int next = t0 + Q;
     if (next < end) load(next, quad, column);
     if (update && works) {
       // step_s exp(c_last - c_s), from the last s backwards
-      float f = __builtin_amdgcn_exp2f((own.hi[R - 1] - last_hi) + (own.lo[R - 1] - last_lo));
+      float f = __builtin_amdgcn_exp2f((own.hi[Q - 1] - last_hi) + (own.lo[Q - 1] - last_lo));
       float g[8];
 #pragma unroll
       for (int j = 7; j >= 0; --j) {
@@ -709,12 +760,21 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(M
         split(e, xs[n]);
       }
 #pragma unroll
-      for (int kt = 0; kt < kKeyTiles; ++kt) {
-        u32x4 bk[TS];
+      for (int kt = 0; kt < kKeyTiles; kt += 2) {
+        u32x4 bk[2][TS];
+        f32x4 s[2][NT];
 #pragma unroll
-        for (int m = 0; m < TS; ++m) bk[m] = sh.b[m][kt][lane];
+        for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) S[kt][n] = product(bk, xs[n], S[kt][n] * total);
+          for (int m = 0; m < TS; ++m) bk[i][m] = sh.b[m][kt + i][lane];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) s[i][n] = S[kt + i][n] * total;
+        }
+        products(bk, xs, s);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) S[kt + i][n] = s[i][n];
       }
     }
     if (next < end) store();
@@ -793,9 +853,9 @@ hipError_t scan(const Plan& plan, int dv, bool state_bf16, bool v_first, hipStre
 template <bool BF16, int TY, int TS>
 hipError_t run(const Plan& plan, int dv, bool state_bf16, bool v_first, hipStream_t stream) {
   void* kargs[] = {const_cast<Plan*>(&plan), &state_bf16, &v_first};
-  const int64_t chunks = static_cast<int64_t>(plan.a.T) / Q + plan.a.B;
+  const uint32_t window_blocks = static_cast<uint32_t>(plan.a.B) * ((plan.a.HV * dv + 255) / 256);
   hipError_t rc = hipLaunchKernel(reinterpret_cast<const void*>(&ssm_keys<BF16, TY, TS>),
-                                  dim3(static_cast<uint32_t>(chunks * plan.a.H)), dim3(256), kargs, 0, stream);
+                                  dim3(plan.key_blocks + window_blocks), dim3(256), kargs, 0, stream);
   if (rc != hipSuccess) return rc;
   if (plan.segment == 0) return scan<BF16, TY, TS, kWhole>(plan, dv, state_bf16, v_first, stream);
   rc = scan<BF16, TY, TS, kSegment>(plan, dv, state_bf16, v_first, stream);
@@ -817,12 +877,13 @@ int launch_ssm_prefill_dk<DK>(const SsmArgs& args, int dv, bool bf16, bool state
   plan.a = args;
   const int64_t chunks = static_cast<int64_t>(args.T) / Q + args.B;
   plan.keys = reinterpret_cast<Keys*>(args.workspace);
-  plan.windows = reinterpret_cast<float*>(plan.keys + chunks * args.H * 2);
+  plan.windows = reinterpret_cast<float*>(plan.keys + chunks * args.H);
   plan.states = plan.windows + static_cast<int64_t>(args.B) * (args.K - 1) * args.C;
   const int64_t waves = static_cast<int64_t>(args.HV) * (dv > 64 ? 2 : 1);
   plan.units = args.B;
+  plan.key_blocks = static_cast<uint32_t>(chunks * args.H);
   const int64_t most = KDA_SSM_SPLIT / waves;       // segments that the workspace has room for, beyond one a request
-  if (args.B * waves < 1024 && most >= 2) {
+  if (args.B * waves < 512 && most >= 2) {
     int64_t length = (args.T + most - 1) / most;
     length = (length + Q - 1) / Q * Q;
     if (length < kMinSegment) length = kMinSegment;

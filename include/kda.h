@@ -407,8 +407,8 @@ int kda_verify(const kda_tensor* n_commit, const kda_tensor* next_token, const k
  *   state_layout  enum kda_state_layout.
  * H is (C - HV*dv) / (2*dk) and must divide HV.  dk and dv must each be 32,
  * 64 or 128 (KDA_ERR_UNSUPPORTED); T, N and B stay below 2^31 - 64, B * HV
- * below 2^21, C below 2^22, B * C below 2^31, and for prompts (T / 64 + B) * H
- * below 2^24 (KDA_ERR_UNSUPPORTED).  Data
+ * below 2^21, C below 2^22, B * C below 2^31, and for prompts (T / 32 + B) * H
+ * below 2^23 and B * C at most 2^29 (KDA_ERR_UNSUPPORTED).  Data
  * are 16-byte aligned.  Preconditions, conventions (a negative index skips a
  * request: zero rows in out, state and window kept; an empty request changes
  * nothing) and errors are those of kda_decode.
@@ -425,24 +425,24 @@ int kda_ssm_decode(const kda_tensor* out, const kda_tensor* xbc, const kda_tenso
                    const kda_tensor* state_indices, int32_t state_layout, hipStream_t stream);
 
 /* Floats of kda_ssm_prefill's workspace, for the sizes of its arguments: the
- * convolved keys and their products per 64 tokens and group, the windows as
+ * convolved keys and their products per 32 tokens and group, the windows as
  * they were, and the states where a long request is split. */
-#define KDA_SSM_CHUNK 64
-#define KDA_SSM_SPLIT 2048
+#define KDA_SSM_CHUNK 32
+#define KDA_SSM_SPLIT 1024
 #define KDA_SSM_WORKSPACE(T, B, H, HV, dk, dv, K)                                                   \
-  (((int64_t)(T) / KDA_SSM_CHUNK + (B)) * (H) * (192 * (int64_t)(dk) + 2048) +                      \
+  (((int64_t)(T) / KDA_SSM_CHUNK + (B)) * (H) * (96 * (int64_t)(dk) + 1024) +                       \
    (int64_t)(B) * ((K)-1) * ((int64_t)(HV) * (dv) + 2 * (int64_t)(H) * (dk)) +                      \
    ((int64_t)KDA_SSM_SPLIT * 64 + (int64_t)(B) * (HV) * (dv)) * (dk) + 2 * (int64_t)KDA_SSM_SPLIT + \
    (int64_t)(B) * (HV) + 64)
 
 /*
- * kda_ssm_prefill - the same operation for whole prompts, in chunks of 64
+ * kda_ssm_prefill - the same operation for whole prompts, in chunks of 32
  * tokens on the matrix cores; the result equals the token-by-token scan up to
  * rounding order.  Operands are split into bf16 terms without loss of range:
  * three terms for an fp32 pool's state and for f32 outputs (a product is good
  * to 2^-20), two for bf16 pools and outputs of a bf16 call (2^-13).  Errors are relative to
  * the sum of the magnitudes of what is added up.  Where the scan has an
- * infinity or NaN, this call may have NaN, and from up to 63 tokens earlier
+ * infinity or NaN, this call may have NaN, and from up to 31 tokens earlier
  * of the same request.
  *   workspace     [>= KDA_SSM_WORKSPACE(...)]  f32; its contents before and
  *                 after mean nothing.  Calls that may run at the same time
