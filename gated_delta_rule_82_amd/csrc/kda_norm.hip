@@ -90,38 +90,46 @@ __device__ __forceinline__ void store_piece(void* base, int64_t off, int count, 
   }
 }
 
-// The row's threads: LANES of a wave, or WAVES waves that meet in LDS.
+// The row's threads: LANES of a wave, or with kBlock a whole workgroup, whose
+// waves meet in LDS.
+constexpr int kBlock = 0;
+constexpr int kMostWaves = 16;
+
 template <int LANES>
 struct Row {
-  static constexpr int WAVES = LANES > kWave ? LANES / kWave : 1;
-  static constexpr int BLOCK = 256;
-  static constexpr int ROWS = BLOCK / LANES;
+  static constexpr bool WHOLE = LANES == kBlock;
+  static constexpr int IN_WAVE = WHOLE ? kWave : LANES;
+  static constexpr int MOST = WHOLE ? kMostWaves * kWave : 256;     // threads of a workgroup
 
-  static __device__ __forceinline__ float sum(float x) {
-    x = sum_levels<log2_exact<LANES < kWave ? LANES : kWave>() - 1, 0>(x);
-    if constexpr (WAVES > 1) {
-      __shared__ float part[WAVES];
-      __syncthreads();      // the last sum has been read
-      if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = x;
-      __syncthreads();
-      x = part[0];
-#pragma unroll
-      for (int w = 1; w < WAVES; ++w) x += part[w];
-    }
-    return x;
+  static __device__ __forceinline__ int lane() { return WHOLE ? threadIdx.x : threadIdx.x % IN_WAVE; }
+  static __device__ __forceinline__ int lanes() { return WHOLE ? blockDim.x : IN_WAVE; }
+  static __device__ __forceinline__ int64_t row() {
+    return WHOLE ? static_cast<int64_t>(blockIdx.x)
+                 : static_cast<int64_t>(blockIdx.x) * (MOST / IN_WAVE) + threadIdx.x / IN_WAVE;
   }
 
+  // The waves' sums, one per lane of 16, to be summed once more.
+  template <typename T>
+  static __device__ __forceinline__ T meet(T x) {
+    __shared__ T part[kMostWaves];
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kMostWaves;
+    __syncthreads();            // the last sums have been read
+    if (threadIdx.x % kWave == 0) part[wave] = x;
+    __syncthreads();
+    return lane < static_cast<int>(blockDim.x / kWave) ? part[lane] : T(0);
+  }
+  static __device__ __forceinline__ float sum(float x) {
+    x = sum_levels<log2_exact<IN_WAVE>() - 1, 0>(x);
+    if (WHOLE && blockDim.x > kWave) x = sum_levels<log2_exact<kMostWaves>() - 1, 0>(meet(x));
+    return x;
+  }
   static __device__ double sum(double x) {
 #pragma unroll
-    for (int m = 1; m < (LANES < kWave ? LANES : kWave); m *= 2) x += __shfl_xor(x, m);
-    if constexpr (WAVES > 1) {
-      __shared__ double part[WAVES];
-      __syncthreads();
-      if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = x;
-      __syncthreads();
-      x = part[0];
+    for (int m = 1; m < IN_WAVE; m *= 2) x += __shfl_xor(x, m);
+    if (WHOLE && blockDim.x > kWave) {
+      x = meet(x);
 #pragma unroll
-      for (int w = 1; w < WAVES; ++w) x += part[w];
+      for (int m = 1; m < kMostWaves; m *= 2) x += __shfl_xor(x, m);
     }
     return x;
   }
@@ -156,15 +164,15 @@ __device__ __forceinline__ Factor norm_factor(const float (&x)[P][kVec], int D, 
 }
 
 template <int LANES, int P, bool HBF16, bool BF16>
-__global__ void __launch_bounds__(256) norm_residual(ResidualArgs a) {
-  const int lane = threadIdx.x % LANES;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * Row<LANES>::ROWS + threadIdx.x / LANES;
+__global__ void __launch_bounds__(Row<LANES>::MOST) norm_residual(ResidualArgs a) {
+  const int lane = Row<LANES>::lane(), lanes = Row<LANES>::lanes();
+  const int64_t row = Row<LANES>::row();
   if (row >= a.rows) return;      // whole rows: no lane of one is missing
   const int64_t at = row * a.D;
   float y[P][kVec], h[P][kVec];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const int i = (p * LANES + lane) * kVec;
+    const int i = (p * lanes + lane) * kVec;
     load_piece<BF16>(a.block_out, at + i, a.D - i, y[p]);
     load_piece<HBF16>(a.hidden, at + i, a.D - i, h[p]);
   }
@@ -172,7 +180,7 @@ __global__ void __launch_bounds__(256) norm_residual(ResidualArgs a) {
     const Factor r = norm_factor<LANES, P>(y, a.D, a.eps);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const int i = (p * LANES + lane) * kVec;
+      const int i = (p * lanes + lane) * kVec;
       float w[kVec];
       load_piece<false>(a.post_weight, i, a.D - i, w);
 #pragma unroll
@@ -182,7 +190,7 @@ __global__ void __launch_bounds__(256) norm_residual(ResidualArgs a) {
   const float one = a.scale != nullptr ? a.scale[0] : 1.0f;
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const int i = (p * LANES + lane) * kVec;
+    const int i = (p * lanes + lane) * kVec;
     if (a.scale_per_channel) {
       float s[kVec];
       load_piece<false>(a.scale, i, a.D - i, s);
@@ -197,7 +205,7 @@ __global__ void __launch_bounds__(256) norm_residual(ResidualArgs a) {
   const Factor r = norm_factor<LANES, P>(h, a.D, a.eps);
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const int i = (p * LANES + lane) * kVec;
+    const int i = (p * lanes + lane) * kVec;
     float w[kVec];
     load_piece<false>(a.weight, i, a.D - i, w);
 #pragma unroll
@@ -207,15 +215,15 @@ __global__ void __launch_bounds__(256) norm_residual(ResidualArgs a) {
 }
 
 template <int LANES, int P, bool FIRST, bool BF16>
-__global__ void __launch_bounds__(256) norm_gate(GateArgs a) {
-  const int lane = threadIdx.x % LANES;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * Row<LANES>::ROWS + threadIdx.x / LANES;
+__global__ void __launch_bounds__(Row<LANES>::MOST) norm_gate(GateArgs a) {
+  const int lane = Row<LANES>::lane(), lanes = Row<LANES>::lanes();
+  const int64_t row = Row<LANES>::row();
   if (row >= a.rows) return;
   const int64_t at = row * a.D;
   float x[P][kVec], z[P][kVec];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const int i = (p * LANES + lane) * kVec;
+    const int i = (p * lanes + lane) * kVec;
     load_piece<BF16>(a.x, at + i, a.D - i, x[p]);
     load_piece<BF16>(a.gate, at + i, a.D - i, z[p]);
   }
@@ -230,7 +238,7 @@ __global__ void __launch_bounds__(256) norm_gate(GateArgs a) {
   const int64_t group = a.groups > 1 ? row % a.groups * a.D : 0;
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const int i = (p * LANES + lane) * kVec;
+    const int i = (p * lanes + lane) * kVec;
     float w[kVec];
     load_piece<false>(a.weight, group + i, a.D - i, w);
 #pragma unroll
@@ -254,27 +262,31 @@ const void* kernel(const GateArgs&) {
 
 template <int LANES, int P, bool X, bool BF16, typename Args>
 int launch(const Args& args, hipStream_t stream) {
-  const int64_t blocks = (args.rows + Row<LANES>::ROWS - 1) / Row<LANES>::ROWS;
-  if (blocks >= 1 << 24) return KDA_ERR_UNSUPPORTED;      // 2^32 work-items
+  constexpr bool whole = LANES == kBlock;
+  constexpr int rows = whole ? 1 : 256 / (whole ? 1 : LANES);
+  const int threads = whole ? (args.D + kVec * P * kWave - 1) / (kVec * P * kWave) * kWave : 256;
+  const int64_t blocks = (args.rows + rows - 1) / rows;
+  if (blocks * threads * P > UINT32_MAX) return KDA_ERR_UNSUPPORTED;      // a dispatch's work-items
   void* kargs[] = {const_cast<Args*>(&args)};
   const hipError_t rc = hipLaunchKernel(kernel<LANES, P, X, BF16>(args), dim3(static_cast<uint32_t>(blocks)),
-                                        dim3(Row<LANES>::BLOCK), kargs, 0, stream);
+                                        dim3(static_cast<uint32_t>(threads)), kargs, 0, stream);
   return rc == hipSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }
 
-// The least threads that hold a row at up to four pieces each in one wave;
-// longer rows take a workgroup.
+// One piece per thread, from eight threads to a workgroup of sixteen waves,
+// and two where that does not hold the row.  More pieces per thread are
+// slower, as fewer rows are under way: norm_residual, bf16, 16384 rows of 8192
+// with 256 threads x 4, 512 x 2, 1024 x 1: 205 / 186 / 179 us; of 4096 with
+// 64 x 8, 128 x 4, 256 x 2, 512 x 1: 159 / 109 / 96 / 90 us.
 template <bool X, bool BF16, typename Args>
 int launch(const Args& args, hipStream_t stream) {
   const int D = args.D;
   if (D <= 8 * kVec) return launch<8, 1, X, BF16>(args, stream);
   if (D <= 16 * kVec) return launch<16, 1, X, BF16>(args, stream);
   if (D <= 64 * kVec) return launch<64, 1, X, BF16>(args, stream);
-  if (D <= 64 * kVec * 4) return launch<64, 4, X, BF16>(args, stream);
-  if (D <= 256 * kVec * 2) return launch<256, 2, X, BF16>(args, stream);
-  if (D <= 256 * kVec * 4) return launch<256, 4, X, BF16>(args, stream);
-  static_assert(KDA_NORM_MAX == 256 * kVec * 8, "the longest row");
-  return launch<256, 8, X, BF16>(args, stream);
+  if (D <= kMostWaves * kWave * kVec) return launch<kBlock, 1, X, BF16>(args, stream);
+  static_assert(KDA_NORM_MAX == kMostWaves * kWave * kVec * 2, "the longest row");
+  return launch<kBlock, 2, X, BF16>(args, stream);
 }
 
 template <bool X, typename Args>

@@ -1,16 +1,18 @@
 // kda_ssm_decode.hip - the selective state space scan token by token
 // (kda_ssm_decode), with its short causal convolution in front.
 //
-// ssm_decode: one workgroup per (request, value head, up to 64 value
-// columns).  Its waves hold 16 columns of the state each, dk / 16 pieces of
-// four values per lane, in the pool's own order: key-first a lane has four
-// columns of every 16th row, value-first four keys of some rows.  The state is
-// fetched once, advanced through the request's tokens in fp32 and written
-// once.  Per token every thread convolves one or two of the head's channels
-// (x) or its group's (B and C), which meet in LDS, double-buffered so that one
-// barrier per token is enough; C^T S is summed over the wave's lanes.
-// ssm_windows: behind it, the new windows.  Every head of a group reads its
-// window of B and C, so no workgroup of the first kernel may write it.
+// ssm_decode: one workgroup per (request, value head, up to 64 value columns),
+// one wave per 16 of the columns.  A lane moves its state in 16-byte pieces of
+// the pool's own rows: value-first a wave holds 16 rows of dk keys, key-first
+// the rows of its share of the keys, whole.  The state is fetched once,
+// advanced through the request's tokens in fp32 and written once.  Per token
+// every thread convolves one to three of the head's channels (x) or its
+// group's (B and C), which meet in LDS, double-buffered so that one barrier
+// per token is enough.  C^T S is summed over the wave's lanes; key-first the
+// waves' parts are added behind the next token's barrier.  It sets the window
+// of its own channels of x.
+// ssm_windows: behind it, the new windows of B and C.  Every head of a group
+// reads them, so no workgroup of the first kernel may write them.
 //
 // Bound: HBM, the state's way in and out.
 
@@ -29,29 +31,36 @@ namespace {
 
 template <int DK, int DV, bool BF16, bool SBF16, bool VFIRST>
 struct Shape {
-  static constexpr int COLS = DV < 64 ? DV : 64;        // value columns of a workgroup
+  static constexpr int COLS = DV;                       // value columns of a workgroup
   static constexpr int SLABS = DV / COLS;
-  static constexpr int THREADS = COLS * 4;              // 16 columns per wave
+  static constexpr int WAVES = COLS < 64 ? 2 : 4;
+  static constexpr int OWN = COLS / WAVES;              // value-first: a wave's rows
+  static constexpr int THREADS = WAVES * kWave;
   static constexpr int CHANNELS = COLS + 2 * DK;        // convolved by a workgroup: x, B, C
   static constexpr int PER = (CHANNELS + THREADS - 1) / THREADS;
-  static constexpr int R = DK / 16;                     // pieces of four values per lane
-  static constexpr int LANES = DK / 4;                  // value-first: lanes of a row
   static constexpr int ELEM = SBF16 ? 2 : 4;
+  static constexpr int VEC = 16 / ELEM;                 // values per piece
+  static constexpr int LANES = (VFIRST ? DK : COLS) / VEC;  // of a row
+  static constexpr int STEP = kWave / LANES;            // rows of a wave's piece
+  static constexpr int R = (VFIRST ? OWN : DK / WAVES) / STEP;   // pieces per lane
+  static_assert(R >= 1, "rows of a wave");
 };
 
 template <int DK, int DV, bool BF16, bool SBF16, bool VFIRST>
 __global__ void __launch_bounds__((Shape<DK, DV, BF16, SBF16, VFIRST>::THREADS)) ssm_decode(SsmArgs a) {
   using S = Shape<DK, DV, BF16, SBF16, VFIRST>;
-  using IO = StateIO<SBF16, 4>;
-  constexpr int R = S::R, PER = S::PER;
+  using IO = StateIO<SBF16, S::VEC>;
+  constexpr int R = S::R, PER = S::PER, VEC = S::VEC;
   __shared__ __attribute__((aligned(16))) float conv[2][S::CHANNELS];
+  __shared__ float parts[2][VFIRST ? 1 : S::WAVES][VFIRST ? 1 : S::COLS];
 
   const int slab = blockIdx.x % S::SLABS;
   const int head = blockIdx.x / S::SLABS;
   const int hv = head % a.HV, b = head / a.HV;
   const Range range = request_range(a, b);
   if (range.n == 0) return;
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int slot = request_slot(a, b);
   const int64_t out_row = static_cast<int64_t>(a.HV) * DV;
   int64_t out_at = static_cast<int64_t>(range.t0) * out_row + static_cast<int64_t>(hv) * DV + slab * S::COLS;
@@ -61,20 +70,18 @@ __global__ void __launch_bounds__((Shape<DK, DV, BF16, SBF16, VFIRST>::THREADS))
     return;
   }
 
-  // the lane's pieces: rows (key-first: keys; value-first: values) row0 +
-  // i * STEP, values col .. col + 3 of them
-  const int first = wave * 16 + slab * S::COLS;         // first of the wave's value columns
-  constexpr int STEP = VFIRST ? kWave / S::LANES : 16;
-  const int row0 = VFIRST ? first + lane / S::LANES : lane >> 2;
-  const int col = VFIRST ? (lane % S::LANES) * 4 : first + (lane & 3) * 4;
+  // the lane's pieces: rows row0 + i * STEP (key-first: keys; value-first:
+  // columns of the workgroup), values col .. col + VEC - 1 of them
+  const int row0 = (VFIRST ? wave * S::OWN : wave * (DK / S::WAVES)) + lane / S::LANES;
+  const int col = lane % S::LANES * VEC;
   constexpr int WIDTH = VFIRST ? DK : DV;
   const int64_t tile = (static_cast<int64_t>(slot) * a.HV + hv) * DK * DV;
   const __amdgpu_buffer_rsrc_t pool =
       tile_resource(static_cast<char*>(a.state_pool) + tile * S::ELEM, DK * DV * S::ELEM);
-  const int voff = (row0 * WIDTH + col) * S::ELEM;
-  float s[R][4];
+  const int voff = (row0 * WIDTH + col + slab * S::COLS * (VFIRST ? DK : 1)) * S::ELEM;
+  float s[R][VEC];
 #pragma unroll
-  for (int i = 0; i < R; ++i) IO::load(pool, voff, i * STEP * WIDTH * S::ELEM, s[i]);
+  for (int i = 0; i < R; ++i) IO::load(pool, voff, i * S::STEP * WIDTH * S::ELEM, s[i]);
 
   // the thread's channels: taps, and the inputs before the next token
   const int h = hv / a.G;
@@ -100,27 +107,43 @@ __global__ void __launch_bounds__((Shape<DK, DV, BF16, SBF16, VFIRST>::THREADS))
   const bool skips = a.d_skip != nullptr;
   const float skip = skips ? a.d_skip[hv] : 0.0f;
 
+  // key-first: adds the waves' parts of the token before, whose x is `last`
+  auto finish = [&](int t, float last) {
+    if (tid < S::COLS) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < S::WAVES; ++w) sum += parts[t & 1][VFIRST ? 0 : w][VFIRST ? 0 : tid];
+      store_scalar<BF16>(a.out, out_at - out_row + tid, skips ? fmaf(skip, last, sum) : sum);
+    }
+  };
+
   int64_t in_at = static_cast<int64_t>(range.t0) * a.C;
-  const float* dt = a.dt + static_cast<int64_t>(range.t0) * a.HV + hv;
-  float next[PER];
+  float next[PER], last = 0.0f;
 #pragma unroll
   for (int p = 0; p < PER; ++p) next[p] = load_scalar<BF16>(a.xbc, in_at + channel[p]);
+  float steps = 0.0f, decays = 0.0f;    // of 64 tokens, one per lane
   for (int t = 0; t < range.n; ++t) {
+    if (t % kWave == 0) {
+      const int64_t at = static_cast<int64_t>(range.t0) + min(t + lane, range.n - 1);
+      steps = softplus_f(a.dt[at * a.HV + hv] + bias);
+      decays = exp_f(-amp * steps);
+    }
+    const float step = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(steps), t % kWave));
+    const float decay = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(decays), t % kWave));
     float* const buf = conv[t & 1];
+    float mine = 0.0f;
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
-      const float y = taps[p].dot(a.K, past[p][0], past[p][1], past[p][2], next[p]);
+      const float y = silu_f(taps[p].dot(a.K, past[p][0], past[p][1], past[p][2], next[p]));
       past[p][0] = past[p][1];
       past[p][1] = past[p][2];
       past[p][2] = next[p];
       const int i = tid + p * S::THREADS;
-      if (i < S::CHANNELS) buf[i] = silu_f(y);
+      if (i < S::CHANNELS) buf[i] = y;
+      if (p == 0) mine = y;
     }
-    const float step = softplus_f(*dt + bias);
-    const float decay = exp_f(-amp * step);
     if (t + 1 < range.n) {
       in_at += a.C;
-      dt += a.HV;
 #pragma unroll
       for (int p = 0; p < PER; ++p) next[p] = load_scalar<BF16>(a.xbc, in_at + channel[p]);
     }
@@ -129,55 +152,82 @@ __global__ void __launch_bounds__((Shape<DK, DV, BF16, SBF16, VFIRST>::THREADS))
     const float* const kb = buf + S::COLS;
     const float* const kc = kb + DK;
     if constexpr (VFIRST) {
-      const f32x4 bk = *reinterpret_cast<const f32x4*>(kb + col);
-      const f32x4 ck = *reinterpret_cast<const f32x4*>(kc + col);
-      float y[R];
+      float bk[VEC], ck[VEC], y[R];
+#pragma unroll
+      for (int e = 0; e < VEC; e += 4) {
+        *reinterpret_cast<f32x4*>(bk + e) = *reinterpret_cast<const f32x4*>(kb + col + e);
+        *reinterpret_cast<f32x4*>(ck + e) = *reinterpret_cast<const f32x4*>(kc + col + e);
+      }
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const float w = step * x[row0 - slab * S::COLS + i * STEP];
+        const float w = step * x[row0 + i * S::STEP];
         y[i] = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < VEC; ++e) {
           s[i][e] = fmaf(bk[e], w, decay * s[i][e]);
           y[i] = fmaf(ck[e], s[i][e], y[i]);
         }
       }
-      // lanes of a row: the upper bits pick the piece, the two lowest are summed
-      constexpr int TOP = log2_exact<S::LANES>() - 1;
-      transpose_levels<R / 2, TOP>(y, lane);
-      const float sum = sum_levels<1, 0>(y[0]);
-      const int v = row0 - slab * S::COLS + ((lane % S::LANES) >> 2) * STEP;
-      if ((lane & 3) == 0) store_scalar<BF16>(a.out, out_at + v, skips ? fmaf(skip, x[v], sum) : sum);
+      // lanes of a row: the upper bits pick the piece, the lowest are summed
+      constexpr int LOW = log2_exact<S::LANES>() - log2_exact<R>();
+      static_assert(LOW >= 0, "lanes of a row");
+      if constexpr (R > 1) transpose_levels<R / 2, log2_exact<S::LANES>() - 1>(y, lane);
+      const float sum = sum_levels<LOW - 1, 0>(y[0]);
+      const int v = row0 + ((lane % S::LANES) >> LOW) * S::STEP;
+      if ((lane & ((1 << LOW) - 1)) == 0) store_scalar<BF16>(a.out, out_at + v, skips ? fmaf(skip, x[v], sum) : sum);
     } else {
-      const f32x4 xv = *reinterpret_cast<const f32x4*>(x + col - slab * S::COLS);
-      float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (t > 0) finish(t - 1, last);
+      last = mine;
+      float xv[VEC], y[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; e += 4) *reinterpret_cast<f32x4*>(xv + e) = *reinterpret_cast<const f32x4*>(x + col + e);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) y[e] = 0.0f;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const float w = step * kb[row0 + i * STEP], ck = kc[row0 + i * STEP];
+        const float w = step * kb[row0 + i * S::STEP], ck = kc[row0 + i * S::STEP];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < VEC; ++e) {
           s[i][e] = fmaf(w, xv[e], decay * s[i][e]);
           y[e] = fmaf(ck, s[i][e], y[e]);
         }
       }
-      // lanes of a column group differ in bits 2..5: bits 5 and 4 pick the column
-      transpose_levels<2, 5>(y, lane);
-      const float sum = sum_levels<3, 2>(y[0]);
-      const int v = wave * 16 + (lane & 3) * 4 + (lane >> 4 & 1) + (lane >> 5) * 2;
-      if ((lane & 12) == 0) store_scalar<BF16>(a.out, out_at + v, skips ? fmaf(skip, x[v], sum) : sum);
+      // lanes of a column group: their upper bits pick columns, what is left
+      // of them is summed; LEFT columns stay in a lane
+      constexpr int BITS = log2_exact<S::STEP>(), LOW = log2_exact<S::LANES>();
+      constexpr int LEVELS = BITS < log2_exact<VEC>() ? BITS : log2_exact<VEC>(), LEFT = VEC >> LEVELS;
+      static_assert(BITS + LOW == 6 && LEVELS > 0 && (LEFT == 1 || LEVELS == BITS), "lanes of a wave");
+      transpose_levels<VEC / 2, 5, LEVELS>(y, lane);
+      if constexpr (LEFT == 1) y[0] = sum_levels<5 - LEVELS, LOW>(y[0]);
+      if (((lane >> LOW) & ((1 << (BITS - LEVELS)) - 1)) == 0) {
+#pragma unroll
+        for (int e = 0; e < LEFT; ++e) parts[t & 1][wave][col + (lane >> (6 - LEVELS)) * LEFT + e] = y[e];
+      }
     }
     out_at += out_row;
   }
 #pragma unroll
-  for (int i = 0; i < R; ++i) IO::store(pool, voff, i * STEP * WIDTH * S::ELEM, s[i]);
+  for (int i = 0; i < R; ++i) IO::store(pool, voff, i * S::STEP * WIDTH * S::ELEM, s[i]);
+  if constexpr (!VFIRST) {
+    __syncthreads();
+    finish(range.n - 1, last);
+  }
+  if (tid < S::COLS) {        // a thread's first channel is of x where it has one
+#pragma unroll
+    for (int j = 0; j < kPast; ++j) {
+      const int r = j - (kTaps - a.K);
+      if (r >= 0) a.conv_win[(static_cast<int64_t>(slot) * (a.K - 1) + r) * a.C + channel[0]] = past[0][j];
+    }
+  }
 }
 
-// The last K-1 inputs of every request, one thread per (request, channel).
+// The last K-1 inputs of B and C of every request, one thread per (request,
+// channel).
 template <bool BF16>
-__global__ void __launch_bounds__(256) ssm_windows(SsmArgs a) {
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (at >= static_cast<int64_t>(a.B) * a.C) return;
-  const int b = static_cast<int>(at / a.C), c = static_cast<int>(at % a.C);
+__global__ void __launch_bounds__(256) ssm_windows(SsmArgs a, uint32_t keys) {
+  const uint32_t at = blockIdx.x * 256 + threadIdx.x, b = at / keys;
+  if (b >= static_cast<uint32_t>(a.B)) return;
+  const int c = a.C - keys + static_cast<int>(at % keys);
   const Range range = request_range(a, b);
   const int slot = request_slot(a, b);
   if (slot < 0 || range.n == 0) return;
@@ -199,9 +249,11 @@ hipError_t launch(const SsmArgs& args, hipStream_t stream) {
   hipError_t rc = hipLaunchKernel(reinterpret_cast<const void*>(&ssm_decode<DK, DV, BF16, SBF16, VFIRST>),
                                   dim3(blocks), dim3(S::THREADS), kargs, 0, stream);
   if (rc != hipSuccess) return rc;
-  const int64_t channels = static_cast<int64_t>(args.B) * args.C;
-  return hipLaunchKernel(reinterpret_cast<const void*>(&ssm_windows<BF16>),
-                         dim3(static_cast<uint32_t>((channels + 255) / 256)), dim3(256), kargs, 0, stream);
+  uint32_t keys = 2 * static_cast<uint32_t>(args.H) * DK;
+  void* wargs[] = {const_cast<SsmArgs*>(&args), &keys};
+  const uint32_t channels = static_cast<uint32_t>(args.B) * keys;     // below 2^31, as B * C is
+  return hipLaunchKernel(reinterpret_cast<const void*>(&ssm_windows<BF16>), dim3((channels + 255) / 256), dim3(256),
+                         wargs, 0, stream);
 }
 
 template <int DK, int DV>

@@ -473,8 +473,8 @@ int kda_ssm_prefill(const kda_tensor* out, const kda_tensor* xbc, const kda_tens
  *   scale               [D] or [1] f32; NULL: one.
  *   eps                 finite, >= 0; 0 selects 1e-5.
  * Leading dimensions may be up to three (row-major); D is the last, 1 to
- * KDA_NORM_MAX, and at most 2^24 - 1 workgroups take the rows, 32 each for D
- * up to 64, 16 up to 128, 4 up to 2048 and else one (KDA_ERR_UNSUPPORTED).
+ * KDA_NORM_MAX, and rows times D rounded up to 64, 128 or a multiple of 512
+ * below 2^35 (KDA_ERR_UNSUPPORTED).
  * Other overlaps are not allowed.  hidden, block_out and the outputs need 16-byte alignment, the
  * vectors 4 (KDA_ERR_UNSUPPORTED).
  */
