@@ -11,6 +11,7 @@
 
 #include "kda_device.h"
 #include "kda_internal.h"
+#include "kda_tile.h"
 
 namespace kda {
 namespace {
@@ -37,21 +38,20 @@ __device__ __forceinline__ int request_slot(const SsmArgs& a, int b) {
   return s < 0 || s >= a.N ? -1 : s;
 }
 
-__device__ __forceinline__ float load_weight(const SsmArgs& a, const void* p, int64_t i) {
-  return a.w_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
-}
-
 // One channel's taps, newest last; w[kTaps - K ..] are used.
 struct Taps {
   float w[kTaps], bias;
-  __device__ __forceinline__ void load(const SsmArgs& a, int c) {
+
+  template <bool WBF16>
+  __device__ __forceinline__ void load_as(const SsmArgs& a, int c) {
 #pragma unroll
     for (int j = 0; j < kTaps; ++j) {
       const int tap = j - (kTaps - a.K);
-      w[j] = tap >= 0 ? load_weight(a, a.conv_w, static_cast<int64_t>(tap) * a.C + c) : 0.0f;
+      w[j] = tap >= 0 ? load_scalar<WBF16>(a.conv_w, static_cast<int64_t>(tap) * a.C + c) : 0.0f;
     }
-    bias = a.conv_b != nullptr ? load_weight(a, a.conv_b, c) : 0.0f;
+    bias = a.conv_b != nullptr ? load_scalar<WBF16>(a.conv_b, c) : 0.0f;
   }
+
   // Inputs oldest first.  Taps that are not there are left out, not
   // multiplied by zero: their inputs may be infinite.
   __device__ __forceinline__ float dot(int K, float x0, float x1, float x2, float x3) const {
@@ -62,6 +62,18 @@ struct Taps {
     return fmaf(w[3], x3, y);
   }
 };
+
+// Taps of N channels c[0], c[1], ..: one choice of the type, then all loads.
+template <int N>
+__device__ __forceinline__ void load_taps(const SsmArgs& a, const int (&c)[N], Taps (&taps)[N]) {
+  if (a.w_bf16) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) taps[n].template load_as<true>(a, c[n]);
+  } else {
+#pragma unroll
+    for (int n = 0; n < N; ++n) taps[n].template load_as<false>(a, c[n]);
+  }
+}
 
 // x * sigmoid(x); exp(-x) = inf for very negative x gives x * 0 = -0.
 __device__ __forceinline__ float silu_f(float x) { return x * sigmoid_f(x); }

@@ -96,11 +96,14 @@ __global__ void __launch_bounds__((Shape<DK, DV, BF16, SBF16, VFIRST>::THREADS))
                         : (i < S::COLS + DK ? keys + (i - S::COLS) : keys + a.H * DK + (i - S::COLS - DK));
     if (i >= S::CHANNELS) c = hv * DV;      // a channel of the head, convolved for nothing
     channel[p] = c;
-    taps[p].load(a, c);
+  }
+  load_taps(a, channel, taps);
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
 #pragma unroll
     for (int j = 0; j < kPast; ++j) {
       const int r = j - (kTaps - a.K);
-      past[p][j] = r >= 0 ? a.conv_win[(static_cast<int64_t>(slot) * (a.K - 1) + r) * a.C + c] : 0.0f;
+      past[p][j] = r >= 0 ? a.conv_win[(static_cast<int64_t>(slot) * (a.K - 1) + r) * a.C + channel[p]] : 0.0f;
     }
   }
   const float amp = exp_f(a.a_log[hv]), bias = a.dt_bias[hv];

@@ -209,8 +209,7 @@ __global__ void __launch_bounds__(256) ssm_keys(Plan p, bool, bool) {
     const int which = i / DK, k = i % DK;
     const int c = channels + which * a.H * DK + h * DK + k;
     Taps taps[2];
-    taps[0].load(a, c);
-    taps[1].load(a, c + 1);
+    load_taps(a, {c, c + 1}, taps);
     float in[TOKENS + kPast][2];
 #pragma unroll
     for (int j = 0; j < TOKENS + kPast; ++j) {
@@ -546,8 +545,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(M
   }
 
   Taps taps[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) taps[n].load(a, column + n);
+  load_taps(a, {column, column + 1}, taps);
   const float amp = exp_f(a.a_log[hv]), bias = a.dt_bias[hv];
   const float skip = a.d_skip != nullptr ? a.d_skip[hv] : 0.0f;
   auto& own = sh.wave[wave];
