@@ -110,7 +110,8 @@ def build(verbose: bool = True) -> str:
     units.append(("kda_verify", "kda_verify", []))
     units.append(("kda_gdr_prefill", "kda_gdr_prefill", []))
     units.append(("kda_ssm_decode", "kda_ssm_decode", []))
-    units += [("kda_ssm_prefill", f"kda_ssm_prefill_dk{dk}", [f"-DKDA_SSM_DK={dk}"]) for dk in (32, 64, 128)]
+    units += [("kda_ssm_prefill", f"kda_ssm_prefill_{dk}_{dv}", [f"-DKDA_SSM_DK={dk}", f"-DKDA_SSM_DV={dv}"])
+              for dk in (32, 64, 128) for dv in (32, 64, 128)]
     units.append(("kda_norm", "kda_norm", []))
     lib_objs = [os.path.join(BUILD, f"{obj}.o") for _, obj, _ in units]
     bench_o = os.path.join(BUILD, "bench_copy.o")

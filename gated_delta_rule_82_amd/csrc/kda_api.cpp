@@ -81,12 +81,11 @@ int launch_window(const WindowArgs& args, int dk, int dv, bool qkv_bf16, bool st
 
 int launch_ssm_prefill(const SsmArgs& args, int dk, int dv, bool bf16, bool state_bf16, int state_layout,
                        hipStream_t stream) {
-  switch (dk) {
-    case 32: return launch_ssm_prefill_dk<32>(args, dv, bf16, state_bf16, state_layout, stream);
-    case 64: return launch_ssm_prefill_dk<64>(args, dv, bf16, state_bf16, state_layout, stream);
-    case 128: return launch_ssm_prefill_dk<128>(args, dv, bf16, state_bf16, state_layout, stream);
-    default: return KDA_ERR_UNSUPPORTED;
-  }
+#define KDA_SSM_CASE(DK, DV) \
+  if (dk == DK && dv == DV) return launch_ssm_prefill_of<DK, DV>(args, bf16, state_bf16, state_layout, stream);
+  KDA_SSM_SIZES(KDA_SSM_CASE)
+#undef KDA_SSM_CASE
+  return KDA_ERR_UNSUPPORTED;
 }
 
 }  // namespace kda

@@ -126,19 +126,18 @@ struct SsmArgs {
 };
 
 // Enqueue kda_ssm_decode (kda_ssm_decode.hip) and kda_ssm_prefill
-// (kda_ssm_prefill.hip, compiled once per dk with KDA_SSM_DK; kda_api.cpp
-// picks the object).  Return codes as below.
+// (kda_ssm_prefill.hip, compiled once per dk and dv with KDA_SSM_DK and
+// KDA_SSM_DV; kda_api.cpp picks the object).  Return codes as below.
 int launch_ssm_decode(const SsmArgs& args, int dk, int dv, bool bf16, bool state_bf16, int state_layout,
                       hipStream_t stream);
-template <int DK>
-int launch_ssm_prefill_dk(const SsmArgs& args, int dv, bool bf16, bool state_bf16, int state_layout,
-                          hipStream_t stream);
-template <>
-int launch_ssm_prefill_dk<32>(const SsmArgs&, int, bool, bool, int, hipStream_t);
-template <>
-int launch_ssm_prefill_dk<64>(const SsmArgs&, int, bool, bool, int, hipStream_t);
-template <>
-int launch_ssm_prefill_dk<128>(const SsmArgs&, int, bool, bool, int, hipStream_t);
+template <int DK, int DV>
+int launch_ssm_prefill_of(const SsmArgs& args, bool bf16, bool state_bf16, int state_layout, hipStream_t stream);
+#define KDA_SSM_SIZES(X) X(32, 32) X(32, 64) X(32, 128) X(64, 32) X(64, 64) X(64, 128) X(128, 32) X(128, 64) X(128, 128)
+#define KDA_SSM_DECLARE(DK, DV) \
+  template <>                   \
+  int launch_ssm_prefill_of<DK, DV>(const SsmArgs&, bool, bool, int, hipStream_t);
+KDA_SSM_SIZES(KDA_SSM_DECLARE)
+#undef KDA_SSM_DECLARE
 
 // kda_norm_residual and kda_norm_gate, flattened (kda_norm.hip).
 struct ResidualArgs {

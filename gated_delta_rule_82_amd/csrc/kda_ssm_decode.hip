@@ -281,15 +281,7 @@ int launch_ssm_decode(const SsmArgs& args, int dk, int dv, bool bf16, bool state
   hipError_t rc = hipErrorInvalidValue;
 #define KDA_SSM_CASE(K, V) \
   if (dk == K && dv == V) rc = launch<K, V>(args, bf16, state_bf16, v_first, stream);
-  KDA_SSM_CASE(32, 32)
-  KDA_SSM_CASE(32, 64)
-  KDA_SSM_CASE(32, 128)
-  KDA_SSM_CASE(64, 32)
-  KDA_SSM_CASE(64, 64)
-  KDA_SSM_CASE(64, 128)
-  KDA_SSM_CASE(128, 32)
-  KDA_SSM_CASE(128, 64)
-  KDA_SSM_CASE(128, 128)
+  KDA_SSM_SIZES(KDA_SSM_CASE)
 #undef KDA_SSM_CASE
   return rc == hipSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }

@@ -36,14 +36,15 @@
 #include "kda_ssm.h"
 #include "kda_tile.h"
 
-#ifndef KDA_SSM_DK
-#error "compile with -DKDA_SSM_DK=32, 64 or 128"
+#if !defined(KDA_SSM_DK) || !defined(KDA_SSM_DV)
+#error "compile with -DKDA_SSM_DK and -DKDA_SSM_DV, each 32, 64 or 128"
 #endif
 
 namespace kda {
 namespace {
 
 constexpr int DK = KDA_SSM_DK;
+constexpr int DV = KDA_SSM_DV;
 constexpr int Q = kSsmChunk;
 constexpr int kKeySteps = DK / 32;      // matrix steps of 32 over the keys
 constexpr int kKeyTiles = DK / 16;
@@ -65,9 +66,20 @@ struct Keys {
 };
 static_assert(sizeof(Keys) == 4 * (96 * DK + 1024), "KDA_SSM_WORKSPACE");
 
+// ... and of 32 tokens and a head.  c is the running sum of log2 exp(g).
+struct Steps {
+  float hi[Q], lo[Q];                         // c in two parts
+  float decay[Q];                             // exp(g_t)
+  float from[Q];                              // exp(c_t)
+  float step[Q];
+};
+constexpr int kSteps = sizeof(Steps) / 4;
+static_assert(kSteps == 160, "KDA_SSM_WORKSPACE");
+
 struct Plan {
   SsmArgs a;
   Keys* keys;           // [chunk slot][H]
+  Steps* steps;         // [chunk slot][HV]
   float* windows;       // [B][K-1][C], as they were
   float* states;        // [segment slot][HV][DK][DV]: what a segment adds, then the state before it
   float* decays;        // [segment slot][HV]
@@ -101,12 +113,13 @@ __device__ __forceinline__ uint32_t high_halves(float lo, float hi) {
 }
 __device__ __forceinline__ float truncated(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
 
-// Eight values as N bf16 terms.  The last of two terms is rounded to nearest;
-// the last of three holds all bits that are left.
-template <int N>
-__device__ __forceinline__ void split(const float (&x)[8], u32x4 (&term)[N]) {
+// L values as N bf16 terms.  The last of two terms is rounded to nearest; the
+// last of three holds all bits that are left.
+template <int N, int L, typename T>
+__device__ __forceinline__ void split(const float (&x)[L], T (&term)[N]) {
+  static_assert(sizeof(T) == 2 * L, "pairs of bf16");
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
+  for (int e = 0; e < L / 2; ++e) {
     const float x0 = x[2 * e], x1 = x[2 * e + 1];
     term[0][e] = high_halves(x0, x1);
     const float r0 = x0 - truncated(x0), r1 = x1 - truncated(x1);
@@ -174,6 +187,24 @@ __device__ __forceinline__ void set_window(const Plan& p, const Range& range, in
     if (keep) p.windows[(static_cast<int64_t>(b) * (a.K - 1) + j) * a.C + c] = old[j];
     win[static_cast<int64_t>(j) * a.C] = next[j];
   }
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_from(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, ROWS, 0xf, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, ROWS, 0xf, true);
+  return x + __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// Sum over this lane and those before it in its half of the wave: within rows
+// of 16, then the first row's last lane to the second.
+__device__ __forceinline__ double running_sum(double x) {
+  x = add_from<0x111, 0xf>(x);
+  x = add_from<0x112, 0xf>(x);
+  x = add_from<0x114, 0xf>(x);
+  x = add_from<0x118, 0xf>(x);
+  return add_from<0x142, 0xa>(x);
 }
 
 // TY terms of C, and of the pairs' operands; TS of B.
@@ -250,7 +281,25 @@ __global__ void __launch_bounds__(256) ssm_keys(Plan p, bool, bool) {
   if (u.i == 0 && tid < 2 * DK)         // this workgroup alone has read them
     set_window<BF16>(p, range, u.b, slot, channels + tid / DK * a.H * DK + h * DK + tid % DK, false);
 
-  Keys& out = p.keys[(static_cast<int64_t>(range.t0 / Q) + u.b + u.i) * a.H + h];
+  const int64_t here = static_cast<int64_t>(range.t0 / Q) + u.b + u.i;
+  // steps and decays of the group's heads, one per half wave
+  for (int i = 0; i < a.G; i += 8) {
+    const int hv = h * a.G + min(i + tid / Q, a.G - 1), t = tid % Q;
+    const int64_t at = static_cast<int64_t>(range.t0) + begin + min(t, valid - 1);
+    const float step = t < valid ? softplus_f(a.dt[at * a.HV + hv] + a.dt_bias[hv]) : 0.0f;
+    const double g = static_cast<double>(step) * static_cast<double>(-exp_f(a.a_log[hv])) * 1.4426950408889634;
+    const double c = running_sum(g);
+    const float part = static_cast<float>(c);
+    if (i + tid / Q >= a.G) continue;
+    Steps& to = p.steps[here * a.HV + hv];
+    to.hi[t] = part;
+    to.lo[t] = static_cast<float>(c - static_cast<double>(part));
+    to.decay[t] = __builtin_amdgcn_exp2f(static_cast<float>(g));
+    to.from[t] = __builtin_amdgcn_exp2f(part);
+    to.step[t] = step;
+  }
+
+  Keys& out = p.keys[here * a.H + h];
   const int col = lane % 16, quad = lane / 16;
   for (int tile = wave; tile < kKeyTiles; tile += 4) {
     float x[8];
@@ -307,22 +356,17 @@ enum Mode { kWhole, kSegment, kJoined };
 
 constexpr int NT = 2;                   // 16-column tiles of a wave; a lane's columns are adjacent
 constexpr int kColumns = NT * 16;
+constexpr int kSlabs = DV / kColumns;   // waves of a head
 constexpr int kWaves = 4;               // of a workgroup, all of one group
 constexpr int kThreads = kWaves * kWave;
 
-// A workgroup's LDS: the chunk's operands, each read by all waves, and each
-// wave's own step sizes and decays.
+// A workgroup's LDS: the chunk's operands, which its waves share.
 template <int TY, int TS>
 struct Shared {
   u32x4 b[TS][kKeyTiles][kWave];
   u32x4 c[TY][2][kKeySteps][kWave];
-  f32x4 pairs[2][2][kWave];
-  struct {
-    float hi[Q], lo[Q];                 // c in two parts, base 2
-    float decay[Q];                     // exp(g_t)
-    float from[Q];                      // exp(c_t)
-    float step[Q];
-  } wave[kWaves];
+  u32x2 m[kWaves / kSlabs][TY][2][kWave][2];  // of a head: rows 16 tokens t; 32 tokens s
+  Steps steps[kWaves][2];               // of this chunk and the next
 };
 
 // N pieces of 16 bytes, from memory to LDS by way of the threads' registers.
@@ -390,7 +434,7 @@ struct Inputs {
 // A wave's part of a state tile [DK][dv] or [dv][DK] at `tile`: keys
 // kt * 16 + quad * 4 + i, columns v + n.
 template <bool SBF16, bool VFIRST, bool STORE>
-__device__ __forceinline__ void move_state(__amdgpu_buffer_rsrc_t tile, int dv, int quad, int v,
+__device__ __forceinline__ void move_state(__amdgpu_buffer_rsrc_t tile, int quad, int v,
                                            f32x4 (&S)[kKeyTiles][NT]) {
   constexpr int E = SBF16 ? 2 : 4;
 #pragma unroll
@@ -413,7 +457,7 @@ __device__ __forceinline__ void move_state(__amdgpu_buffer_rsrc_t tile, int dv, 
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int at = ((kt * 16 + quad * 4 + i) * dv + v) * E;
+        const int at = ((kt * 16 + quad * 4 + i) * DV + v) * E;
         if constexpr (STORE) {
           if constexpr (SBF16) {
             __builtin_amdgcn_raw_buffer_store_b32(f32x2_to_bf16x2_rne(S[kt][0][i], S[kt][1][i]), tile, at, 0, 0);
@@ -436,34 +480,15 @@ __device__ __forceinline__ void move_state(__amdgpu_buffer_rsrc_t tile, int dv, 
 }
 
 template <bool STORE>
-__device__ __forceinline__ void move_pool(__amdgpu_buffer_rsrc_t tile, bool state_bf16, bool v_first, int dv, int quad,
-                                          int v, f32x4 (&S)[kKeyTiles][NT]) {
+__device__ __forceinline__ void move_pool(__amdgpu_buffer_rsrc_t tile, bool state_bf16, bool v_first, int quad, int v,
+                                          f32x4 (&S)[kKeyTiles][NT]) {
   if (state_bf16) {
-    if (v_first) move_state<true, true, STORE>(tile, dv, quad, v, S);
-    else move_state<true, false, STORE>(tile, dv, quad, v, S);
+    if (v_first) move_state<true, true, STORE>(tile, quad, v, S);
+    else move_state<true, false, STORE>(tile, quad, v, S);
   } else {
-    if (v_first) move_state<false, true, STORE>(tile, dv, quad, v, S);
-    else move_state<false, false, STORE>(tile, dv, quad, v, S);
+    if (v_first) move_state<false, true, STORE>(tile, quad, v, S);
+    else move_state<false, false, STORE>(tile, quad, v, S);
   }
-}
-
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double add_from(double x) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, x);
-  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, ROWS, 0xf, true);
-  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, ROWS, 0xf, true);
-  return x + __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
-}
-
-// Sum over this lane and those before it: within rows of 16, then the rows'
-// last lanes to the rows behind.
-__device__ __forceinline__ double running_sum(double x) {
-  x = add_from<0x111, 0xf>(x);
-  x = add_from<0x112, 0xf>(x);
-  x = add_from<0x114, 0xf>(x);
-  x = add_from<0x118, 0xf>(x);
-  x = add_from<0x142, 0xa>(x);
-  return add_from<0x143, 0xc>(x);
 }
 
 // The lanes 16 quad + col whose token t = 16 mt + col is at or behind token
@@ -478,14 +503,42 @@ __device__ __forceinline__ constexpr uint64_t lanes_from(int mt, int j) {
   return lanes;
 }
 
-template <bool BF16, int TY, int TS, int MODE>
+// Half a fragment of M[t][s] = (C_t.B_s) exp(c_t - c_s) step_s, the lane's
+// tokens t = 16 mt + col and s = 8 quad + 4 half + 0 .. 3 (mt and half are the
+// wave's); zero for s > t.  The factors exp(c_t - c_s) are taken from the last
+// s backwards, one exponential and then the decays in between; one where
+// s >= t.
+template <int TY>
+__device__ __forceinline__ void decayed_pairs(const Steps& of, f32x4 pairs, float skip, int mt, int half, int lane,
+                                              u32x2 (&m)[TY][2][kWave][2]) {
+  const int t = mt * 16 + lane % 16, s = lane / 16 * 8 + half * 4;
+  const f32x4 decay = *reinterpret_cast<const f32x4*>(of.decay + s), step = *reinterpret_cast<const f32x4*>(of.step + s);
+  float f = __builtin_amdgcn_exp2f(fminf((of.hi[t] - of.hi[s + 3]) + (of.lo[t] - of.lo[s + 3]), 0.0f));
+  auto lanes = [&](int j) {     // one of four constants
+    const uint64_t first = half == 0 ? lanes_from(0, j) : lanes_from(0, 4 + j);
+    const uint64_t second = half == 0 ? lanes_from(1, j) : lanes_from(1, 4 + j);
+    return mt == 0 ? first : second;
+  };
+  float x[4];
+#pragma unroll
+  for (int j = 3; j >= 0; --j) {
+    const uint64_t reached = lanes(j), passed = lanes(j + 1);   // s <= t, s < t
+    if (j < 3) f *= __builtin_amdgcn_inverse_ballot_w64(passed) ? decay[j + 1] : 1.0f;
+    x[j] = fmaf(pairs[j] * step[j], __builtin_amdgcn_inverse_ballot_w64(reached) ? f : 0.0f,
+                __builtin_amdgcn_inverse_ballot_w64(reached & ~passed) ? skip : 0.0f);
+  }
+  u32x2 term[TY];
+  split<TY>(x, term);
+#pragma unroll
+  for (int n = 0; n < TY; ++n) m[n][mt][lane][half] = term[n];
+}
+
+template <bool BF16, bool FULL, int TY, int TS, int MODE>
 __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(MODE == kSegment ? 3 : 2, MODE == kSegment ? 3 : 2))) ssm_scan(Plan p, bool state_bf16, bool v_first) {
   const SsmArgs& a = p.a;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   Shared<TY, TS>& sh = *reinterpret_cast<Shared<TY, TS>*>(lds);
-  const int dv = (a.C - 2 * a.H * DK) / a.HV;
-  const int slabs = dv / kColumns;
-  const int waves = a.G * slabs, blocks = (waves + kWaves - 1) / kWaves;    // of a group
+  const int waves = a.G * kSlabs, blocks = (waves + kWaves - 1) / kWaves;    // of a group
 
   // the workgroups of a unit's group share its keys: on one XCD, where there
   // are groups for all of them
@@ -513,11 +566,11 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(M
   // waves behind the group's last help with its operands
   const int w = block * kWaves + wave;
   const bool works = w < waves;
-  const int hv = h * a.G + (works ? w / slabs : 0), slab = works ? w % slabs : 0;
+  const int hv = h * a.G + (works ? w / kSlabs : 0), slab = wave % kSlabs;
   const int col = lane % 16, quad = lane / 16;
   const int v = slab * kColumns + col * NT;       // the lane's first column of the head
-  const int column = hv * dv + v;                 // ... of out, and its channel of x
-  const int out_row = a.HV * dv;
+  const int column = hv * DV + v;                 // ... of out, and its channel of x
+  const int out_row = a.HV * DV;
   constexpr int E = BF16 ? 2 : 4;
   if (slot < 0) {
     if (MODE != kSegment && works) {
@@ -529,14 +582,14 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(M
 
   f32x4 S[kKeyTiles][NT];
   const int64_t here = MODE == kWhole ? 0 : static_cast<int64_t>(range.t0 / p.segment) + u.b + u.i;
-  const int tile_bytes = DK * dv * (MODE == kWhole && state_bf16 ? 2 : 4);
+  const int tile_bytes = DK * DV * (MODE == kWhole && state_bf16 ? 2 : 4);
   char* const tile =
       MODE == kWhole ? static_cast<char*>(a.state_pool) + (static_cast<int64_t>(slot) * a.HV + hv) * tile_bytes
                      : reinterpret_cast<char*>(p.states) + (here * a.HV + hv) * tile_bytes;
   if constexpr (MODE == kWhole) {
-    move_pool<false>(tile_resource(tile, tile_bytes), state_bf16, v_first, dv, quad, v, S);
+    move_pool<false>(tile_resource(tile, tile_bytes), state_bf16, v_first, quad, v, S);
   } else if constexpr (MODE == kJoined) {
-    move_state<false, false, false>(tile_resource(tile, tile_bytes), dv, quad, v, S);
+    move_state<false, false, false>(tile_resource(tile, tile_bytes), quad, v, S);
   } else {
 #pragma unroll
     for (int kt = 0; kt < kKeyTiles; ++kt)
@@ -546,78 +599,77 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(M
 
   Taps taps[NT];
   load_taps(a, {column, column + 1}, taps);
-  const float amp = exp_f(a.a_log[hv]), bias = a.dt_bias[hv];
   const float skip = a.d_skip != nullptr ? a.d_skip[hv] : 0.0f;
-  auto& own = sh.wave[wave];
   float gone = 1.0f;                    // the segment's decay
 
-  constexpr int kC = TY * 2 * kKeySteps * kWave, kPairs = 2 * 2 * kWave, kB = TS * kKeyTiles * kWave;
+  constexpr int kC = TY * 2 * kKeySteps * kWave, kB = TS * kKeyTiles * kWave;
   Staged<kC> stage_c;
-  Staged<kPairs> stage_pairs;
   Staged<kB> stage_b;
   Inputs<BF16> in;
-  float dt;
-  const Keys* const first_keys = p.keys + (static_cast<int64_t>(range.t0 / Q) + u.b) * a.H + h;
+  const int64_t first_slot = static_cast<int64_t>(range.t0 / Q) + u.b;
+  const Keys* const first_keys = p.keys + first_slot * a.H + h;
   auto keys_at = [&](int t0) { return first_keys + static_cast<int64_t>(t0 / Q) * a.H; };
-  auto load = [&](int t0, int quad, int column) {
-    const int valid = min(Q, end - t0);
-    const int64_t t = static_cast<int64_t>(range.t0) + t0 + min(lane, valid - 1);
-    dt = a.dt[t * a.HV + hv];
-    in.load(a, range, t0, valid, quad, column);
-    if constexpr (MODE != kSegment) {
-      const Keys* const keys = keys_at(t0);
-      stage_c.load(&keys->c[0][0][0][0]);
-      stage_pairs.load(reinterpret_cast<const u32x4*>(&keys->pairs[0][0][0]));
-    }
-  };
-  auto store = [&]() {
-    if constexpr (MODE != kSegment) {
-      stage_c.store(&sh.c[0][0][0][0]);
-      stage_pairs.store(reinterpret_cast<u32x4*>(&sh.pairs[0][0][0]));
-    }
-  };
-  load(begin, quad, column);
-  store();
+  const float* const first_steps = reinterpret_cast<const float*>(p.steps + first_slot * a.HV + hv);
 
-  for (int t0 = begin; t0 < end; t0 += Q) {
-    const int valid = min(Q, end - t0);
-    // The lane's place, anew for every 32 tokens: addresses and comparisons
-    // made of it would otherwise be kept in registers through all of them.
-    int col = lane % 16, quad = lane / 16;
-    asm volatile("" : "+v"(col), "+v"(quad));
-    const int column = hv * dv + slab * kColumns + col * NT;
-    lds_barrier();            // c and pairs are there, and b has been read
-    const bool update = MODE != kJoined || t0 + Q < end;     // a joined segment's last state is not used
-    stage_b.load(&keys_at(t0)->b[0][0][0]);
-
-    // steps and the running sum of the decays, one token per lane
-    float total;              // the decay over all 32
-    {
-      const float step = lane < valid ? softplus_f(dt + bias) : 0.0f;
-      const double g = static_cast<double>(step) * static_cast<double>(-amp) * 1.4426950408889634;
-      const double c = running_sum(g);
-      const float part = static_cast<float>(c);
-      const float from = __builtin_amdgcn_exp2f(part);
-      if (lane < Q) {
-        own.hi[lane] = part;
-        own.lo[lane] = static_cast<float>(c - static_cast<double>(part));
-        own.decay[lane] = __builtin_amdgcn_exp2f(static_cast<float>(g));
-        own.from[lane] = from;
-        own.step[lane] = step;
+  // the head's steps, and the wave's share of the pairs
+  constexpr int kShare = 4 / kSlabs;          // half fragments
+  float steps[3];
+  f32x4 pairs[kShare];
+  auto load_steps = [&](int t0) {
+    const float* const from = first_steps + static_cast<int64_t>(t0 / Q) * a.HV * kSteps;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) steps[i] = from[min(i * kWave + lane, kSteps - 1)];
+    if constexpr (MODE != kSegment) {
+#pragma unroll
+      for (int i = 0; i < kShare; ++i) {
+        const int share = slab + i * kSlabs;
+        pairs[i] = keys_at(t0)->pairs[share % 2][share / 2][lane];
       }
-      total = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(from), Q - 1));
-      gone *= total;
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-      __builtin_amdgcn_wave_barrier();
     }
-
-    // the lane's columns, convolved
-    float x[8][NT], past[kPast][NT];
+  };
+  auto store_steps = [&](Steps& to) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) reinterpret_cast<float*>(&to)[min(i * kWave + lane, kSteps - 1)] = steps[i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    if constexpr (MODE != kSegment) {
+#pragma unroll
+      for (int i = 0; i < kShare; ++i) {
+        const int share = slab + i * kSlabs;
+        decayed_pairs<TY>(to, pairs[i], skip, share % 2, share / 2, lane, sh.m[wave / kSlabs]);
+      }
+    }
+  };
+  // the lane's columns, convolved.  Tokens behind the last have step 0 and
+  // keys of zero, so their x meets nothing.
+  float x[8][NT];
+  auto convolve = [&](const float (&past)[kPast][NT]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        auto at = [&](int i) { return i < kPast ? past[i][n] : in.get(i, n); };
+        x[j][n] = silu_f(taps[n].dot(FULL ? kTaps : a.K, at(j), at(j + 1), at(j + 2), at(j + 3)));
+      }
+  };
+  auto unpack_past = [&](float (&past)[kPast][NT]) {
 #pragma unroll
     for (int j = 0; j < kPast; ++j)
 #pragma unroll
       for (int n = 0; n < NT; ++n) past[j][n] = in.get(j, n);
-    if (t0 == 0) {                      // the window of before
+  };
+
+  load_steps(begin);
+  in.load(a, range, begin, min(Q, end - begin), quad, column);
+  if constexpr (MODE != kSegment) {
+    stage_c.load(&keys_at(begin)->c[0][0][0][0]);
+    stage_c.store(&sh.c[0][0][0][0]);
+  }
+  store_steps(sh.steps[wave][begin / Q % 2]);
+  {
+    float past[kPast][NT];
+    unpack_past(past);
+    if (begin == 0) {                   // the window of before
 #pragma unroll
       for (int j = 0; j < kPast; ++j) {
         const int r = a.K - 1 - kPast + j;
@@ -628,161 +680,151 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(M
         }
       }
     }
-    auto convolve = [&](int K) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          auto at = [&](int i) { return i < kPast ? past[i][n] : in.get(i, n); };
-          x[j][n] = silu_f(taps[n].dot(K, at(j), at(j + 1), at(j + 2), at(j + 3)));
-        }
-    };
-    if (a.K == kTaps) convolve(kTaps);  // all taps: no choice per value
-    else convolve(a.K);
-    if (valid < Q) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          if (quad * 8 + j >= valid) x[j][n] = 0.0f;
-    }
-    const int first = quad * 8;         // the lane's eight tokens s
-    float decay[8], d[8];
-#pragma unroll
-    for (int j = 0; j < 8; j += 4) {
-      const f32x4 e = *reinterpret_cast<const f32x4*>(own.decay + first + j);
-      const f32x4 f = *reinterpret_cast<const f32x4*>(own.step + first + j);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        decay[j + i] = e[i];
-        d[j + i] = f[i];
-      }
-    }
-    const float last_hi = own.hi[first + 7], last_lo = own.lo[first + 7];
+    convolve(past);
+  }
 
+  // Per 32 tokens two stretches between barriers, each of products and of
+  // other work for the next ones, without a branch: outputs from the state,
+  // with the operands of the update; the update, with x and m of the next 32
+  // (behind the last, the last again, which nothing reads).
+  for (int t0 = begin; t0 < end; t0 += Q) {
+    const int valid = min(Q, end - t0);
+    const int next = t0 + Q < end ? t0 + Q : t0;
+    // The lane's place, anew for every 32 tokens: addresses made of it would
+    // otherwise be kept in registers through all of them.
+    int col = lane % 16, quad = lane / 16;
+    asm volatile("" : "+v"(col), "+v"(quad));
+    const int column = hv * DV + slab * kColumns + col * NT;
+    const Steps& of = sh.steps[wave][t0 / Q % 2];
+    lds_barrier();            // c and m are there, and b has been read
+    stage_b.load(&keys_at(t0)->b[0][0][0]);
+    load_steps(next);
+    in.load(a, range, next, min(Q, end - next), quad, column);
+
+    f32x4 y[2][NT];
     if constexpr (MODE != kSegment) {
-      if (works) {
-        f32x4 y[2][NT];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+      for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) y[mt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        // C^T S0
+        for (int n = 0; n < NT; ++n) y[mt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      // C^T S0
 #pragma unroll
-        for (int step = 0; step < kKeySteps; ++step) {
-          u32x4 s[NT][TY];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float f[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = S[2 * step + j / 4][n][j % 4];
-            split(f, s[n]);
-          }
-          u32x4 ck[2][TY];
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int m = 0; m < TY; ++m) ck[mt][m] = sh.c[m][mt][step][lane];
-          products(ck, s, y);
-        }
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          const f32x4 f = *reinterpret_cast<const f32x4*>(own.from + mt * 16 + quad * 4);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) y[mt][n] *= f;
-        }
-        // the 32 tokens' own
-        u32x4 xs[NT][TY];
+      for (int step = 0; step < kKeySteps; ++step) {
+        u32x4 s[NT][TY];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float f[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = x[j][n];
-          split(f, xs[n]);
+          for (int j = 0; j < 8; ++j) f[j] = S[2 * step + j / 4][n][j % 4];
+          split(f, s[n]);
         }
-        u32x4 ms[2][TY];
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          const int t = mt * 16 + col;
-          const f32x4 p0 = sh.pairs[mt][0][lane], p1 = sh.pairs[mt][1][lane];
-          // exp(c_t - c_s), from the last s backwards; one where s >= t
-          float f = __builtin_amdgcn_exp2f(fminf((own.hi[t] - last_hi) + (own.lo[t] - last_lo), 0.0f));
-          float m[8];
-#pragma unroll
-          for (int j = 7; j >= 0; --j) {
-            const uint64_t reached = lanes_from(mt, j), passed = lanes_from(mt, j + 1);     // s <= t, s < t
-            if (j < 7) f *= __builtin_amdgcn_inverse_ballot_w64(passed) ? decay[j + 1] : 1.0f;
-            const float pair = (j < 4 ? p0[j % 4] : p1[j % 4]) * d[j];
-            m[j] = fmaf(pair, __builtin_amdgcn_inverse_ballot_w64(reached) ? f : 0.0f,
-                        __builtin_amdgcn_inverse_ballot_w64(reached & ~passed) ? skip : 0.0f);
-          }
-          split(m, ms[mt]);
-        }
-        products(ms, xs, y);
-        const __amdgpu_buffer_rsrc_t out = tile_resource(
-            static_cast<char*>(a.out) + (static_cast<int64_t>(range.t0) + t0) * out_row * E, valid * out_row * E);
+        u32x4 ck[2][TY];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int at = ((mt * 16 + quad * 4 + i) * out_row + column) * E;     // rows behind the last are dropped
-            if constexpr (BF16) {
-              __builtin_amdgcn_raw_buffer_store_b32(f32x2_to_bf16x2_rne(y[mt][0][i], y[mt][1][i]), out, at, 0, 0);
-            } else {
-              const u32x2 o = {__float_as_uint(y[mt][0][i]), __float_as_uint(y[mt][1][i])};
-              __builtin_amdgcn_raw_buffer_store_b64(o, out, at, 0, 0);
-            }
-          }
+          for (int m = 0; m < TY; ++m) ck[mt][m] = sh.c[m][mt][step][lane];
+        products(ck, s, y);
       }
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const f32x4 f = *reinterpret_cast<const f32x4*>(of.from + mt * 16 + quad * 4);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) y[mt][n] *= f;
+      }
+      // the 32 tokens' own
+      u32x4 xs[NT][TY], ms[2][TY];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = x[j][n];
+        split(f, xs[n]);
+      }
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int n = 0; n < TY; ++n)
+          ms[mt][n] = *reinterpret_cast<const u32x4*>(&sh.m[wave / kSlabs][n][mt][lane][0]);
+      products(ms, xs, y);
     }
-    stage_b.store(&sh.b[0][0][0]);
-    lds_barrier();            // b is there, and c and pairs have been read
-
-    const int next = t0 + Q;
-    if (next < end) load(next, quad, column);
-    if (update && works) {
-      // step_s exp(c_last - c_s), from the last s backwards
-      float f = __builtin_amdgcn_exp2f((own.hi[Q - 1] - last_hi) + (own.lo[Q - 1] - last_lo));
+    // x weighted for the update: step_s exp(c_last - c_s), from the last s
+    // backwards
+    u32x4 xw[NT][TS];
+    {
+      const int first = quad * 8;         // the lane's eight tokens s
+      float f = __builtin_amdgcn_exp2f((of.hi[Q - 1] - of.hi[first + 7]) + (of.lo[Q - 1] - of.lo[first + 7]));
       float g[8];
 #pragma unroll
-      for (int j = 7; j >= 0; --j) {
-        if (j < 7) f *= decay[j + 1];
-        g[j] = f * d[j];
+      for (int j = 4; j >= 0; j -= 4) {
+        const f32x4 decay = *reinterpret_cast<const f32x4*>(of.decay + first + j);
+        const f32x4 step = *reinterpret_cast<const f32x4*>(of.step + first + j);
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+          g[j + i] = f * step[i];
+          f *= decay[i];
+        }
       }
-      u32x4 xs[NT][TS];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float e[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) e[j] = x[j][n] * g[j];
-        split(e, xs[n]);
-      }
-#pragma unroll
-      for (int kt = 0; kt < kKeyTiles; kt += 2) {
-        u32x4 bk[2][TS];
-        f32x4 s[2][NT];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int m = 0; m < TS; ++m) bk[i][m] = sh.b[m][kt + i][lane];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) s[i][n] = S[kt + i][n] * total;
-        }
-        products(bk, xs, s);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) S[kt + i][n] = s[i][n];
+        split(e, xw[n]);
       }
     }
-    if (next < end) store();
+    if constexpr (MODE != kSegment) {
+      // rows behind the last, and all of a wave without columns, are dropped
+      const __amdgpu_buffer_rsrc_t out =
+          tile_resource(static_cast<char*>(a.out) + (static_cast<int64_t>(range.t0) + t0) * out_row * E,
+                        works ? valid * out_row * E : 0);
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = ((mt * 16 + quad * 4 + i) * out_row + column) * E;
+          if constexpr (BF16) {
+            __builtin_amdgcn_raw_buffer_store_b32(f32x2_to_bf16x2_rne(y[mt][0][i], y[mt][1][i]), out, at, 0, 0);
+          } else {
+            const u32x2 o = {__float_as_uint(y[mt][0][i]), __float_as_uint(y[mt][1][i])};
+            __builtin_amdgcn_raw_buffer_store_b64(o, out, at, 0, 0);
+          }
+        }
+    }
+    stage_b.store(&sh.b[0][0][0]);
+    lds_barrier();            // b is there, and c and m have been read
+
+    if constexpr (MODE != kSegment) stage_c.load(&keys_at(next)->c[0][0][0][0]);
+    const float total = of.from[Q - 1];
+    gone *= total;
+#pragma unroll
+    for (int kt = 0; kt < kKeyTiles; kt += 2) {
+      u32x4 bk[2][TS];
+      f32x4 s[2][NT];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int m = 0; m < TS; ++m) bk[i][m] = sh.b[m][kt + i][lane];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[i][n] = S[kt + i][n] * total;
+      }
+      products(bk, xw, s);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) S[kt + i][n] = s[i][n];
+    }
+    float past[kPast][NT];
+    unpack_past(past);
+    convolve(past);
+    store_steps(sh.steps[wave][next / Q % 2]);
+    if constexpr (MODE != kSegment) stage_c.store(&sh.c[0][0][0][0]);
   }
 
   if (!works) return;
   if constexpr (MODE == kWhole) {
-    move_pool<true>(tile_resource(tile, tile_bytes), state_bf16, v_first, dv, quad, v, S);
+    move_pool<true>(tile_resource(tile, tile_bytes), state_bf16, v_first, quad, v, S);
   } else if constexpr (MODE == kSegment) {
-    move_state<false, false, true>(tile_resource(tile, tile_bytes), dv, quad, v, S);
+    move_state<false, false, true>(tile_resource(tile, tile_bytes), quad, v, S);
     if (slab == 0 && lane == 0) p.decays[here * a.HV + hv] = gone;
   }
 }
@@ -791,27 +833,26 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(M
 // adjacent columns per thread.
 __global__ void __launch_bounds__(256) ssm_join(Plan p, bool state_bf16, bool v_first) {
   const SsmArgs& a = p.a;
-  const int dv = (a.C - 2 * a.H * DK) / a.HV;
-  const int parts = DK * dv / 1024;
+  constexpr int parts = DK * DV / 1024;
   const int part = blockIdx.x % parts, head = blockIdx.x / parts;
   const int hv = head % a.HV, b = head / a.HV;
   const Range range = request_range(a, b);
   const int slot = request_slot(a, b);
   if (slot < 0 || range.n == 0) return;
   const int at = (part * 256 + threadIdx.x) * 4;
-  const int k = at / dv, v = at % dv;
-  const int64_t tile = (static_cast<int64_t>(slot) * a.HV + hv) * DK * dv;
+  const int k = at / DV, v = at % DV;
+  const int64_t tile = (static_cast<int64_t>(slot) * a.HV + hv) * DK * DV;
   f32x4 s;
   int64_t where[4];
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
-    where[n] = tile + (v_first ? static_cast<int64_t>(v + n) * DK + k : static_cast<int64_t>(k) * dv + v + n);
+    where[n] = tile + (v_first ? static_cast<int64_t>(v + n) * DK + k : static_cast<int64_t>(k) * DV + v + n);
     s[n] = state_bf16 ? load_scalar<true>(a.state_pool, where[n]) : load_scalar<false>(a.state_pool, where[n]);
   }
   const int64_t first = static_cast<int64_t>(range.t0 / p.segment) + b;
   const int segments = (range.n - 1) / p.segment + 1;
-  const int64_t stride = static_cast<int64_t>(a.HV) * DK * dv;
-  float* const states = p.states + first * stride + static_cast<int64_t>(hv) * DK * dv + at;
+  const int64_t stride = static_cast<int64_t>(a.HV) * DK * DV;
+  float* const states = p.states + first * stride + static_cast<int64_t>(hv) * DK * DV + at;
   const float* const decays = p.decays + first * a.HV + hv;
 #pragma unroll 4
   for (int i = 0; i < segments; ++i) {
@@ -834,14 +875,15 @@ __global__ void __launch_bounds__(256) ssm_join(Plan p, bool state_bf16, bool v_
 // ---------------------------------------------------------------------------
 
 template <bool BF16, int TY, int TS, int MODE>
-hipError_t scan(const Plan& plan, int dv, bool state_bf16, bool v_first, hipStream_t stream) {
-  const void* const fn = reinterpret_cast<const void*>(&ssm_scan<BF16, TY, TS, MODE>);
+hipError_t scan(const Plan& plan, bool state_bf16, bool v_first, hipStream_t stream) {
+  const void* const fn = plan.a.K == kTaps ? reinterpret_cast<const void*>(&ssm_scan<BF16, true, TY, TS, MODE>)
+                                           : reinterpret_cast<const void*>(&ssm_scan<BF16, false, TY, TS, MODE>);
   constexpr int bytes = sizeof(Shared<TY, TS>);
   if constexpr (bytes > 65536) {        // beyond the default limit of dynamic LDS
     const hipError_t rc = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (rc != hipSuccess) return rc;
   }
-  const int64_t blocks = (static_cast<int64_t>(plan.a.G) * (dv / kColumns) + kWaves - 1) / kWaves;
+  const int64_t blocks = (static_cast<int64_t>(plan.a.G) * kSlabs + kWaves - 1) / kWaves;
   int64_t groups = static_cast<int64_t>(plan.units) * plan.a.H;
   if (groups >= kXcds) groups = (groups + kXcds - 1) / kXcds * kXcds;
   void* kargs[] = {const_cast<Plan*>(&plan), &state_bf16, &v_first};
@@ -849,35 +891,36 @@ hipError_t scan(const Plan& plan, int dv, bool state_bf16, bool v_first, hipStre
 }
 
 template <bool BF16, int TY, int TS>
-hipError_t run(const Plan& plan, int dv, bool state_bf16, bool v_first, hipStream_t stream) {
+hipError_t run(const Plan& plan, bool state_bf16, bool v_first, hipStream_t stream) {
   void* kargs[] = {const_cast<Plan*>(&plan), &state_bf16, &v_first};
-  const uint32_t window_blocks = static_cast<uint32_t>(plan.a.B) * ((plan.a.HV * dv + 255) / 256);
+  const uint32_t window_blocks = static_cast<uint32_t>(plan.a.B) * ((plan.a.HV * DV + 255) / 256);
   hipError_t rc = hipLaunchKernel(reinterpret_cast<const void*>(&ssm_keys<BF16, TY, TS>),
                                   dim3(plan.key_blocks + window_blocks), dim3(256), kargs, 0, stream);
   if (rc != hipSuccess) return rc;
-  if (plan.segment == 0) return scan<BF16, TY, TS, kWhole>(plan, dv, state_bf16, v_first, stream);
-  rc = scan<BF16, TY, TS, kSegment>(plan, dv, state_bf16, v_first, stream);
+  if (plan.segment == 0) return scan<BF16, TY, TS, kWhole>(plan, state_bf16, v_first, stream);
+  rc = scan<BF16, TY, TS, kSegment>(plan, state_bf16, v_first, stream);
   if (rc != hipSuccess) return rc;
-  const int64_t blocks = static_cast<int64_t>(plan.a.B) * plan.a.HV * (DK * dv / 1024);
+  const int64_t blocks = static_cast<int64_t>(plan.a.B) * plan.a.HV * (DK * DV / 1024);
   rc = hipLaunchKernel(reinterpret_cast<const void*>(&ssm_join), dim3(static_cast<uint32_t>(blocks)), dim3(256), kargs,
                        0, stream);
   if (rc != hipSuccess) return rc;
   // the state of a joined segment only reaches its outputs
-  return scan<BF16, TY, TY, kJoined>(plan, dv, state_bf16, v_first, stream);
+  return scan<BF16, TY, TY, kJoined>(plan, state_bf16, v_first, stream);
 }
 
 }  // namespace
 
 template <>
-int launch_ssm_prefill_dk<DK>(const SsmArgs& args, int dv, bool bf16, bool state_bf16, int state_layout,
-                              hipStream_t stream) {
+int launch_ssm_prefill_of<DK, DV>(const SsmArgs& args, bool bf16, bool state_bf16, int state_layout,
+                                  hipStream_t stream) {
   Plan plan{};
   plan.a = args;
   const int64_t chunks = static_cast<int64_t>(args.T) / Q + args.B;
   plan.keys = reinterpret_cast<Keys*>(args.workspace);
-  plan.windows = reinterpret_cast<float*>(plan.keys + chunks * args.H);
+  plan.steps = reinterpret_cast<Steps*>(plan.keys + chunks * args.H);
+  plan.windows = reinterpret_cast<float*>(plan.steps + chunks * args.HV);
   plan.states = plan.windows + static_cast<int64_t>(args.B) * (args.K - 1) * args.C;
-  const int64_t waves = static_cast<int64_t>(args.HV) * (dv > 64 ? 2 : 1);
+  const int64_t waves = static_cast<int64_t>(args.HV) * (DV > 64 ? 2 : 1);
   plan.units = args.B;
   plan.key_blocks = static_cast<uint32_t>(chunks * args.H);
   const int64_t most = KDA_SSM_SPLIT / waves;       // segments that the workspace has room for, beyond one a request
@@ -888,14 +931,14 @@ int launch_ssm_prefill_dk<DK>(const SsmArgs& args, int dv, bool bf16, bool state
     if (length < args.T) {
       plan.segment = static_cast<int32_t>(length);
       plan.units = static_cast<int32_t>(args.T / length + args.B);
-      plan.decays = plan.states + static_cast<int64_t>(plan.units) * args.HV * DK * dv;
+      plan.decays = plan.states + static_cast<int64_t>(plan.units) * args.HV * DK * DV;
     }
   }
   const bool v_first = state_layout == KDA_STATE_V_FIRST;
   hipError_t rc;
-  if (!bf16) rc = run<false, 3, 3>(plan, dv, state_bf16, v_first, stream);
-  else if (state_bf16) rc = run<true, 2, 2>(plan, dv, state_bf16, v_first, stream);
-  else rc = run<true, 2, 3>(plan, dv, state_bf16, v_first, stream);
+  if (!bf16) rc = run<false, 3, 3>(plan, state_bf16, v_first, stream);
+  else if (state_bf16) rc = run<true, 2, 2>(plan, state_bf16, v_first, stream);
+  else rc = run<true, 2, 3>(plan, state_bf16, v_first, stream);
   return rc == hipSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }
 

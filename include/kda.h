@@ -430,7 +430,7 @@ int kda_ssm_decode(const kda_tensor* out, const kda_tensor* xbc, const kda_tenso
 #define KDA_SSM_CHUNK 32
 #define KDA_SSM_SPLIT 1024
 #define KDA_SSM_WORKSPACE(T, B, H, HV, dk, dv, K)                                                   \
-  (((int64_t)(T) / KDA_SSM_CHUNK + (B)) * (H) * (96 * (int64_t)(dk) + 1024) +                       \
+  (((int64_t)(T) / KDA_SSM_CHUNK + (B)) * ((H) * (96 * (int64_t)(dk) + 1024) + 160 * (int64_t)(HV)) + \
    (int64_t)(B) * ((K)-1) * ((int64_t)(HV) * (dv) + 2 * (int64_t)(H) * (dk)) +                      \
    ((int64_t)KDA_SSM_SPLIT * 64 + (int64_t)(B) * (HV) * (dv)) * (dk) + 2 * (int64_t)KDA_SSM_SPLIT + \
    (int64_t)(B) * (HV) + 64)
