@@ -632,9 +632,9 @@ int plan_ssm(const kda_tensor* out, const kda_tensor* xbc, const kda_tensor* dt,
   for (const kda_tensor* t : optional)
     if (t != nullptr && !aligned(t, 16)) return KDA_ERR_UNSUPPORTED;
   if (prefill) {
-    // workgroups of 256: one per chunk and group, and per request and 256
-    // channels (fewer than B * C / 128, by the above below 2^24)
-    if (product_exceeds({T / KDA_SSM_CHUNK + B, H}, (1 << 23) - 1) || product_exceeds({B, C}, 1 << 29))
+    // workgroups of 256, below 2^24 in all: one per chunk and group, one per
+    // request and 256 channels, one per chunk and 32 heads
+    if (product_exceeds({T / KDA_SSM_CHUNK + B, H + (HV + 31) / 32}, (1 << 23) - 1) || product_exceeds({B, C}, 1 << 29))
       return KDA_ERR_UNSUPPORTED;
     if (workspace->shape[0] < KDA_SSM_WORKSPACE(T, B, H, HV, DK, DV, K)) return KDA_ERR_SHAPE;
   }

@@ -85,7 +85,7 @@ struct Plan {
   float* decays;        // [segment slot][HV]
   int32_t segment;      // tokens per segment, 0: not split
   int32_t units;        // segment slots, or B
-  uint32_t key_blocks;  // workgroups of ssm_keys that have a chunk
+  uint32_t key_blocks, window_blocks, step_blocks;    // workgroups of ssm_keys
 };
 
 // Requests' chunks (or segments) are numbered through: request b's begin at
@@ -207,16 +207,61 @@ __device__ __forceinline__ double running_sum(double x) {
   return add_from<0x142, 0xa>(x);
 }
 
+// Steps of 32 tokens and 32 heads: read by rows of heads, a half wave per head.
+constexpr int kHeads = 32;
+__device__ __forceinline__ void set_steps(const Plan& p, int slot_at, int head0, float (&tile)[kHeads][Q + 1]) {
+  const SsmArgs& a = p.a;
+  const Unit u = find_unit(a, slot_at, Q);
+  const Range range = request_range(a, u.b);
+  if (request_slot(a, u.b) < 0 || u.i < 0 || static_cast<int64_t>(u.i) * Q >= range.n) return;
+  const int valid = min(Q, range.n - u.i * Q);
+  const int64_t first = static_cast<int64_t>(range.t0) + u.i * Q;
+  const int lane = threadIdx.x % kHeads, part = threadIdx.x / kHeads;
+#pragma unroll
+  for (int t = part; t < Q; t += 256 / kHeads)
+    tile[lane][t] = a.dt[(first + min(t, valid - 1)) * a.HV + min(head0 + lane, a.HV - 1)];
+  constexpr int EACH = kHeads / (256 / Q);      // heads of a half wave
+  float bias[EACH], amp[EACH];
+#pragma unroll
+  for (int e = 0; e < EACH; ++e) {
+    const int hv = min(head0 + part * EACH + e, a.HV - 1);
+    bias[e] = a.dt_bias[hv];
+    amp[e] = a.a_log[hv];
+  }
+  __syncthreads();
+  Steps* const to = p.steps + (static_cast<int64_t>(range.t0 / Q) + u.b + u.i) * a.HV + head0 + part * EACH;
+  const int t = lane;
+#pragma unroll
+  for (int e = 0; e < EACH; ++e) {
+    const float step = t < valid ? softplus_f(tile[part * EACH + e][t] + bias[e]) : 0.0f;
+    const double g = static_cast<double>(step) * static_cast<double>(-exp_f(amp[e])) * 1.4426950408889634;
+    const double c = running_sum(g);
+    const float high = static_cast<float>(c);
+    if (head0 + part * EACH + e < a.HV) {
+      to[e].hi[t] = high;
+      to[e].lo[t] = static_cast<float>(c - static_cast<double>(high));
+      to[e].decay[t] = __builtin_amdgcn_exp2f(static_cast<float>(g));
+      to[e].from[t] = __builtin_amdgcn_exp2f(high);
+      to[e].step[t] = step;
+    }
+  }
+}
+
 // TY terms of C, and of the pairs' operands; TS of B.
 template <bool BF16, int TY, int TS>
 __global__ void __launch_bounds__(256) ssm_keys(Plan p, bool, bool) {
   const SsmArgs& a = p.a;
-  constexpr int STRIDE = DK + 2;        // rows 8 apart start 16 banks apart
+  constexpr int STRIDE = DK + (DK == 32 ? 4 : 2);       // rows 8 apart start 16 or 32 banks apart
   __shared__ __attribute__((aligned(16))) float rows[2][Q][STRIDE];   // B, C
-  constexpr int PSTRIDE = Q + 4;
-  __shared__ __attribute__((aligned(16))) float squares[2][Q][PSTRIDE];
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int channels = a.C - 2 * a.H * DK;      // of x
+  static_assert(sizeof(rows) >= sizeof(float) * kHeads * (Q + 1), "dt where B and C are otherwise");
+  if (blockIdx.x >= p.key_blocks + p.window_blocks) {
+    const int tiles = (a.HV + kHeads - 1) / kHeads;
+    const int i = blockIdx.x - p.key_blocks - p.window_blocks;
+    set_steps(p, i / tiles, i % tiles * kHeads, reinterpret_cast<float (&)[kHeads][Q + 1]>(rows));
+    return;
+  }
   if (blockIdx.x >= p.key_blocks) {
     // windows of x, which ssm_scan finds in the workspace
     const int blocks = (channels + 255) / 256;
@@ -282,23 +327,6 @@ __global__ void __launch_bounds__(256) ssm_keys(Plan p, bool, bool) {
     set_window<BF16>(p, range, u.b, slot, channels + tid / DK * a.H * DK + h * DK + tid % DK, false);
 
   const int64_t here = static_cast<int64_t>(range.t0 / Q) + u.b + u.i;
-  // steps and decays of the group's heads, one per half wave
-  for (int i = 0; i < a.G; i += 8) {
-    const int hv = h * a.G + min(i + tid / Q, a.G - 1), t = tid % Q;
-    const int64_t at = static_cast<int64_t>(range.t0) + begin + min(t, valid - 1);
-    const float step = t < valid ? softplus_f(a.dt[at * a.HV + hv] + a.dt_bias[hv]) : 0.0f;
-    const double g = static_cast<double>(step) * static_cast<double>(-exp_f(a.a_log[hv])) * 1.4426950408889634;
-    const double c = running_sum(g);
-    const float part = static_cast<float>(c);
-    if (i + tid / Q >= a.G) continue;
-    Steps& to = p.steps[here * a.HV + hv];
-    to.hi[t] = part;
-    to.lo[t] = static_cast<float>(c - static_cast<double>(part));
-    to.decay[t] = __builtin_amdgcn_exp2f(static_cast<float>(g));
-    to.from[t] = __builtin_amdgcn_exp2f(part);
-    to.step[t] = step;
-  }
-
   Keys& out = p.keys[here * a.H + h];
   const int col = lane % 16, quad = lane / 16;
   for (int tile = wave; tile < kKeyTiles; tile += 4) {
@@ -336,6 +364,10 @@ __global__ void __launch_bounds__(256) ssm_keys(Plan p, bool, bool) {
     }
   }
   // rows t, columns s -> operand order, and the sum of both waves, through LDS
+  constexpr int PSTRIDE = Q + 4;
+  static_assert(sizeof(rows) >= sizeof(float) * 2 * Q * PSTRIDE, "the pairs where B and C were");
+  auto& squares = reinterpret_cast<float (&)[2][Q][PSTRIDE]>(rows);
+  __syncthreads();
 #pragma unroll
   for (int st = 0; st < 2; ++st)
 #pragma unroll
@@ -818,6 +850,17 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(M
     convolve(past);
     store_steps(sh.steps[wave][next / Q % 2]);
     if constexpr (MODE != kSegment) stage_c.store(&sh.c[0][0][0][0]);
+    if constexpr (MODE == kSegment) {
+      // Each product followed by its share of the convolution (16384 tokens x
+      // 32 heads 64 -> 61 us; with outputs there is enough else to do, and the
+      // compiler's own order is better: 541 against 617 us at 8 x 2048 x 96).
+      constexpr int kProducts = kKeyTiles * NT * (TS == 3 ? 6 : 3), kOther = 220;
+#pragma unroll
+      for (int i = 0; i < kProducts; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x2, (kOther + kProducts - 1) / kProducts, 0);
+      }
+    }
   }
 
   if (!works) return;
@@ -893,9 +936,8 @@ hipError_t scan(const Plan& plan, bool state_bf16, bool v_first, hipStream_t str
 template <bool BF16, int TY, int TS>
 hipError_t run(const Plan& plan, bool state_bf16, bool v_first, hipStream_t stream) {
   void* kargs[] = {const_cast<Plan*>(&plan), &state_bf16, &v_first};
-  const uint32_t window_blocks = static_cast<uint32_t>(plan.a.B) * ((plan.a.HV * DV + 255) / 256);
   hipError_t rc = hipLaunchKernel(reinterpret_cast<const void*>(&ssm_keys<BF16, TY, TS>),
-                                  dim3(plan.key_blocks + window_blocks), dim3(256), kargs, 0, stream);
+                                  dim3(plan.key_blocks + plan.window_blocks + plan.step_blocks), dim3(256), kargs, 0, stream);
   if (rc != hipSuccess) return rc;
   if (plan.segment == 0) return scan<BF16, TY, TS, kWhole>(plan, state_bf16, v_first, stream);
   rc = scan<BF16, TY, TS, kSegment>(plan, state_bf16, v_first, stream);
@@ -923,6 +965,8 @@ int launch_ssm_prefill_of<DK, DV>(const SsmArgs& args, bool bf16, bool state_bf1
   const int64_t waves = static_cast<int64_t>(args.HV) * (DV > 64 ? 2 : 1);
   plan.units = args.B;
   plan.key_blocks = static_cast<uint32_t>(chunks * args.H);
+  plan.window_blocks = static_cast<uint32_t>(args.B) * ((args.HV * DV + 255) / 256);
+  plan.step_blocks = static_cast<uint32_t>(chunks * ((args.HV + kHeads - 1) / kHeads));
   const int64_t most = KDA_SSM_SPLIT / waves;       // segments that the workspace has room for, beyond one a request
   if (args.B * waves < 512 && most >= 2) {
     int64_t length = (args.T + most - 1) / most;

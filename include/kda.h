@@ -407,8 +407,9 @@ int kda_verify(const kda_tensor* n_commit, const kda_tensor* next_token, const k
  *   state_layout  enum kda_state_layout.
  * H is (C - HV*dv) / (2*dk) and must divide HV.  dk and dv must each be 32,
  * 64 or 128 (KDA_ERR_UNSUPPORTED); T, N and B stay below 2^31 - 64, B * HV
- * below 2^21, C below 2^22, B * C below 2^31, and for prompts (T / 32 + B) * H
- * below 2^23 and B * C at most 2^29 (KDA_ERR_UNSUPPORTED).  Data
+ * below 2^21, C below 2^22, B * C below 2^31, and for prompts (T / 32 + B) *
+ * (H + HV / 32, rounded up) below 2^23 and B * C at most 2^29
+ * (KDA_ERR_UNSUPPORTED).  Data
  * are 16-byte aligned.  Preconditions, conventions (a negative index skips a
  * request: zero rows in out, state and window kept; an empty request changes
  * nothing) and errors are those of kda_decode.
