@@ -49,7 +49,7 @@ constexpr int Q = kSsmChunk;
 constexpr int kKeySteps = DK / 32;      // matrix steps of 32 over the keys
 constexpr int kKeyTiles = DK / 16;
 constexpr int kMostTerms = 3;
-constexpr int kMinSegment = 256;        // tokens
+constexpr int kMinSegment = 64;         // tokens
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -535,6 +535,10 @@ __device__ __forceinline__ constexpr uint64_t lanes_from(int mt, int j) {
   return lanes;
 }
 
+// Waves per SIMD.
+template <int MODE>
+constexpr int kResident = MODE == kSegment || DK <= 64 ? 3 : 2;
+
 // Half a fragment of M[t][s] = (C_t.B_s) exp(c_t - c_s) step_s, the lane's
 // tokens t = 16 mt + col and s = 8 quad + 4 half + 0 .. 3 (mt and half are the
 // wave's); zero for s > t.  The factors exp(c_t - c_s) are taken from the last
@@ -566,7 +570,7 @@ __device__ __forceinline__ void decayed_pairs(const Steps& of, f32x4 pairs, floa
 }
 
 template <bool BF16, bool FULL, int TY, int TS, int MODE>
-__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(MODE == kSegment ? 3 : 2, MODE == kSegment ? 3 : 2))) ssm_scan(Plan p, bool state_bf16, bool v_first) {
+__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(kResident<MODE>, kResident<MODE>))) ssm_scan(Plan p, bool state_bf16, bool v_first) {
   const SsmArgs& a = p.a;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   Shared<TY, TS>& sh = *reinterpret_cast<Shared<TY, TS>*>(lds);
@@ -950,6 +954,20 @@ hipError_t run(const Plan& plan, bool state_bf16, bool v_first, hipStream_t stre
   return scan<BF16, TY, TY, kJoined>(plan, state_bf16, v_first, stream);
 }
 
+// Whether requests are split into segments, which costs a second pass over
+// them and two more launches, for waves of 64 columns per request.  By the
+// waves that the batch has without (whole / split, us; dk = 128, dv = 64, 2000
+// tokens each: 64 heads x 2 requests 213 / 98, x 4 219 / 224, x 6 223 / 326;
+// lengths of 1 .. 4000 x 4 384 / 197, x 8 409 / 472; dk = 64, 2000 tokens x 4
+// 197 / 149), and by the tokens: 32 heads, one request of 200 tokens 36 / 33,
+// 512 64 / 41, 1024 99 / 44.  The longest request is not known here: with
+// enough tokens in all there may be a long one.  Segments of at least
+// 64 / 128 / 256 tokens: 512 tokens 41 / 43 / 60, 2048 55 / 50 / 66, 4 x 500
+// 57 / 62 / 70.
+bool splits(const SsmArgs& args, int64_t waves) {
+  return args.B * waves <= 160 * kResident<kJoined> && (args.T / args.B >= 192 || args.T >= 1024);
+}
+
 }  // namespace
 
 template <>
@@ -967,8 +985,9 @@ int launch_ssm_prefill_of<DK, DV>(const SsmArgs& args, bool bf16, bool state_bf1
   plan.key_blocks = static_cast<uint32_t>(chunks * args.H);
   plan.window_blocks = static_cast<uint32_t>(args.B) * ((args.HV * DV + 255) / 256);
   plan.step_blocks = static_cast<uint32_t>(chunks * ((args.HV + kHeads - 1) / kHeads));
-  const int64_t most = KDA_SSM_SPLIT / waves;       // segments that the workspace has room for, beyond one a request
-  if (args.B * waves < 512 && most >= 2) {
+  // segments that the chip holds at once, beyond one a request
+  const int64_t most = KDA_SSM_SPLIT * kResident<kJoined> / 3 / waves;
+  if (splits(args, waves) && most >= 1) {
     int64_t length = (args.T + most - 1) / most;
     length = (length + Q - 1) / Q * Q;
     if (length < kMinSegment) length = kMinSegment;

@@ -49,7 +49,7 @@ MATMULS = {"split_bf16": KDA_MATMUL_SPLIT_BF16, "f32": KDA_MATMUL_F32}
 KDA_VERIFY_SEGMENT = 1024
 
 KDA_SSM_CHUNK = 32
-KDA_SSM_SPLIT = 1024
+KDA_SSM_SPLIT = 1536
 
 KDA_ACT_SIGMOID = 0
 KDA_ACT_SILU = 1

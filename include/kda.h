@@ -429,7 +429,7 @@ int kda_ssm_decode(const kda_tensor* out, const kda_tensor* xbc, const kda_tenso
  * convolved keys and their products per 32 tokens and group, the windows as
  * they were, and the states where a long request is split. */
 #define KDA_SSM_CHUNK 32
-#define KDA_SSM_SPLIT 1024
+#define KDA_SSM_SPLIT 1536
 #define KDA_SSM_WORKSPACE(T, B, H, HV, dk, dv, K)                                                   \
   (((int64_t)(T) / KDA_SSM_CHUNK + (B)) * ((H) * (96 * (int64_t)(dk) + 1024) + 160 * (int64_t)(HV)) + \
    (int64_t)(B) * ((K)-1) * ((int64_t)(HV) * (dv) + 2 * (int64_t)(H) * (dk)) +                      \
