@@ -1,16 +1,15 @@
 // kda_ssm_decode.hip - the selective state space scan token by token
 // (kda_ssm_decode), with its short causal convolution in front.
 //
-// ssm_decode: one workgroup per (request, value head, up to 64 value columns),
-// one wave per 16 of the columns.  A lane moves its state in 16-byte pieces of
-// the pool's own rows: value-first a wave holds 16 rows of dk keys, key-first
-// the rows of its share of the keys, whole.  The state is fetched once,
-// advanced through the request's tokens in fp32 and written once.  Per token
-// every thread convolves one to three of the head's channels (x) or its
-// group's (B and C), which meet in LDS, double-buffered so that one barrier
-// per token is enough.  C^T S is summed over the wave's lanes; key-first the
-// waves' parts are added behind the next token's barrier.  It sets the window
-// of its own channels of x.
+// ssm_decode: one workgroup of four waves (two for dv = 32) per (request, value
+// head).  A lane moves its state in 16-byte pieces of the pool's own rows:
+// value-first a wave holds its share of the rows of dk keys, key-first the rows
+// of its share of the keys.  The state is fetched once, advanced through the
+// request's tokens in fp32 and written once.  Per token every thread convolves
+// one to three of the head's channels (x) or its group's (B and C), which meet
+// in LDS, double-buffered so that one barrier per token is enough.  C^T S is
+// summed over the wave's lanes; key-first the waves' parts are added behind
+// the next token's barrier.  It sets the window of its own channels of x.
 // ssm_windows: behind it, the new windows of B and C.  Every head of a group
 // reads them, so no workgroup of the first kernel may write them.
 //
@@ -31,16 +30,14 @@ namespace {
 
 template <int DK, int DV, bool BF16, bool SBF16, bool VFIRST>
 struct Shape {
-  static constexpr int COLS = DV;                       // value columns of a workgroup
-  static constexpr int SLABS = DV / COLS;
-  static constexpr int WAVES = COLS < 64 ? 2 : 4;
-  static constexpr int OWN = COLS / WAVES;              // value-first: a wave's rows
+  static constexpr int WAVES = DV < 64 ? 2 : 4;
+  static constexpr int OWN = DV / WAVES;                // value-first: a wave's rows
   static constexpr int THREADS = WAVES * kWave;
-  static constexpr int CHANNELS = COLS + 2 * DK;        // convolved by a workgroup: x, B, C
+  static constexpr int CHANNELS = DV + 2 * DK;          // convolved by a workgroup: x, B, C
   static constexpr int PER = (CHANNELS + THREADS - 1) / THREADS;
   static constexpr int ELEM = SBF16 ? 2 : 4;
   static constexpr int VEC = 16 / ELEM;                 // values per piece
-  static constexpr int LANES = (VFIRST ? DK : COLS) / VEC;  // of a row
+  static constexpr int LANES = (VFIRST ? DK : DV) / VEC;    // of a row
   static constexpr int STEP = kWave / LANES;            // rows of a wave's piece
   static constexpr int R = (VFIRST ? OWN : DK / WAVES) / STEP;   // pieces per lane
   static_assert(R >= 1, "rows of a wave");
@@ -52,20 +49,18 @@ __global__ void __launch_bounds__((Shape<DK, DV, BF16, SBF16, VFIRST>::THREADS))
   using IO = StateIO<SBF16, S::VEC>;
   constexpr int R = S::R, PER = S::PER, VEC = S::VEC;
   __shared__ __attribute__((aligned(16))) float conv[2][S::CHANNELS];
-  __shared__ float parts[2][VFIRST ? 1 : S::WAVES][VFIRST ? 1 : S::COLS];
+  __shared__ float parts[2][VFIRST ? 1 : S::WAVES][VFIRST ? 1 : DV];
 
-  const int slab = blockIdx.x % S::SLABS;
-  const int head = blockIdx.x / S::SLABS;
-  const int hv = head % a.HV, b = head / a.HV;
+  const int hv = blockIdx.x % a.HV, b = blockIdx.x / a.HV;
   const Range range = request_range(a, b);
   if (range.n == 0) return;
   const int tid = threadIdx.x, lane = tid % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int slot = request_slot(a, b);
   const int64_t out_row = static_cast<int64_t>(a.HV) * DV;
-  int64_t out_at = static_cast<int64_t>(range.t0) * out_row + static_cast<int64_t>(hv) * DV + slab * S::COLS;
+  int64_t out_at = static_cast<int64_t>(range.t0) * out_row + static_cast<int64_t>(hv) * DV;
   if (slot < 0) {
-    for (int i = tid; i < S::COLS; i += S::THREADS)
+    for (int i = tid; i < DV; i += S::THREADS)
       for (int t = 0; t < range.n; ++t) store_scalar<BF16>(a.out, out_at + t * out_row + i, 0.0f);
     return;
   }
@@ -78,7 +73,7 @@ __global__ void __launch_bounds__((Shape<DK, DV, BF16, SBF16, VFIRST>::THREADS))
   const int64_t tile = (static_cast<int64_t>(slot) * a.HV + hv) * DK * DV;
   const __amdgpu_buffer_rsrc_t pool =
       tile_resource(static_cast<char*>(a.state_pool) + tile * S::ELEM, DK * DV * S::ELEM);
-  const int voff = (row0 * WIDTH + col + slab * S::COLS * (VFIRST ? DK : 1)) * S::ELEM;
+  const int voff = (row0 * WIDTH + col) * S::ELEM;
   float s[R][VEC];
 #pragma unroll
   for (int i = 0; i < R; ++i) IO::load(pool, voff, i * S::STEP * WIDTH * S::ELEM, s[i]);
@@ -92,8 +87,8 @@ __global__ void __launch_bounds__((Shape<DK, DV, BF16, SBF16, VFIRST>::THREADS))
   for (int p = 0; p < PER; ++p) {
     const int i = tid + p * S::THREADS;
     const int keys = a.HV * DV + h * DK;
-    int c = i < S::COLS ? hv * DV + slab * S::COLS + i
-                        : (i < S::COLS + DK ? keys + (i - S::COLS) : keys + a.H * DK + (i - S::COLS - DK));
+    int c = i < DV ? hv * DV + i
+                        : (i < DV + DK ? keys + (i - DV) : keys + a.H * DK + (i - DV - DK));
     if (i >= S::CHANNELS) c = hv * DV;      // a channel of the head, convolved for nothing
     channel[p] = c;
   }
@@ -112,7 +107,7 @@ __global__ void __launch_bounds__((Shape<DK, DV, BF16, SBF16, VFIRST>::THREADS))
 
   // key-first: adds the waves' parts of the token before, whose x is `last`
   auto finish = [&](int t, float last) {
-    if (tid < S::COLS) {
+    if (tid < DV) {
       float sum = 0.0f;
 #pragma unroll
       for (int w = 0; w < S::WAVES; ++w) sum += parts[t & 1][VFIRST ? 0 : w][VFIRST ? 0 : tid];
@@ -129,7 +124,7 @@ __global__ void __launch_bounds__((Shape<DK, DV, BF16, SBF16, VFIRST>::THREADS))
     if (t % kWave == 0) {
       const int64_t at = static_cast<int64_t>(range.t0) + min(t + lane, range.n - 1);
       steps = softplus_f(a.dt[at * a.HV + hv] + bias);
-      decays = exp_f(-amp * steps);
+      decays = steps > 0.0f ? exp_f(-amp * steps) : 1.0f;       // without a step nothing decays, whatever a_log
     }
     const float step = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(steps), t % kWave));
     const float decay = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(decays), t % kWave));
@@ -152,7 +147,7 @@ __global__ void __launch_bounds__((Shape<DK, DV, BF16, SBF16, VFIRST>::THREADS))
     }
     __syncthreads();
     const float* const x = buf;
-    const float* const kb = buf + S::COLS;
+    const float* const kb = buf + DV;
     const float* const kc = kb + DK;
     if constexpr (VFIRST) {
       float bk[VEC], ck[VEC], y[R];
@@ -215,7 +210,7 @@ __global__ void __launch_bounds__((Shape<DK, DV, BF16, SBF16, VFIRST>::THREADS))
     __syncthreads();
     finish(range.n - 1, last);
   }
-  if (tid < S::COLS) {        // a thread's first channel is of x where it has one
+  if (tid < DV) {        // a thread's first channel is of x where it has one
 #pragma unroll
     for (int j = 0; j < kPast; ++j) {
       const int r = j - (kTaps - a.K);
@@ -244,13 +239,27 @@ __global__ void __launch_bounds__(256) ssm_windows(SsmArgs a, uint32_t keys) {
   for (int j = 0; j < a.K - 1; ++j) win[static_cast<int64_t>(j) * a.C] = x[j];
 }
 
+// LDS that nothing uses holds a CU to three workgroups, so that it mixes the
+// reads and writes of fewer states.  No claim / 38000 / 50000 bytes, dk = 128,
+// dv = 64, fp32 pool, one token, us:
+//   64 heads x 256 requests, key-first 200 / 197 / 195, value-first 203 / 202 / 198
+//   x 128 103 / 100 / 101, x 64 52.4 / 53.2 / 53.7, x 32 28.5 / 29.4 / 30.5
+// and not where a workgroup has more to do: 256 requests x 2 tokens
+// 202 / 197 / 211, x 4 196 / 212 / 245; dv = 128 190 / 191 / 186 and
+// value-first 190 / 189 / 190; a bf16 pool 107 / 109 / 130.
+template <int DK, int DV, bool SBF16>
+uint32_t idle_lds(const SsmArgs& args, uint32_t blocks) {
+  return !SBF16 && DK == 128 && DV == 64 && args.T <= args.B && blocks >= 8192 ? 50000 : 0;
+}
+
 template <int DK, int DV, bool BF16, bool SBF16, bool VFIRST>
 hipError_t launch(const SsmArgs& args, hipStream_t stream) {
   using S = Shape<DK, DV, BF16, SBF16, VFIRST>;
   void* kargs[] = {const_cast<SsmArgs*>(&args)};
-  const uint32_t blocks = static_cast<uint32_t>(args.B) * static_cast<uint32_t>(args.HV) * S::SLABS;
+  const uint32_t blocks = static_cast<uint32_t>(args.B) * static_cast<uint32_t>(args.HV);
   hipError_t rc = hipLaunchKernel(reinterpret_cast<const void*>(&ssm_decode<DK, DV, BF16, SBF16, VFIRST>),
-                                  dim3(blocks), dim3(S::THREADS), kargs, 0, stream);
+                                  dim3(blocks), dim3(S::THREADS), kargs,
+                                  idle_lds<DK, DV, SBF16>(args, blocks), stream);
   if (rc != hipSuccess) return rc;
   uint32_t keys = 2 * static_cast<uint32_t>(args.H) * DK;
   void* wargs[] = {const_cast<SsmArgs*>(&args), &keys};

@@ -224,3 +224,91 @@ def test_large_values_stay_finite():
     case.pool *= np.float32(1e30)
     run(case, "prefill")
     run(case, "decode")
+
+
+@pytest.mark.parametrize("entry", ["decode", "prefill"])
+def test_decays_of_nothing_left(entry):
+    """exp(a_log) beyond fp32, and steps from none to large: factors of zero and one, nothing undefined."""
+    case = Case(14, [40, 3], H=1, HV=4, dk=32, dv=32, bf16=False)
+    case.a_log[:] = (100.0, -100.0, 2.0, 50.0)
+    case.dt[5] = 1e4
+    case.dt[9] = -1e4
+    case.dt[9, 0] = case.dt[9, 3] = 0.0       # (infinity times no step has no value)
+    run(case, entry)
+
+
+@pytest.mark.parametrize("dv", [32, 64, 128])
+def test_captured_fp32_of_128_keys(dv):
+    """The operands that take the most LDS."""
+    case = Case(15, [700, 33], H=1, HV=2, dk=128, dv=dv, bf16=False)
+    t, eager = case.tensors(DEVICE), case.tensors(DEVICE)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):       # the first call of this form in the process, if run alone
+        call(case, t, "prefill")
+    for replay in range(3):
+        graph.replay()
+        call(case, eager, "prefill")
+        torch.cuda.synchronize()
+        if replay == 0:
+            case.check(eager, True)
+        for n in ("out", "state_pool", "conv_win"):
+            assert torch.equal(t[n], eager[n]), (replay, n)
+
+
+def test_rows_behind_the_last_request():
+    """Rows of out behind cu_seqlens' end are left."""
+    case = Case(16, [3, 50, 20], H=1, HV=2, dk=32, dv=32)
+    for entry in CALLS:
+        t = case.tensors(DEVICE)
+        t["cu_seqlens"] = t["cu_seqlens"][:3].clone()
+        t["state_indices"] = t["state_indices"][:2].clone()
+        call(case, t, entry)
+        torch.cuda.synchronize()
+        assert (t["out"][0, 53:] == 7).all()
+        o, mag, *_ = case.walk(1)
+        off = np.abs(t["out"][0, 3:53].float().cpu().numpy() - o) - 2.0 ** -8 * np.abs(o) - 2.0 ** -11 * mag
+        assert off.max() <= 0
+
+
+def test_same_results_again():
+    """Nothing depends on the order in which workgroups run."""
+    case = Case(17, [500, 900, 10], H=2, HV=4, dk=64, dv=64)
+    first = None
+    for _ in range(4):
+        t = case.tensors(DEVICE)
+        call(case, t, "prefill")
+        torch.cuda.synchronize()
+        got = [t[n] for n in ("out", "state_pool", "conv_win")]
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+def test_workspace_bounds():
+    """The workspace is enough and nothing outside it is written: guards on both sides stay."""
+    for lens, H, HV, dk, dv in (([1000, 1, 0, 77], 1, 2, 32, 32), ([64] * 9, 3, 6, 64, 128), ([2000], 1, 1, 128, 64)):
+        case = Case(18, lens, H=H, HV=HV, dk=dk, dv=dv)
+        t = case.tensors(DEVICE)
+        n = kda.ssm_prefill_workspace(case.T, case.B, H, HV, dk, dv, case.K)
+        buf = torch.full((n + 2048,), 3.25, device=DEVICE)
+        call(case, t, "prefill", workspace=buf[1024:1024 + n])
+        torch.cuda.synchronize()
+        case.check(t, True)
+        assert (buf[:1024] == 3.25).all() and (buf[1024 + n:] == 3.25).all()
+
+
+def test_refusals():
+    case = Case(19, [5], H=1, HV=2, dk=32, dv=32)
+    t = case.tensors(DEVICE)
+    for n, x in (("xbc", t["xbc"][..., :-1].contiguous()), ("dt", t["dt"][:, :4].contiguous()),
+                 ("conv_win", t["conv_win"][:, :2].contiguous()), ("state_pool", t["state_pool"].half()),
+                 ("out", t["out"].float()), ("conv_b", t["conv_b"].bfloat16())):
+        for entry in CALLS:
+            with pytest.raises((kda.KdaError, ValueError)):
+                call(case, dict(t, **{n: x}), entry)
+    for entry in CALLS:
+        with pytest.raises(ValueError, match="contiguous"):
+            call(case, dict(t, xbc=torch.cat([t["xbc"]] * 2, -1)[..., ::2]), entry)
+    with pytest.raises(ValueError, match="workspace"):
+        call(case, t, "prefill", stream=torch.cuda.current_stream().cuda_stream)
+    with pytest.raises(kda.KdaError):
+        call(case, t, "prefill", workspace=torch.empty(10, device=DEVICE))
