@@ -6,7 +6,9 @@
 
 ``kda.gdr_decode`` and ``kda.gdr_prefill`` run the gated delta rule with one decay
 per head, ``kda.decode_window`` a window of drafted tokens and ``kda.verify``
-decides which of them stand.
+decides which of them stand.  ``kda.ssm_decode`` and ``kda.ssm_prefill`` run the
+selective state space scan with its convolution, ``kda.norm_residual`` and
+``kda.norm_gate`` the norms before and after a block.
 
 ``workloads`` draws the seeded synthetic inputs; ``build`` compiles the
 library for gfx950.
