@@ -5,26 +5,36 @@
 // start, S0 the state before the chunk and x', B, C the convolved channels:
 //     y_t = exp(c_t) C_t^T S0 + sum_{s<=t} (C_t.B_s) exp(c_t - c_s) step_s x'_s + d_skip x'_t
 //     S   = exp(c_last) S0 + sum_s B_s (exp(c_last - c_s) step_s x'_s)^T
-// Every factor is at most one, so nothing overflows that the scan does not.
+// Every factor is at most one; what the scan does not form is C.B.
 //
 // ssm_keys, one workgroup per (chunk, group): convolves B and C, which all
 // heads of the group share, and leaves them and C.B in the order in which the
-// matrix instructions take them, in bf16 terms.  It also sets the windows.
-// ssm_scan, one wave per (request, value head, up to 64 value columns): walks
-// the chunks with the state in its accumulators.  The accumulators of two
-// 16-key tiles are the instruction's other operand for 32 keys in the order
-// that ssm_keys stores C in, and the pairs (C.B) arrive in operand order, so
-// no value moves between lanes.  It convolves its own columns of x.
+// matrix instructions take them, B and C in bf16 terms.  Further workgroups
+// make the steps and decays of 32 tokens and 32 heads, and set the windows.
+// ssm_scan, one wave per (request, value head, 32 value columns): walks the
+// chunks with the state in its accumulators.  The accumulators of two 16-key
+// tiles are the instruction's other operand for 32 keys in the order that
+// ssm_keys stores C in, so no value moves between lanes.  Four waves of a group
+// share the operands through LDS, and those of a head its factors of C.B; a
+// wave convolves its own columns of x.  Two barriers per chunk: behind one the
+// outputs, behind the other the update.
 // Where a batch has few heads for the chip, requests are split into segments:
 // ssm_scan (kSegment) runs all segments from a zero state, ssm_join passes
 // the states on, and ssm_scan (kJoined) runs the segments from there.
 //
 // Precision: an fp32 value is the sum of three bf16 terms, 8 bits each, taken
 // by truncation, so that no term leaves the value's range.  Products of three
-// terms each keep about 24 bits (six matrix instructions), of two about 16
-// (three): the state takes three for an fp32 pool or fp32 activations, and
-// what only reaches bf16 outputs or a bf16 pool takes two.  c is summed in
-// fp64 and kept in two fp32 parts: differences of large sums are what counts.
+// terms each are good to 2^-20 of what is added up (six matrix instructions;
+// measured 1.3e-7 on the state), of two to 2^-13 (three): the state takes three
+// for an fp32 pool or fp32 activations, and what only reaches bf16 outputs or
+// a bf16 pool takes two.  c is summed in fp64 and kept in two fp32 parts:
+// differences of large sums are what counts.
+//
+// Bound: vector instructions (splitting the state into terms every 32 tokens,
+// the convolution with its SiLU) and the clock under them; 8 x 2048 tokens over
+// 96 heads of 128 columns, bf16 pool: 534 us, of which ssm_keys 57 and ssm_scan
+// 475, vector units busy 64% of the cycles and matrix units 33%.  16384 tokens
+// over 32 heads of 64 columns: 168 us (keys 12, segments 57, join 15, joined 83).
 
 #include <hip/hip_runtime.h>
 
@@ -167,7 +177,8 @@ __device__ __forceinline__ f32x4 product(const u32x4 (&a)[N], const u32x4 (&b)[N
 // keys
 // ---------------------------------------------------------------------------
 
-// The new window of request b's channel c; `kept`, if given, takes the old one.
+// The new window of request b's channel c; the workspace keeps the old one if
+// `keep`.
 template <bool BF16>
 __device__ __forceinline__ void set_window(const Plan& p, const Range& range, int b, int slot, int c, bool keep) {
   const SsmArgs& a = p.a;
@@ -538,7 +549,9 @@ __device__ __forceinline__ constexpr uint64_t lanes_from(int mt, int j) {
   return lanes;
 }
 
-// Waves per SIMD.
+// Waves per SIMD, as their registers allow: 16384 tokens over 32 heads of 128
+// keys need 240 with outputs; at dk = 64 three waves took the ragged fp32
+// prompts from 122 to 111 us (with the shorter segments).
 template <int MODE>
 constexpr int kResident = MODE == kSegment || DK <= 64 ? 3 : 2;
 
@@ -563,8 +576,8 @@ __device__ __forceinline__ void decayed_pairs(const Steps& of, f32x4 pairs, floa
   for (int j = 3; j >= 0; --j) {
     const uint64_t reached = lanes(j), passed = lanes(j + 1);   // s <= t, s < t
     if (j < 3) f *= __builtin_amdgcn_inverse_ballot_w64(passed) ? decay[j + 1] : 1.0f;
-    x[j] = fmaf(pairs[j] * step[j], __builtin_amdgcn_inverse_ballot_w64(reached) ? f : 0.0f,
-                __builtin_amdgcn_inverse_ballot_w64(reached & ~passed) ? skip : 0.0f);
+    const float own = __builtin_amdgcn_inverse_ballot_w64(reached & ~passed) ? skip : 0.0f;
+    x[j] = __builtin_amdgcn_inverse_ballot_w64(reached) ? fmaf(pairs[j] * step[j], f, own) : 0.0f;
   }
   u32x2 term[TY];
   split<TY>(x, term);
@@ -573,7 +586,8 @@ __device__ __forceinline__ void decayed_pairs(const Steps& of, f32x4 pairs, floa
 }
 
 template <bool BF16, bool FULL, int TY, int TS, int MODE>
-__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(kResident<MODE>, kResident<MODE>))) ssm_scan(Plan p, bool state_bf16, bool v_first) {
+__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(kResident<MODE>, kResident<MODE>)))
+ssm_scan(Plan p, bool state_bf16, bool v_first) {
   const SsmArgs& a = p.a;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   Shared<TY, TS>& sh = *reinterpret_cast<Shared<TY, TS>*>(lds);
@@ -944,7 +958,8 @@ template <bool BF16, int TY, int TS>
 hipError_t run(const Plan& plan, bool state_bf16, bool v_first, hipStream_t stream) {
   void* kargs[] = {const_cast<Plan*>(&plan), &state_bf16, &v_first};
   hipError_t rc = hipLaunchKernel(reinterpret_cast<const void*>(&ssm_keys<BF16, TY, TS>),
-                                  dim3(plan.key_blocks + plan.window_blocks + plan.step_blocks), dim3(256), kargs, 0, stream);
+                                  dim3(plan.key_blocks + plan.window_blocks + plan.step_blocks), dim3(256), kargs, 0,
+                                  stream);
   if (rc != hipSuccess) return rc;
   if (plan.segment == 0) return scan<BF16, TY, TS, kWhole>(plan, state_bf16, v_first, stream);
   rc = scan<BF16, TY, TS, kSegment>(plan, state_bf16, v_first, stream);

@@ -227,6 +227,18 @@ def test_large_values_stay_finite():
 
 
 @pytest.mark.parametrize("entry", ["decode", "prefill"])
+@pytest.mark.parametrize("at", [5, 20, 40])
+def test_keys_of_later_tokens_stay_out(entry, at):
+    """C of a token times B of a later one leaves fp32; the scan never forms that product."""
+    case = Case(21, [50], H=1, HV=4, dk=32, dv=32, K=2, bf16=False, bias=False)
+    keys, read = case.HV * case.dv, case.HV * case.dv + case.dk
+    case.conv_w[:, keys:] = np.array([[0.0], [1.0]], dtype=np.float32)
+    case.xbc[at, keys:read] = 1e25
+    case.xbc[:at, read:] = 1e25
+    run(case, entry)
+
+
+@pytest.mark.parametrize("entry", ["decode", "prefill"])
 def test_decays_of_nothing_left(entry):
     """exp(a_log) beyond fp32, and steps from none to large: factors of zero and one, nothing undefined."""
     case = Case(14, [40, 3], H=1, HV=4, dk=32, dv=32, bf16=False)
