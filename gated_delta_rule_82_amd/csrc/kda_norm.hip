@@ -136,8 +136,12 @@ struct Row {
   }
 };
 
-// 1 / sqrt(mean(x^2) + eps) in two factors, their product the value; the
-// second is 1 unless the squares leave fp32.
+// 1 / sqrt(mean(x^2) + eps) in two factors, their product the value, the
+// first applied first; the second is 1 unless the squares leave fp32.  The
+// first of a value below one is below one itself: x may be anything up to
+// fp32's largest, and x * f must not pass it (a row of 128 with 3e38 alone has
+// the value 2^-125 * 1.604).  From one on x * f * g is at most sqrt(D), and f
+// is at least one, so that a small x keeps its bits.
 struct Factor {
   float f, g;
   __device__ __forceinline__ float operator()(float x) const { return x * f * g; }
@@ -160,7 +164,7 @@ __device__ __forceinline__ Factor norm_factor(const float (&x)[P][kVec], int D, 
   wide = Row<LANES>::sum(wide);
   const double r = 1.0 / sqrt(wide / D + static_cast<double>(eps));
   if (!(r > 0.0 && r < 1e300)) return {static_cast<float>(r), 1.0f};
-  const int e = min(max(ilogb(r), -126), 126);
+  const int e = min(max(ilogb(r) + (r < 1.0 ? 1 : 0), -126), 126);
   return {static_cast<float>(ldexp(r, -e)), ldexpf(1.0f, e)};
 }
 

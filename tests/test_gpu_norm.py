@@ -125,6 +125,34 @@ def test_sums_of_squares_beyond_fp32(size):
         residual(3, 600, False, False, False, None, size=size, eps=eps)
 
 
+@pytest.mark.parametrize("value", [1.8e38, -2.5e38, 3.3e38])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("D", [1, 16, 64, 128, 130, 512, 4096, 16384])
+def test_values_above_half_of_fp32(D, bf16, value):
+    """A value above 2^127 alone in its row, among ordinary ones, and beside its like: the row's factor must not
+    take it to infinity.  bf16 results below 2^-126 are multiples of 2^-133."""
+    gen = torch.Generator(device=DEVICE).manual_seed(D)
+    rows = draw(gen, 4, D, bf16=bf16)
+    rows[0] = 0
+    rows[0, D // 2] = rows[1, D // 3] = rows[2, 0] = value
+    rows[2, D - 1] = -value
+    small, w = draw(gen, 4, D, bf16=bf16), draw(gen, D, bf16=False)
+    tiny = 2.0 ** -134 if bf16 else 0.0
+    x = wide(rows)
+    z = torch.full_like(rows, 40.0)         # sigmoid is 1
+    for first in (False, True):
+        out = torch.empty_like(rows)
+        kda.norm_gate(out, rows, z, w, gate_first=first)
+        check(out, unit(x, 1e-5) * wide(w) * sigmoid(40.0), bf16, extra=tiny)
+    for hidden, block_out, post in ((rows, small, None), (small, rows, w)):
+        want_h, want_n, mag = residual_reference(hidden, block_out, w, post, None, 1e-5)
+        h_out, normed = torch.empty_like(hidden), torch.empty_like(block_out)
+        kda.norm_residual(h_out, normed, hidden, block_out, w, post_weight=post)
+        check(h_out, want_h, bf16, extra=UNITS * mag + tiny)
+        r = 1.0 / np.sqrt((want_h ** 2).mean(-1, keepdims=True) + 1e-5)
+        check(normed, want_n, bf16, extra=2 * (UNITS * mag + 2.0 ** -150) * r * np.abs(wide(w)) + tiny)
+
+
 def test_zero_rows():
     x = torch.zeros(4, 3, 64, device=DEVICE, dtype=torch.bfloat16)
     out = torch.ones_like(x)
