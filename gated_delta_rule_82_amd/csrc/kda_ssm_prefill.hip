@@ -246,9 +246,10 @@ __device__ __forceinline__ void set_steps(const Plan& p, int slot_at, int head0,
   for (int e = 0; e < EACH; ++e) {
     const float step = t < valid ? softplus_f(tile[part * EACH + e][t] + bias[e]) : 0.0f;
     // Without a step nothing decays, whatever a_log; a factor below 2^-10000
-    // is zero all the same, and keeps the sums finite.
+    // is zero all the same, and keeps the sums finite.  NaN stays NaN.
     const double rate = static_cast<double>(-exp_f(amp[e])) * 1.4426950408889634;
-    const double g = step > 0.0f ? fmax(step * rate, -1e4) : 0.0;
+    const double wide = step * rate;
+    const double g = step > 0.0f ? (wide < -1e4 ? -1e4 : wide) : 0.0;
     const double c = running_sum(g);
     const float high = static_cast<float>(c);
     if (head0 + part * EACH + e < a.HV) {

@@ -249,6 +249,27 @@ def test_decays_of_nothing_left(entry):
     run(case, entry)
 
 
+@pytest.mark.parametrize("entry,lens", [("decode", [3, 40]), ("prefill", [3, 40]), ("prefill", [1500, 40])])
+@pytest.mark.parametrize("which", ["a_log", "dt_bias"])
+def test_a_head_without_a_decay(entry, lens, which):
+    """NaN in a head's parameters is NaN in all its outputs and its state, and reaches no other head."""
+    case = Case(22, lens, H=1, HV=4, dk=32, dv=64, bf16=False, slots=[0, 1], extra_slots=0)
+    t = case.tensors(DEVICE)
+    t[which][2] = float("nan")
+    call(case, t, entry)
+    torch.cuda.synchronize()
+    assert torch.isnan(t["out"][0, :, 2]).all() and torch.isnan(t["state_pool"][:, 2]).all()
+    keep = [0, 1, 3]
+    for b in range(2):
+        o, mag, S, M, w = case.walk(b)
+        rows = slice(case.cu[b], case.cu[b + 1])
+        n = np.arange(1, lens[b] + 1)[:, None, None]
+        tol = (32 * (n + 1) * 2.0 ** -24 + 2 * 2.0 ** -20.4) * mag
+        assert (np.abs(t["out"][0, rows].cpu().numpy() - o) <= tol)[:, keep].all()
+        assert (np.abs(t["state_pool"][b].cpu().numpy() - S) <= (32 * lens[b] * 2.0 ** -24 + 2.0 ** -20.4) * M)[keep].all()
+        assert np.array_equal(t["conv_win"][b].cpu().numpy(), w.astype(np.float32))
+
+
 @pytest.mark.parametrize("dv", [32, 64, 128])
 def test_captured_fp32_of_128_keys(dv):
     """The operands that take the most LDS."""
