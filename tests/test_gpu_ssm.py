@@ -270,6 +270,20 @@ def test_a_head_without_a_decay(entry, lens, which):
         assert np.array_equal(t["conv_win"][b].cpu().numpy(), w.astype(np.float32))
 
 
+@pytest.mark.parametrize("entry", ["decode", "prefill"])
+@pytest.mark.parametrize("n", [50, 1500])
+@pytest.mark.parametrize("K", [2, 4])
+def test_taps_of_no_token(entry, n, K):
+    """A tap that would leave fp32 for a token behind the last meets nothing: there is no such token."""
+    case = Case(23, [n, 3], H=1, HV=2, dk=32, dv=32, K=K, bf16=False)
+    x = case.HV * case.dv
+    case.conv_w[K - 2, :x] = 1e30
+    case.xbc[:, :x] = 0
+    case.conv_win[:, :, :x] = 0
+    case.xbc[n - 1, :x] = 1e10
+    run(case, entry)
+
+
 @pytest.mark.parametrize("dv", [32, 64, 128])
 def test_captured_fp32_of_128_keys(dv):
     """The operands that take the most LDS."""
