@@ -59,7 +59,7 @@ constexpr int Q = kSsmChunk;
 constexpr int kKeySteps = DK / 32;      // matrix steps of 32 over the keys
 constexpr int kKeyTiles = DK / 16;
 constexpr int kMostTerms = 3;
-constexpr int kMinSegment = 64;         // tokens
+constexpr int kMinSegment = 64;         // tokens; KDA_SSM_WORKSPACE
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -995,8 +995,11 @@ hipError_t run(const Plan& plan, bool state_bf16, bool v_first, hipStream_t stre
 // enough tokens in all there may be a long one.  Segments of at least
 // 64 / 128 / 256 tokens: 512 tokens 41 / 43 / 60, 2048 55 / 50 / 66, 4 x 500
 // 57 / 62 / 70.
+constexpr int kSplitWaves = KDA_SSM_SPLIT / 16 * 5 * kResident<kJoined> / 3;
+static_assert(kSplitWaves * 64 <= KDA_SSM_SPLIT * 20, "a state per request in KDA_SSM_WORKSPACE");
+
 bool splits(const SsmArgs& args, int64_t waves) {
-  return args.B * waves <= 160 * kResident<kJoined> && (args.T / args.B >= 192 || args.T >= 1024);
+  return args.B * waves <= kSplitWaves && (args.T / args.B >= 192 || args.T >= 1024);
 }
 
 }  // namespace

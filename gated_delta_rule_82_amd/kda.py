@@ -525,7 +525,8 @@ SSM_NAMES = ("out", "xbc", "dt", "conv_w", "conv_b", "conv_win", "a_log", "dt_bi
 def ssm_prefill_workspace(T: int, B: int, H: int, HV: int, dk: int, dv: int, K: int) -> int:
     """Floats of :func:`ssm_prefill`'s workspace (KDA_SSM_WORKSPACE)."""
     return ((T // KDA_SSM_CHUNK + B) * (H * (96 * dk + 1024) + 160 * HV) + B * (K - 1) * (HV * dv + 2 * H * dk)
-            + (KDA_SSM_SPLIT * 64 + B * HV * dv) * dk + 2 * KDA_SSM_SPLIT + B * HV + 64)
+            + (min(T // 64 * HV * dv, KDA_SSM_SPLIT * 64) + min(B * HV * dv, KDA_SSM_SPLIT * 20)) * dk
+            + 2 * KDA_SSM_SPLIT + B * HV + 64)
 
 
 def ssm_decode(out, xbc, dt, conv_w, conv_b, conv_win, a_log, dt_bias, d_skip, cu_seqlens, state_pool,

@@ -426,14 +426,25 @@ int kda_ssm_decode(const kda_tensor* out, const kda_tensor* xbc, const kda_tenso
 
 /* Floats of kda_ssm_prefill's workspace, for the sizes of its arguments: the
  * convolved keys and their products per 32 tokens and group, the windows as
- * they were, and the states where a long request is split. */
+ * they were, and the states where long requests are split: of up to
+ * KDA_SSM_SPLIT pairs of a head and a segment (64 tokens or more), half as many
+ * of heads of more than 64 columns, and of one more segment per request.
+ * Batches of more than KDA_SSM_SPLIT / 16 * 5 heads in all, those of more than
+ * 64 columns counted twice, are not split, so the states take 63 MiB at most.
+ * The workspace grows with every size: one for the largest batch serves the
+ * smaller ones. */
 #define KDA_SSM_CHUNK 32
 #define KDA_SSM_SPLIT 1536
-#define KDA_SSM_WORKSPACE(T, B, H, HV, dk, dv, K)                                                   \
+#define KDA_SSM_WORKSPACE(T, B, H, HV, dk, dv, K)                                                     \
   (((int64_t)(T) / KDA_SSM_CHUNK + (B)) * ((H) * (96 * (int64_t)(dk) + 1024) + 160 * (int64_t)(HV)) + \
-   (int64_t)(B) * ((K)-1) * ((int64_t)(HV) * (dv) + 2 * (int64_t)(H) * (dk)) +                      \
-   ((int64_t)KDA_SSM_SPLIT * 64 + (int64_t)(B) * (HV) * (dv)) * (dk) + 2 * (int64_t)KDA_SSM_SPLIT + \
-   (int64_t)(B) * (HV) + 64)
+   (int64_t)(B) * ((K)-1) * ((int64_t)(HV) * (dv) + 2 * (int64_t)(H) * (dk)) +                        \
+   (KDA_SSM_SPLIT * 64 +                                                                              \
+    ((int64_t)(T) / 64 * (HV) * (dv) < KDA_SSM_SPLIT * 64) *                                          \
+        ((int64_t)(T) / 64 * (HV) * (dv)-KDA_SSM_SPLIT * 64) +                                        \
+    KDA_SSM_SPLIT * 20 +                                                                              \
+    ((int64_t)(B) * (HV) * (dv) < KDA_SSM_SPLIT * 20) * ((int64_t)(B) * (HV) * (dv)-KDA_SSM_SPLIT * 20)) * \
+       (int64_t)(dk) +                                                                                \
+   2 * (int64_t)KDA_SSM_SPLIT + (int64_t)(B) * (HV) + 64)
 
 /*
  * kda_ssm_prefill - the same operation for whole prompts, in chunks of 32

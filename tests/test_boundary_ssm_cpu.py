@@ -99,6 +99,23 @@ def test_ssm_workspace():
         assert int(re.search(rf"#define {name} (\d+)", header).group(1)) == getattr(kda, name)
 
 
+def test_ssm_workspace_is_bounded():
+    """States of split requests: 63 MiB at most and no more than the tokens need; no smaller batch needs more."""
+    def rest(T, B, H, HV, dk, dv, K):
+        return (T // 32 + B) * (H * (96 * dk + 1024) + 160 * HV) + B * (K - 1) * (HV * dv + 2 * H * dk) + B * HV
+    for sizes in ((256 * 700, 256, 8, 96, 128, 128, 4), (256, 256, 1, 64, 128, 64, 4), (16384, 1, 1, 32, 128, 64, 4),
+                  (10 ** 6, 3, 1, 64, 128, 128, 2)):
+        assert (kda.ssm_prefill_workspace(*sizes) - rest(*sizes)) * 4 <= (63 << 20) + 4 * 2 ** 12, sizes
+    assert kda.ssm_prefill_workspace(117, 1, 1, 32, 128, 64, 4) * 4 < 4 << 20
+    most = (5000, 9, 4, 16, 128, 128, 4)
+    largest = kda.ssm_prefill_workspace(*most)
+    for T in (0, 1, 63, 64, 1000, 4999):
+        for B in (1, 2, 5, 9):
+            for HV in (4, 8, 16):
+                for d in (32, 64, 128):
+                    assert kda.ssm_prefill_workspace(T, B, 4, HV, d, d, 3) <= largest
+
+
 def residual_descriptors(rows=(3, 5), D=64, scale=None):
     shapes = {"hidden_out": (F32, (*rows, D)), "normed": (BF16, (*rows, D)), "hidden": (F32, (*rows, D)),
               "block_out": (BF16, (*rows, D)), "weight": (F32, (D,)), "post_weight": (F32, (D,)),

@@ -343,6 +343,19 @@ def test_workspace_bounds():
         assert (buf[:1024] == 3.25).all() and (buf[1024 + n:] == 3.25).all()
 
 
+@pytest.mark.parametrize("lens", [[300, 200, 210, 190, 130], [300, 200, 210, 190, 130, 1]])
+def test_workspace_where_splitting_ends(lens):
+    """The largest batch of 96 heads that is split, and one request more, between guards."""
+    case = Case(25, lens, H=1, HV=96, dk=32, dv=32)
+    t = case.tensors(DEVICE)
+    n = kda.ssm_prefill_workspace(case.T, case.B, 1, 96, 32, 32, 4)
+    buf = torch.full((n + 2048,), 3.25, device=DEVICE)
+    call(case, t, "prefill", workspace=buf[1024:1024 + n])
+    torch.cuda.synchronize()
+    case.check(t, True)
+    assert (buf[:1024] == 3.25).all() and (buf[1024 + n:] == 3.25).all()
+
+
 def test_refusals():
     case = Case(19, [5], H=1, HV=2, dk=32, dv=32)
     t = case.tensors(DEVICE)
