@@ -15,7 +15,7 @@
 //
 // Bound: HBM, the state's way in and out: 256 requests of 64 heads (dk = 128,
 // dv = 64, fp32 pool, 1.1 GB moved) 195 us, 5.7 TB/s; one request of 64 heads
-// is bound by latency, 7.7 us for both kernels.
+// is bound by latency, 6.7 us in the two kernels.
 
 #include <hip/hip_runtime.h>
 
@@ -242,16 +242,20 @@ __global__ void __launch_bounds__(256) ssm_windows(SsmArgs a, uint32_t keys) {
 }
 
 // LDS that nothing uses holds a CU to three workgroups, so that it mixes the
-// reads and writes of fewer states.  No claim / 38000 / 50000 bytes, dk = 128,
-// dv = 64, fp32 pool, one token, us:
-//   64 heads x 256 requests, key-first 200 / 197 / 195, value-first 203 / 202 / 198
-//   x 128 103 / 100 / 101, x 64 52.4 / 53.2 / 53.7, x 32 28.5 / 29.4 / 30.5
-// and not where a workgroup has more to do: 256 requests x 2 tokens
-// 202 / 197 / 211, x 4 196 / 212 / 245; dv = 128 190 / 191 / 186 and
-// value-first 190 / 189 / 190; a bf16 pool 107 / 109 / 130.
+// reads and writes of fewer states.  No claim / 50000 bytes, fp32 pool, one
+// token for each of 256 requests of 64 heads, us:
+//   dk = 128, dv = 64 key-first 201 / 195, value-first 202 / 198;
+//   64 x 128 200 / 194, 203 / 201; 128 x 128 358 / 347, 358 / 359
+//   128 requests 101 / 101, 103 / 101; 102 / 101, 102 / 102; 182 / 178, 182 / 184
+//   64 requests (128 x 64, key-first) 52.4 / 53.7, 32 requests 28.5 / 30.5.
+// Smaller states lose: 64 x 64 104 / 102, 105 / 106; a bf16 pool's 108 / 130.
+// So do workgroups with more to do, 256 requests x 2 tokens 203 / 213, and
+// batches of long windows among empty requests, 4 tokens for every fourth of
+// 256 59 / 72.  Lengths are not known here: as many tokens as requests are taken
+// for one each.
 template <int DK, int DV, bool SBF16>
 uint32_t idle_lds(const SsmArgs& args, uint32_t blocks) {
-  return !SBF16 && DK == 128 && DV == 64 && args.T <= args.B && blocks >= 8192 ? 50000 : 0;
+  return !SBF16 && DK * DV >= 128 * 64 && args.T == args.B && blocks >= 8192 ? 50000 : 0;
 }
 
 template <int DK, int DV, bool BF16, bool SBF16, bool VFIRST>

@@ -39,6 +39,13 @@ def test_decode(dk, dv, bf16, state_bf16, layout):
         "decode")
 
 
+@pytest.mark.parametrize("lens,dk,dv,HV,layout", [([1] * 128, 128, 64, 64, "k_first"), ([0, 2] * 128, 64, 128, 32, "v_first"),
+                                                  ([3, 0, 0, 1] * 32, 128, 128, 64, "k_first")])
+def test_decode_of_a_full_batch(lens, dk, dv, HV, layout):
+    """As many tokens as requests and workgroups enough for the launch of full batches, one token each or not."""
+    run(Case(24, lens, H=1, HV=HV, dk=dk, dv=dv, layout=layout), "decode")
+
+
 @pytest.mark.parametrize("layout,state_bf16,bf16", [("k_first", False, True), ("v_first", True, True),
                                                     ("v_first", False, False), ("k_first", True, False)])
 @pytest.mark.parametrize("dk,dv", SIZES)
