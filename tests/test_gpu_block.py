@@ -83,6 +83,11 @@ def test_prompt_and_tokens(lens, cut):
     case.check(dict(t, out=out), True)
 
 
+def test_prompt_and_tokens_of_split_requests():
+    """A prompt long enough to run in segments, beside a short one and then token by token."""
+    test_prompt_and_tokens([1200, 40], [1197, 38])
+
+
 def test_captured_step():
     """A block's token step, captured and replayed, is the eager one, replay after replay."""
     b = Block([1, 1, 1], seed=5)

@@ -81,6 +81,16 @@ def test_split_requests(lens, bf16, state_bf16, layout, dk, dv):
     run(Case(len(lens), lens, H=1, HV=2, dk=dk, dv=dv, bf16=bf16, state_bf16=state_bf16, layout=layout), "prefill")
 
 
+@pytest.mark.parametrize("K", [2, 3, 4])
+@pytest.mark.parametrize("H,HV,dk,dv,bf16,state_bf16,layout", [
+    (2, 6, 64, 64, False, False, "v_first"), (4, 4, 32, 128, True, False, "k_first"),
+    (3, 6, 128, 32, True, True, "v_first"), (2, 2, 128, 128, False, True, "k_first")])
+def test_split_requests_forms(H, HV, dk, dv, bf16, state_bf16, layout, K):
+    """Segments and their join with several groups, fewer taps, slots that are skipped and no skip connection."""
+    run(Case(K + H, [1100, 40, 0, 333, 65], H=H, HV=HV, dk=dk, dv=dv, K=K, bf16=bf16, state_bf16=state_bf16,
+             w_bf16=bf16, layout=layout, skip=False, bias=K != 3, slots=[3, -1, 0, 6, 9]), "prefill")
+
+
 @pytest.mark.parametrize("entry", ["decode", "prefill"])
 @pytest.mark.parametrize("decay", [1e-4, 30.0, 300.0])
 def test_decays(entry, decay):
