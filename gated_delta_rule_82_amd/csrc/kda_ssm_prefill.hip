@@ -264,7 +264,7 @@ __device__ __forceinline__ void set_steps(const Plan& p, int slot_at, int head0,
 
 // TY terms of C, and of the pairs' operands; TS of B.
 template <bool BF16, int TY, int TS>
-__global__ void __launch_bounds__(256) ssm_keys(Plan p, bool, bool) {
+__global__ void __launch_bounds__(256) ssm_keys(Plan p) {
   const SsmArgs& a = p.a;
   constexpr int STRIDE = DK + (DK == 32 ? 4 : 2);       // rows 8 apart start 16 or 32 banks apart
   __shared__ __attribute__((aligned(16))) float rows[2][Q][STRIDE];   // B, C
@@ -969,7 +969,7 @@ hipError_t scan(const Plan& plan, bool state_bf16, bool v_first, hipStream_t str
 
 template <bool BF16, int TY, int TS>
 hipError_t run(const Plan& plan, bool state_bf16, bool v_first, hipStream_t stream) {
-  void* kargs[] = {const_cast<Plan*>(&plan), &state_bf16, &v_first};
+  void* kargs[] = {const_cast<Plan*>(&plan), &state_bf16, &v_first};      // ssm_keys takes the first alone
   hipError_t rc = hipLaunchKernel(reinterpret_cast<const void*>(&ssm_keys<BF16, TY, TS>),
                                   dim3(plan.key_blocks + plan.window_blocks + plan.step_blocks), dim3(256), kargs, 0,
                                   stream);
