@@ -409,9 +409,9 @@ int kda_verify(const kda_tensor* n_commit, const kda_tensor* next_token, const k
  * 64 or 128 (KDA_ERR_UNSUPPORTED); T, N and B stay below 2^31 - 64, B * HV
  * below 2^21, C below 2^22, B * C below 2^31, and for prompts (T / 32 + B) *
  * (H + HV / 32, rounded up) below 2^23 and B * C at most 2^29
- * (KDA_ERR_UNSUPPORTED).  Data are 16-byte aligned.  Preconditions, conventions (a negative index skips a
- * request: zero rows in out, state and window kept; an empty request changes
- * nothing) and errors are those of kda_decode.
+ * (KDA_ERR_UNSUPPORTED).  Data are 16-byte aligned.  Preconditions, conventions
+ * (a negative index skips a request: zero rows in out, state and window kept; an
+ * empty request changes nothing) and errors are those of kda_decode.
  */
 
 /*
@@ -451,11 +451,16 @@ int kda_ssm_decode(const kda_tensor* out, const kda_tensor* xbc, const kda_tenso
  * tokens on the matrix cores; the result equals the token-by-token scan up to
  * rounding order.  Operands are split into bf16 terms without loss of range:
  * three terms for an fp32 pool's state and for f32 outputs (a product is good
- * to 2^-20), two for bf16 pools and outputs of a bf16 call (2^-13).  Errors
- * are relative to the sum of the magnitudes of what is added up.  Where the
- * scan has an infinity or NaN, this call may have NaN, and from up to 31
- * tokens earlier of the same request; so it may where C^T B of a token and one
- * before it, which the scan does not form, leaves fp32.
+ * to 2^-20), two for bf16 pools and outputs of a bf16 call (2^-13, of which an
+ * output passes two; a split bf16 call on an f32 pool takes two for the states
+ * inside segments too, which only reach outputs, so that these depend within
+ * that on whether the batch is split).  Callers that want three throughout pass
+ * xbc and out in f32.  Errors are relative to the sum of the magnitudes of what
+ * is added up.  Where the scan has an infinity or NaN, this call may have NaN,
+ * and from up to 31 tokens earlier of the same request; so it may where a
+ * product that the scan does not form leaves fp32: C of a token with B (times
+ * its step) of one up to 31 tokens before it, or with the state up to 32 tokens
+ * before it, whatever the decays in between leave of it.
  *   workspace     [>= KDA_SSM_WORKSPACE(...)]  f32; its contents before and
  *                 after mean nothing.  Calls that may run at the same time
  *                 need one each.
@@ -485,8 +490,9 @@ int kda_ssm_prefill(const kda_tensor* out, const kda_tensor* xbc, const kda_tens
  *   scale               [D] or [1] f32; NULL: one.
  *   eps                 finite, >= 0; 0 selects 1e-5.
  * Leading dimensions may be up to three (row-major); D is the last, 1 to
- * KDA_NORM_MAX, and rows times D rounded up to 64, 128 or a multiple of 512
- * below 2^35 (KDA_ERR_UNSUPPORTED).
+ * KDA_NORM_MAX, and rows, rounded up to a multiple of 32, times D, rounded up to
+ * 64, 128 or a multiple of 512 (of 1024 beyond 8192), below 2^35
+ * (KDA_ERR_UNSUPPORTED).
  * Other overlaps are not allowed.  hidden, block_out and the outputs need
  * 16-byte alignment, the vectors 4 (KDA_ERR_UNSUPPORTED).
  */
