@@ -32,9 +32,9 @@
 //
 // Bound: vector instructions (splitting the state into terms every 32 tokens,
 // the convolution with its SiLU) and the clock under them; 8 x 2048 tokens over
-// 96 heads of 128 columns, bf16 pool: 534 us, of which ssm_keys 57 and ssm_scan
-// 475, vector units busy 64% of the cycles and matrix units 33%.  16384 tokens
-// over 32 heads of 64 columns: 168 us (keys 12, segments 57, join 15, joined 83).
+// 96 heads of 128 columns, bf16 pool: 540 us, of which ssm_keys 58 and ssm_scan
+// 478, vector units busy 63% of the cycles and matrix units 33%.  16384 tokens
+// over 32 heads of 64 columns: 170 us (keys 12, segments 60, join 15, joined 85).
 
 #include <hip/hip_runtime.h>
 
@@ -992,7 +992,9 @@ hipError_t run(const Plan& plan, bool state_bf16, bool v_first, hipStream_t stre
 // lengths of 1 .. 4000 x 4 384 / 197, x 8 409 / 472; dk = 64, 2000 tokens x 4
 // 197 / 149), and by the tokens: 32 heads, one request of 200 tokens 36 / 33,
 // 512 64 / 41, 1024 99 / 44.  The longest request is not known here: with
-// enough tokens in all there may be a long one.  Segments of at least
+// enough tokens in all there may be a long one, and a batch above the limit runs
+// it in one piece (64 heads, 16384 tokens and four requests of 100 353 us, and
+// five 1710; 4000 tokens 145 and 431).  Segments of at least
 // 64 / 128 / 256 tokens: 512 tokens 41 / 43 / 60, 2048 55 / 50 / 66, 4 x 500
 // 57 / 62 / 70.
 constexpr int kSplitWaves = KDA_SSM_SPLIT / 16 * 5 * kResident<kJoined> / 3;
