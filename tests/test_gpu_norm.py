@@ -219,3 +219,22 @@ def test_captured_and_on_another_stream():
         kda.norm_gate(o2, n2, z, w, activation="silu", gate_first=True, stream=stream.cuda_stream)
         stream.synchronize()
         assert torch.equal(h, h2) and torch.equal(n1, n2) and torch.equal(o1, o2)
+
+
+def test_rows_beyond_32_bits():
+    """The last rows of more than 2^31 values are those of a short call."""
+    D, last = 2304, 64
+    rows = 2 ** 31 // D + 1 + last
+    gen = torch.Generator(device=DEVICE).manual_seed(4)
+    h, y = draw(gen, last, D, bf16=True), draw(gen, last, D, bf16=True)
+    w = draw(gen, D, bf16=False)
+    want_h, want_n, want_g = (torch.empty_like(y) for _ in range(3))
+    kda.norm_residual(want_h, want_n, h, y, w)
+    kda.norm_gate(want_g, y, h, w)
+    long_h, long_y = (torch.empty(rows, D, dtype=torch.bfloat16, device=DEVICE) for _ in range(2))
+    gated = torch.empty_like(long_y)
+    long_h[-last:], long_y[-last:] = h, y
+    kda.norm_gate(gated, long_y, long_h, w)
+    kda.norm_residual(long_h, long_y, long_h, long_y, w)
+    assert torch.equal(gated[-last:], want_g)
+    assert torch.equal(long_h[-last:], want_h) and torch.equal(long_y[-last:], want_n)

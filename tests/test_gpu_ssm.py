@@ -373,6 +373,30 @@ def test_workspace_where_splitting_ends(lens):
     assert (buf[:1024] == 3.25).all() and (buf[1024 + n:] == 3.25).all()
 
 
+@pytest.mark.parametrize("entry", ["decode", "prefill"])
+@pytest.mark.parametrize("lens", [[2, 1, 3], [700, 40, 1]])
+def test_offsets_beyond_32_bits(entry, lens):
+    """Tokens behind a skipped request of 2^31 values, in slots behind as many of the pool."""
+    case = Case(26, lens, H=1, HV=64, dk=32, dv=128)
+    t = case.tensors(DEVICE)
+    rows, slots = 2 ** 31 // (case.HV * case.dv) + 1, 2 ** 31 // (case.HV * case.dk * case.dv) + 1
+    big = dict(t)
+    for n in ("out", "xbc", "dt"):
+        big[n] = torch.empty((1, rows + case.T) + t[n].shape[2:], dtype=t[n].dtype, device=DEVICE)
+        big[n][:, rows:] = t[n]
+    for n in ("state_pool", "conv_win"):
+        big[n] = torch.empty((slots + case.N,) + t[n].shape[1:], dtype=t[n].dtype, device=DEVICE)
+        big[n][slots:] = t[n]
+    skipped = torch.tensor([-1], dtype=torch.int32, device=DEVICE)
+    big["state_indices"] = torch.cat([skipped, t["state_indices"] + slots])
+    big["cu_seqlens"] = torch.cat([torch.zeros_like(skipped), t["cu_seqlens"] + rows])
+    call(case, big, entry)
+    torch.cuda.synchronize()
+    assert not big["out"][0, :rows].any()
+    case.check(dict(t, out=big["out"][:, rows:], state_pool=big["state_pool"][slots:], conv_win=big["conv_win"][slots:]),
+               entry == "prefill")
+
+
 def test_refusals():
     case = Case(19, [5], H=1, HV=2, dk=32, dv=32)
     t = case.tensors(DEVICE)
